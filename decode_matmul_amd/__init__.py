@@ -30,7 +30,9 @@ TQ_DATA_ALPHABET = 8
 EXPORTS = ("tq_pack", "tq_unpack", "tq_matmul", "tq_matmul_hot", "rb_table", "rb_encode",
            "rb_matmul", "rb_matmul_rho_block", "rb_matmul_blocks", "rb_truncate",
            "rb_matmul7", "rb_matmul_ws", "rb_prefill_workspace_bytes", "tq_matmul_ws",
-           "tq_prefill_workspace_bytes", "rb_matmul_noalloc", "tq_status_string")
+           "tq_prefill_workspace_bytes", "rb_matmul_noalloc", "mx_pack", "mx_unpack", "mx_matmul",
+           "mx_matmul_mx", "mx_matmul_experts", "moe_route", "moe_route_workspace_bytes",
+           "moe_balance", "moe_balance_workspace_bytes", "moe_balance_grad", "tq_status_string")
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(
@@ -66,12 +68,25 @@ _lib.tq_matmul_ws.argtypes = [_p, _i64, _i64, _p, _p, _p, _p, _i64, _i32, _p, _i
 _lib.rb_matmul_noalloc.argtypes = [_p, _i64, _i64, _p, _i64, _p, _i32, ctypes.c_float, _p, _i32,
                                    _p, _p, _i32, _p]
 _lib.tq_prefill_workspace_bytes.argtypes = [_i64, _i64]
+_lib.mx_pack.argtypes = [_p, _i32, _i64, _i64, _i64, _p, _p, _p, _p]
+_lib.mx_unpack.argtypes = [_p, _p, _i64, _i64, _p, _i32, _p, _p]
+_lib.mx_matmul.argtypes = [_p, _i64, _i64, _i64, _p, _p, _i64, _p, _p, _i32, _p]
+_lib.mx_matmul_mx.argtypes = [_p, _p, _i64, _i64, _p, _p, _i64, _p, _p, _i32, _p]
+_lib.mx_matmul_experts.argtypes = [_p, _i64, _i64, _i64, _p, _p, _i64, _i32, _p, _p, _p, _i32, _p,
+                                   _i32, _p]
+_lib.moe_route.argtypes = [_p, _i64, _i32, _i32, _p, _p, _p, _p, _i64, _p]
+_lib.moe_route_workspace_bytes.argtypes = [_i64, _i32, _i32]
+_lib.moe_balance.argtypes = [_p, _i32, _i64, _i32, _i64, _p, _p, _p, _p, _p, _i64, _p]
+_lib.moe_balance_workspace_bytes.argtypes = [_i64, _i32]
+_lib.moe_balance_grad.argtypes = [_p, _i32, _i64, _i32, _i64, _p, _p, _p, _p, _p]
 _lib.tq_status_string.argtypes = [_i32]
 _lib.tq_status_string.restype = ctypes.c_char_p
 for _name in EXPORTS[:-1]:
     getattr(_lib, _name).restype = _i32
 _lib.rb_prefill_workspace_bytes.restype = _i64
 _lib.tq_prefill_workspace_bytes.restype = _i64
+_lib.moe_route_workspace_bytes.restype = _i64
+_lib.moe_balance_workspace_bytes.restype = _i64
 
 
 def tq_status_string(status):
@@ -431,6 +446,215 @@ def rb_matmul7(x, codes7, N, used, tables, table_rows, alpha, y, row_scale=None,
                          int(table_rows), float(alpha), _ptr(row_scale), int(rho_rows),
                          _ptr(bias), _ptr(y), _ydtype(y), _stream(dev))
     _raise(rc, "rb_matmul7")
+
+
+def mx_shape(rows, K):
+    """(codes shape, scales shape) of the MXFP4 package of a [rows, K] matrix."""
+    nb = -(-K // 32)
+    return (rows, nb, 16), (rows, nb)
+
+
+def _rows(t, name, dtypes, rows, cols, device):
+    """Check a [rows, cols] matrix whose rows may lie apart; their distance."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
+    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+        raise ValueError(f"{name}: strides {t.stride()} are not those of rows of {cols} elements")
+    return t.stride(0) if rows > 1 else cols
+
+
+def _float_dtype(t, name):
+    if t.dtype == torch.float32:
+        return TQ_F32
+    if t.dtype == torch.bfloat16:
+        return TQ_BF16
+    raise TypeError(f"{name} dtype {t.dtype} must be float32 or bfloat16")
+
+
+def _on_gpu(device, what):
+    """The device as a context: kernels are launched with it current."""
+    if device.type != "cuda":
+        raise ValueError(f"{what}: tensors are on {device}, not on a GPU")
+    return torch.cuda.device(device)
+
+
+def _package(codes, scales, rows, K, device, prefix=""):
+    nb = -(-K // 32)
+    _need(codes, prefix + "codes", _U8, rows * nb * 16, device)
+    _need(scales, prefix + "scales", _U8, rows * nb, device)
+
+
+def mx_pack(W, codes, scales, status=None):
+    """Quantize W [rows, K] (float32 or bfloat16, rows may lie apart) to MXFP4
+    in caller-allocated codes and scales (mx_shape).  With status (int32 [1])
+    data errors are reported there; a block with a non-finite value becomes
+    NaN either way."""
+    dev = W.device
+    wdt = _float_dtype(W, "W")
+    rows, K = W.shape
+    ldw = _rows(W, "W", (W.dtype,), rows, K, dev)
+    _package(codes, scales, rows, K, dev)
+    if status is not None:
+        _need(status, "status", _I32, 1, dev)
+    with _on_gpu(dev, "mx_pack"):
+        rc = _lib.mx_pack(_ptr(W), wdt, rows, K, ldw, _ptr(codes), _ptr(scales), _ptr(status),
+                          _stream(dev))
+    _raise(rc, "mx_pack")
+    return status
+
+
+def mx_unpack(codes, scales, rows, K, W_out, status=None):
+    """Decode an MXFP4 package into W_out [rows, K] (float32 or bfloat16, both
+    exact).  With status (int32 [1]) data errors are reported there."""
+    dev = codes.device
+    _package(codes, scales, rows, K, dev)
+    odt = _float_dtype(W_out, "W_out")
+    _need(W_out, "W_out", (W_out.dtype,), rows * K, dev)
+    if status is not None:
+        _need(status, "status", _I32, 1, dev)
+    with _on_gpu(dev, "mx_unpack"):
+        rc = _lib.mx_unpack(_ptr(codes), _ptr(scales), rows, K, _ptr(W_out), odt, _ptr(status),
+                            _stream(dev))
+    _raise(rc, "mx_unpack")
+    return status
+
+
+def mx_matmul(x, codes, scales, N, y, bias=None):
+    """y = x W_hat^T (+ bias) for bf16 x [M, K] (rows may lie apart) and an
+    MXFP4 package of the [N, K] weights."""
+    dev = x.device
+    M, K = x.shape
+    ldx = _rows(x, "x", _BF16, M, K, dev)
+    _package(codes, scales, N, K, dev)
+    if bias is not None:
+        _need(bias, "bias", _F32, N, dev)
+    _need(y, "y", (y.dtype,), M * N, dev)
+    ydt = _ydtype(y)
+    with _on_gpu(dev, "mx_matmul"):
+        rc = _lib.mx_matmul(_ptr(x), M, K, ldx, _ptr(codes), _ptr(scales), N, _ptr(bias), _ptr(y),
+                            ydt, _stream(dev))
+    _raise(rc, "mx_matmul")
+
+
+def mx_matmul_mx(x_codes, x_scales, M, K, codes, scales, N, y, bias=None):
+    """mx_matmul with the [M, K] activations as an MXFP4 package too."""
+    dev = x_codes.device
+    _package(x_codes, x_scales, M, K, dev, "x_")
+    _package(codes, scales, N, K, dev)
+    if bias is not None:
+        _need(bias, "bias", _F32, N, dev)
+    _need(y, "y", (y.dtype,), M * N, dev)
+    ydt = _ydtype(y)
+    with _on_gpu(dev, "mx_matmul_mx"):
+        rc = _lib.mx_matmul_mx(_ptr(x_codes), _ptr(x_scales), M, K, _ptr(codes), _ptr(scales), N,
+                               _ptr(bias), _ptr(y), ydt, _stream(dev))
+    _raise(rc, "mx_matmul_mx")
+
+
+def moe_route_workspace_bytes(M, top_k, n_experts):
+    """Bytes of the workspace moe_route takes (0: none)."""
+    n = int(_lib.moe_route_workspace_bytes(int(M), int(top_k), int(n_experts)))
+    if n < 0:
+        raise ValueError(f"moe_route_workspace_bytes: bad sizes {M}, {top_k}, {n_experts}")
+    return n
+
+
+def _workspace(workspace, dev):
+    """Pointer and size of an optional uint8 workspace."""
+    if workspace is None:
+        return None, 0
+    _need(workspace, "workspace", _U8, workspace.numel(), dev)
+    return _ptr(workspace), workspace.numel()
+
+
+def moe_route(expert_ids, n_experts, counts, offsets, order, workspace=None):
+    """Count and list the slots of each expert: int32 expert_ids [M, top_k] ->
+    counts [n_experts], offsets [n_experts + 1], order [M * top_k] (slots by
+    expert; ids outside [0, n_experts) last)."""
+    dev = expert_ids.device
+    M, top_k = expert_ids.shape
+    _need(expert_ids, "expert_ids", _I32, M * top_k, dev)
+    _need(counts, "counts", _I32, n_experts, dev)
+    _need(offsets, "offsets", _I32, n_experts + 1, dev)
+    _need(order, "order", _I32, M * top_k, dev)
+    ws, nbytes = _workspace(workspace, dev)
+    with _on_gpu(dev, "moe_route"):
+        rc = _lib.moe_route(_ptr(expert_ids), M, top_k, n_experts, _ptr(counts), _ptr(offsets),
+                            _ptr(order), ws, nbytes, _stream(dev))
+    _raise(rc, "moe_route")
+
+
+def mx_matmul_experts(x, codes, scales, N, y, n_experts, offsets, order, top_k, bias=None):
+    """Grouped mx_matmul: y[t, j] = x[t] W_hat_e^T (+ bias[e]) for the expert e
+    of slot (t, j), with offsets and order from moe_route."""
+    dev = x.device
+    M, K = x.shape
+    ldx = _rows(x, "x", _BF16, M, K, dev)
+    _package(codes, scales, n_experts * N, K, dev)
+    if bias is not None:
+        _need(bias, "bias", _F32, n_experts * N, dev)
+    _need(offsets, "offsets", _I32, n_experts + 1, dev)
+    _need(order, "order", _I32, M * top_k, dev)
+    _need(y, "y", (y.dtype,), M * top_k * N, dev)
+    ydt = _ydtype(y)
+    with _on_gpu(dev, "mx_matmul_experts"):
+        rc = _lib.mx_matmul_experts(_ptr(x), M, K, ldx, _ptr(codes), _ptr(scales), N, n_experts,
+                                    _ptr(bias), _ptr(offsets), _ptr(order), top_k, _ptr(y), ydt,
+                                    _stream(dev))
+    _raise(rc, "mx_matmul_experts")
+
+
+def moe_balance_workspace_bytes(M, n_experts):
+    """Bytes of the workspace moe_balance takes."""
+    n = int(_lib.moe_balance_workspace_bytes(int(M), int(n_experts)))
+    if n < 0:
+        raise ValueError(f"moe_balance_workspace_bytes: bad sizes {M}, {n_experts}")
+    return n
+
+
+def moe_balance(logits, counts, loss, weights, token_mask=None, workspace=None):
+    """Load-balance loss of logits [M, n_experts] (float32 or bfloat16, rows may
+    lie apart) and the counts of moe_route -> loss float32 [1] and weights
+    float32 [n_experts] (for moe_balance_grad).  token_mask uint8 or bool [M]: 0
+    leaves a token out."""
+    dev = logits.device
+    ldt = _float_dtype(logits, "logits")
+    M, E = logits.shape
+    ldl = _rows(logits, "logits", (logits.dtype,), M, E, dev)
+    _need(counts, "counts", _I32, E, dev)
+    _need(loss, "loss", _F32, 1, dev)
+    _need(weights, "weights", _F32, E, dev)
+    if token_mask is not None:
+        _need(token_mask, "token_mask", (torch.uint8, torch.bool), M, dev)
+    ws, nbytes = _workspace(workspace, dev)
+    with _on_gpu(dev, "moe_balance"):
+        rc = _lib.moe_balance(_ptr(logits), ldt, M, E, ldl, _ptr(token_mask), _ptr(counts), _ptr(loss),
+                              _ptr(weights), ws, nbytes, _stream(dev))
+    _raise(rc, "moe_balance")
+
+
+def moe_balance_grad(logits, weights, dloss, dlogits, token_mask=None):
+    """Gradient of moe_balance's loss times dloss (float32 [1]) with respect to
+    the logits, into dlogits (the logits' shape and dtype)."""
+    dev = logits.device
+    ldt = _float_dtype(logits, "logits")
+    M, E = logits.shape
+    ldl = _rows(logits, "logits", (logits.dtype,), M, E, dev)
+    _need(weights, "weights", _F32, E, dev)
+    _need(dloss, "dloss", _F32, 1, dev)
+    _need(dlogits, "dlogits", (logits.dtype,), M * E, dev)
+    if token_mask is not None:
+        _need(token_mask, "token_mask", (torch.uint8, torch.bool), M, dev)
+    with _on_gpu(dev, "moe_balance_grad"):
+        rc = _lib.moe_balance_grad(_ptr(logits), ldt, M, E, ldl, _ptr(token_mask), _ptr(weights),
+                                   _ptr(dloss), _ptr(dlogits), _stream(dev))
+    _raise(rc, "moe_balance_grad")
 
 
 def raw():

@@ -14,6 +14,16 @@ bool group_ok(int G) { return G == 64 || G == 128; }
 
 int hip_status(hipError_t e) { return e == hipSuccess ? TQ_OK : TQ_ERR_HIP; }
 
+// Launchers that refuse too large a grid themselves say so with hipErrorInvalidConfiguration.
+int grid_status(hipError_t e) { return e == hipErrorInvalidConfiguration ? TQ_ERR_SHAPE : hip_status(e); }
+
+bool is_dtype(int32_t d) { return d == TQ_F32 || d == TQ_BF16; }
+
+uintptr_t bytes_of(int32_t d) { return d == TQ_F32 ? 4 : 2; }
+
+// Rows of `cols` elements, `ld` apart (one row has no distance).
+bool rows_ok(int64_t rows, int64_t cols, int64_t ld) { return rows <= 1 || (ld >= cols && ld < kMaxDim); }
+
 }  // namespace
 
 extern "C" {
@@ -332,6 +342,132 @@ int rb_matmul7(const uint16_t* x, int64_t M, int64_t K, const uint8_t* codes7, i
     if (!used) return TQ_ERR_NULL;
     return rb_matmul_common(x, M, K, codes7, used, N, tables, table_rows, alpha, row_scale,
                             rho_rows, bias, y, y_dtype, stream);
+}
+
+int mx_pack(const void* W, int32_t w_dtype, int64_t rows, int64_t K, int64_t ldw, uint8_t* codes,
+            uint8_t* scales, int32_t* d_status, void* stream) {
+    if (rows < 0 || K < 0 || rows >= kMaxDim || K >= kMaxDim || !rows_ok(rows, K, ldw)) return TQ_ERR_SHAPE;
+    if (!is_dtype(w_dtype)) return TQ_ERR_DTYPE;
+    if (rows > 0 && K > 0 && (!W || !codes || !scales)) return TQ_ERR_NULL;
+    if (!aligned(W, bytes_of(w_dtype)) || !aligned(codes, 16) || !aligned(d_status, 4)) return TQ_ERR_ALIGN;
+    if (!dmm::grid_fits(rows * ((K + 31) / 32) / 64 + 1, 256)) return TQ_ERR_SHAPE;
+    hipStream_t s = (hipStream_t)stream;
+    if (d_status && dmm::launch_status_clear(d_status, s) != hipSuccess) return TQ_ERR_HIP;
+    return grid_status(dmm::launch_mx_pack(W, w_dtype, rows, K, ldw, codes, scales, d_status, s));
+}
+
+int mx_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, void* W_out,
+              int32_t out_dtype, int32_t* d_status, void* stream) {
+    if (rows < 0 || K < 0 || rows >= kMaxDim || K >= kMaxDim) return TQ_ERR_SHAPE;
+    if (!is_dtype(out_dtype)) return TQ_ERR_DTYPE;
+    if (rows > 0 && K > 0 && (!W_out || !codes || !scales)) return TQ_ERR_NULL;
+    if (!aligned(W_out, bytes_of(out_dtype)) || !aligned(codes, 16) || !aligned(d_status, 4))
+        return TQ_ERR_ALIGN;
+    if (!dmm::grid_fits(rows * ((K + 31) / 32) / 64 + 1, 256)) return TQ_ERR_SHAPE;
+    hipStream_t s = (hipStream_t)stream;
+    if (d_status && dmm::launch_status_clear(d_status, s) != hipSuccess) return TQ_ERR_HIP;
+    return grid_status(dmm::launch_mx_unpack(codes, scales, rows, K, W_out, out_dtype, d_status, s));
+}
+
+// Every MXFP4 product; a holds the call's arguments, x_any its activations.
+static int mx_matmul_common(dmm::MxMatmulArgs& a, const void* x_any, bool x_rows_ok, void* stream) {
+    if (a.M < 0 || a.K < 0 || a.N < 0 || a.M >= kMaxDim || a.K >= kMaxDim || a.N >= kMaxDim || !x_rows_ok)
+        return TQ_ERR_SHAPE;
+    if (!is_dtype(a.y_dtype)) return TQ_ERR_DTYPE;
+    if (a.M == 0 || a.N == 0) return TQ_OK;
+    if (!a.y || (a.K > 0 && (!x_any || !a.codes || !a.scales))) return TQ_ERR_NULL;
+    if (!aligned(a.x, 2) || !aligned(a.x_codes, 16) || !aligned(a.codes, 16) || !aligned(a.bias, 4) ||
+        !aligned(a.y, bytes_of(a.y_dtype)))
+        return TQ_ERR_ALIGN;
+    return grid_status(dmm::launch_mx_matmul(a, (hipStream_t)stream));
+}
+
+int mx_matmul(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint8_t* codes,
+              const uint8_t* scales, int64_t N, const float* bias, void* y, int32_t y_dtype,
+              void* stream) {
+    dmm::MxMatmulArgs a = {x,    ldx, nullptr, nullptr, M, K, N,      codes, scales,
+                           bias, 0,   nullptr, nullptr, 1, y, y_dtype};
+    return mx_matmul_common(a, x, rows_ok(M, K, ldx), stream);
+}
+
+int mx_matmul_mx(const uint8_t* x_codes, const uint8_t* x_scales, int64_t M, int64_t K,
+                 const uint8_t* codes, const uint8_t* scales, int64_t N, const float* bias, void* y,
+                 int32_t y_dtype, void* stream) {
+    dmm::MxMatmulArgs a = {nullptr, 0, x_codes, x_scales, M, K, N,      codes, scales,
+                           bias,    0, nullptr, nullptr,  1, y, y_dtype};
+    return mx_matmul_common(a, x_codes && x_scales ? x_codes : nullptr, true, stream);
+}
+
+int mx_matmul_experts(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint8_t* codes,
+                      const uint8_t* scales, int64_t N, int32_t n_experts, const float* bias,
+                      const int32_t* offsets, const int32_t* order, int32_t top_k, void* y,
+                      int32_t y_dtype, void* stream) {
+    if (n_experts < 1 || top_k < 1) return TQ_ERR_SHAPE;
+    if (M >= 0 && M < kMaxDim && M * top_k >= kMaxDim) return TQ_ERR_SHAPE;
+    if (M > 0 && N > 0 && (!offsets || !order)) return TQ_ERR_NULL;
+    if (!aligned(offsets, 4) || !aligned(order, 4)) return TQ_ERR_ALIGN;
+    dmm::MxMatmulArgs a = {x,    ldx,       nullptr, nullptr, M,     K, N,      codes, scales,
+                           bias, n_experts, offsets, order,   top_k, y, y_dtype};
+    return mx_matmul_common(a, x, rows_ok(M, K, ldx), stream);
+}
+
+int64_t moe_route_workspace_bytes(int64_t M, int32_t top_k, int32_t n_experts) {
+    if (M < 0 || M >= kMaxDim || top_k < 1 || M * top_k >= kMaxDim || n_experts < 1 ||
+        n_experts > dmm::kMoeMaxExperts)
+        return -1;
+    return dmm::moe_route_ws_bytes(M * top_k, n_experts);
+}
+
+int moe_route(const int32_t* expert_ids, int64_t M, int32_t top_k, int32_t n_experts,
+              int32_t* counts, int32_t* offsets, int32_t* order, void* workspace,
+              int64_t workspace_bytes, void* stream) {
+    if (n_experts > dmm::kMoeMaxExperts) return TQ_ERR_UNSUPPORTED;
+    const int64_t need = moe_route_workspace_bytes(M, top_k, n_experts);
+    if (need < 0) return TQ_ERR_SHAPE;
+    if (!counts || !offsets || (M > 0 && (!expert_ids || !order))) return TQ_ERR_NULL;
+    if (need > 0 && !workspace) return TQ_ERR_NULL;
+    if (!aligned(expert_ids, 4) || !aligned(counts, 4) || !aligned(offsets, 4) || !aligned(order, 4) ||
+        !aligned(workspace, 4))
+        return TQ_ERR_ALIGN;
+    if (need > 0 && workspace_bytes < need) return TQ_ERR_SHAPE;
+    return hip_status(dmm::launch_moe_route(expert_ids, M * top_k, n_experts, counts, offsets, order,
+                                            workspace, (hipStream_t)stream));
+}
+
+int64_t moe_balance_workspace_bytes(int64_t M, int32_t n_experts) {
+    if (M < 0 || M >= kMaxDim || n_experts < 1 || n_experts > dmm::kMoeMaxExperts) return -1;
+    return dmm::moe_balance_ws_bytes(M, n_experts);
+}
+
+int moe_balance(const void* logits, int32_t l_dtype, int64_t M, int32_t n_experts, int64_t ldl,
+                const uint8_t* token_mask, const int32_t* counts, float* loss, float* weights,
+                void* workspace, int64_t workspace_bytes, void* stream) {
+    if (n_experts > dmm::kMoeMaxExperts) return TQ_ERR_UNSUPPORTED;
+    const int64_t need = moe_balance_workspace_bytes(M, n_experts);
+    if (need < 0 || !rows_ok(M, n_experts, ldl)) return TQ_ERR_SHAPE;
+    if (!is_dtype(l_dtype)) return TQ_ERR_DTYPE;
+    if (!counts || !loss || !weights || (M > 0 && (!logits || !workspace))) return TQ_ERR_NULL;
+    if (!aligned(logits, bytes_of(l_dtype)) || !aligned(counts, 4) || !aligned(loss, 4) ||
+        !aligned(weights, 4) || !aligned(workspace, 8))
+        return TQ_ERR_ALIGN;
+    if (workspace_bytes < need) return TQ_ERR_SHAPE;
+    return hip_status(dmm::launch_moe_balance(logits, l_dtype, M, n_experts, ldl, token_mask, counts, loss,
+                                              weights, workspace, (hipStream_t)stream));
+}
+
+int moe_balance_grad(const void* logits, int32_t l_dtype, int64_t M, int32_t n_experts, int64_t ldl,
+                     const uint8_t* token_mask, const float* weights, const float* dloss,
+                     void* dlogits, void* stream) {
+    if (n_experts > dmm::kMoeMaxExperts) return TQ_ERR_UNSUPPORTED;
+    if (M < 0 || M >= kMaxDim || n_experts < 1 || !rows_ok(M, n_experts, ldl)) return TQ_ERR_SHAPE;
+    if (!is_dtype(l_dtype)) return TQ_ERR_DTYPE;
+    if (M == 0) return TQ_OK;
+    if (!logits || !weights || !dloss || !dlogits) return TQ_ERR_NULL;
+    if (!aligned(logits, bytes_of(l_dtype)) || !aligned(weights, 4) || !aligned(dloss, 4) ||
+        !aligned(dlogits, bytes_of(l_dtype)))
+        return TQ_ERR_ALIGN;
+    return grid_status(dmm::launch_moe_balance_grad(logits, l_dtype, M, n_experts, ldl, token_mask, weights,
+                                                    dloss, dlogits, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -269,4 +269,45 @@ hipError_t launch_rb_encode(const float* W, int64_t N, int64_t K, const float* l
                             int64_t rho_rows, uint8_t* codes, float* alpha, uint16_t* row_scale,
                             int32_t* status, hipStream_t s);
 
+// ------------------------------------------------------------ MXFP4, experts' routing
+
+// Launchers below return hipErrorInvalidConfiguration, before any launch, for
+// a call that needs more than 2^32 - 1 threads.
+inline bool grid_fits(int64_t blocks, int threads) { return blocks <= (int64_t)0xffffffffll / threads; }
+
+hipError_t launch_mx_pack(const void* W, int w_dtype, int64_t rows, int64_t K, int64_t ldw, uint8_t* codes,
+                          uint8_t* scales, int32_t* status, hipStream_t s);
+hipError_t launch_mx_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, void* out,
+                            int out_dtype, int32_t* status, hipStream_t s);
+
+struct MxMatmulArgs {
+    const uint16_t* x;        // bf16 activations, rows ldx apart; NULL for MXFP4 ones
+    int64_t ldx;
+    const uint8_t* x_codes;   // MXFP4 activations
+    const uint8_t* x_scales;
+    int64_t M, K, N;
+    const uint8_t* codes;     // [N, K], or n_experts of them back to back
+    const uint8_t* scales;
+    const float* bias;        // NULL, [N] or [n_experts][N]
+    int n_experts;            // 0: dense
+    const int32_t* offsets;   // grouped: [n_experts + 1] into order
+    const int32_t* order;     // grouped: [M * top_k] slots
+    int top_k;                // 1 when dense
+    void* y;                  // [M, N] or [M, top_k, N]
+    int y_dtype;
+};
+hipError_t launch_mx_matmul(const MxMatmulArgs& a, hipStream_t s);
+
+// Most experts of moe_route and moe_balance.
+constexpr int kMoeMaxExperts = 512;
+int64_t moe_route_ws_bytes(int64_t slots, int E);
+hipError_t launch_moe_route(const int32_t* ids, int64_t slots, int E, int32_t* counts, int32_t* offsets,
+                            int32_t* order, void* workspace, hipStream_t s);
+int64_t moe_balance_ws_bytes(int64_t M, int E);
+hipError_t launch_moe_balance(const void* logits, int l_dtype, int64_t M, int E, int64_t ldl, const uint8_t* mask,
+                              const int32_t* counts, float* loss, float* weights, void* workspace, hipStream_t s);
+hipError_t launch_moe_balance_grad(const void* logits, int l_dtype, int64_t M, int E, int64_t ldl,
+                                   const uint8_t* mask, const float* weights, const float* dloss, void* dlogits,
+                                   hipStream_t s);
+
 }  // namespace dmm

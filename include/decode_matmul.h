@@ -2,7 +2,7 @@
  * decode_matmul.h -- C ABI of the packed ternary-code matmul library for
  * AMD MI355X (gfx950).
  *
- * Two weight formats, both decoded inside the matmul kernels (no bf16 copy of
+ * Three weight formats, all decoded inside the matmul kernels (no bf16 copy of
  * the weight matrix is ever written):
  *
  *  1. Mean-abs ternary ("Does your weight format deserve a kernel?",
@@ -18,6 +18,13 @@
  *     Models", sections 3.2, 3.3, 4.1, 4.2): one byte per weight indexes a
  *     243-entry table of 5-step ternary ladder values, times one fp32 scale
  *     per layer and an optional fp16 scale per output row.
+ *
+ *  3. MXFP4 (the microscaled 4-bit format of the OCP Microscaling Formats
+ *     specification): 32 consecutive weights of a row share a power of two, and
+ *     each is one of 16 e2m1 values.  Its entry points are the mx_* ones.
+ *
+ * The moe_* entry points are the router's side of the grouped experts: counts
+ * and lists of the slots routed to each expert, and the balance loss.
  *
  * Conventions for every entry point:
  *  - Pointers named d_* or documented "device" are device pointers owned by
@@ -443,6 +450,185 @@ int rb_matmul7(const uint16_t* x, int64_t M, int64_t K, const uint8_t* codes7, i
                const uint8_t* used, const float* tables, int32_t table_rows, float alpha,
                const uint16_t* row_scale, int32_t rho_rows, const float* bias, void* y,
                int32_t y_dtype, void* stream);
+
+/*
+ * MXFP4 packages.  A block of 32 consecutive values of a row shares one byte
+ * s (E8M0): its scale is 2^(s - 127), and s = 255 makes the whole block NaN.
+ * An element is a 4-bit code c: bit 3 is the sign and bits 0..2 index the
+ * magnitudes {0, 0.5, 1, 1.5, 2, 3, 4, 6}.  Two codes share a byte, the first
+ * in the low nibble.  A [rows, K] matrix is planar, with nb = ceil(K / 32):
+ *     codes  uint8 [rows][nb][16]     16-byte aligned
+ *     scales uint8 [rows][nb]
+ * A ragged last block (K % 32 != 0) still takes 16 bytes; the codes past K
+ * are 0.  A weight takes 4.25 bits.
+ */
+
+/*
+ * mx_pack -- quantize W to MXFP4.
+ *
+ *  W         device [rows, K] of w_dtype (TQ_F32 or TQ_BF16), row r at element
+ *            r * ldw; aligned to its element.
+ *  ldw       elements between rows, >= K (rows > 1 need it; TQ_ERR_SHAPE).
+ *  codes, scales  device outputs (layout above).
+ *  d_status  device int32, or NULL for no report; set to 0, then
+ *            TQ_DATA_RANGE if a value is not finite.
+ *
+ * Per block, with a = max |W_j|: s = clamp(floor(log2 a) - 2 + 127, 0, 254)
+ * (s = 0 for a = 0), and each code is the e2m1 value nearest to W_j 2^(127 - s),
+ * ties to the even code, magnitudes above 6 taken to 6, the sign kept.  The
+ * scaling is exact, so there is one rounding.  A block with a value that is
+ * not finite gets s = 255 and codes 0: it decodes to NaN, and so do the
+ * products it takes part in.
+ */
+int mx_pack(const void* W, int32_t w_dtype, int64_t rows, int64_t K, int64_t ldw, uint8_t* codes,
+            uint8_t* scales, int32_t* d_status, void* stream);
+
+/*
+ * mx_unpack -- decode an MXFP4 package to W_out [rows, K] of out_dtype, row r
+ * at element r * K.  Both TQ_F32 and TQ_BF16 hold every value exactly (4 or 6
+ * times 2^127, which neither holds, becomes an infinity).
+ *
+ *  d_status  device int32, or NULL for no report; set to 0, then
+ *            TQ_DATA_RANGE if a block is NaN (s = 255), TQ_DATA_PADDING if a
+ *            code past K is not 0.
+ */
+int mx_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, void* W_out,
+              int32_t out_dtype, int32_t* d_status, void* stream);
+
+/*
+ * mx_matmul -- bf16 activations times an MXFP4 weight matrix:
+ *
+ *     y[m, n] = sum_k x[m, k] w_hat[n, k]  (+ bias[n])
+ *
+ *  x       device bf16 [M, K], row m at element m * ldx (ldx >= K), 2-byte
+ *          aligned (fastest with 16-byte aligned rows and K % 32 == 0).
+ *  codes, scales  device MXFP4 package of the [N, K] weights.
+ *  bias    device fp32 [N] or NULL.
+ *  y       device [M, N] of y_dtype (fp32, or bf16 nearest-even of the fp32
+ *          result).
+ *
+ * Every weight is exact in bf16 and every product in fp32; sums are held in
+ * fp32, in an order fixed by the shape (two calls give the same bits).  A NaN
+ * block makes its output column NaN.  What x holds past K, and codes past K,
+ * take no part.  M = 0 or N = 0 is a no-op; with K = 0, x and the package may
+ * be NULL and y = bias (or 0).  Sizes below 2^31.
+ */
+int mx_matmul(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint8_t* codes,
+              const uint8_t* scales, int64_t N, const float* bias, void* y, int32_t y_dtype,
+              void* stream);
+
+/*
+ * mx_matmul_mx -- mx_matmul with the activations in MXFP4 too (mx_pack of x):
+ * both operands go undecoded into the scaled matrix instructions, at four
+ * times the bf16 rate.
+ *
+ *  x_codes, x_scales  device MXFP4 package of the [M, K] activations.
+ *
+ * Products are exact and sums are held in fp32.  In a ragged last block the
+ * codes past K of at least one operand have to be 0, as mx_pack writes them.
+ * Every other argument and error is that of mx_matmul.
+ */
+int mx_matmul_mx(const uint8_t* x_codes, const uint8_t* x_scales, int64_t M, int64_t K,
+                 const uint8_t* codes, const uint8_t* scales, int64_t N, const float* bias, void* y,
+                 int32_t y_dtype, void* stream);
+
+/*
+ * moe_route -- the slots routed to each expert, counted and listed.
+ *
+ * Slot t * top_k + j holds expert_ids[t, j].  An id outside [0, n_experts)
+ * (-1 for the tokens of a padded batch) belongs to no expert.
+ *
+ *  expert_ids  device int32 [M, top_k].
+ *  n_experts   1 .. 512 (TQ_ERR_UNSUPPORTED above).
+ *  counts      device int32 [n_experts]: slots of each expert (e.g. to choose
+ *              the hot prefix of tq_matmul_hot, or for moe_balance).
+ *  offsets     device int32 [n_experts + 1]: sum of the counts before e; the
+ *              last is the number of routed slots.
+ *  order       device int32 [M * top_k]: the slots sorted by expert, equal
+ *              ones by slot, those of no expert last.
+ *  workspace   device memory of moe_route_workspace_bytes(M, top_k,
+ *              n_experts) bytes, 4-byte aligned; NULL where that is 0 (few
+ *              slots).  Overwritten; calls that share it must not overlap.
+ *
+ * M * top_k < 2^31.  Whole numbers only: the result does not depend on timing.
+ */
+int moe_route(const int32_t* expert_ids, int64_t M, int32_t top_k, int32_t n_experts,
+              int32_t* counts, int32_t* offsets, int32_t* order, void* workspace,
+              int64_t workspace_bytes, void* stream);
+
+/* Bytes of moe_route's workspace; -1 for sizes moe_route refuses. */
+int64_t moe_route_workspace_bytes(int64_t M, int32_t top_k, int32_t n_experts);
+
+/*
+ * mx_matmul_experts -- grouped mx_matmul over the lists of moe_route:
+ *
+ *     y[t, j, n] = sum_k x[t, k] w_hat_e[n, k]  (+ bias[e, n]),  e = expert_ids[t, j]
+ *
+ *  x       as in mx_matmul, M tokens.
+ *  codes, scales  n_experts packages of [N, K] back to back.
+ *  bias    device fp32 [n_experts][N] or NULL.
+ *  offsets, order  from moe_route with the same M, top_k and n_experts.
+ *  y       device [M, top_k, N] of y_dtype; the rows of slots of no expert
+ *          are NaN, as in tq_matmul.
+ *
+ * Where every slot has its own activations (an expert's second product), x is
+ * [M * top_k, K]: pass M * top_k for M and 1 for top_k with the same lists.
+ * Entries of the lists outside their range are skipped (nothing is read or
+ * written out of bounds; rows that are then listed nowhere stay as they
+ * were).  The accuracy is that of mx_matmul.
+ */
+int mx_matmul_experts(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint8_t* codes,
+                      const uint8_t* scales, int64_t N, int32_t n_experts, const float* bias,
+                      const int32_t* offsets, const int32_t* order, int32_t top_k, void* y,
+                      int32_t y_dtype, void* stream);
+
+/*
+ * moe_balance -- the load-balance loss of a router.  With p_t = softmax of
+ * token t's logits, T the number of tokens that take part, c_e the counts of
+ * moe_route and n their sum:
+ *
+ *     w_e = n_experts / T * c_e / n        loss = sum_t sum_e w_e p_te
+ *
+ * that is n_experts * sum_e f_e P_e with f_e the share of the slots that
+ * expert e got and P_e its mean probability: 1 for an even router.  w and
+ * the loss are 0 when T = 0 or n = 0.
+ *
+ *  logits      device [M, n_experts] of l_dtype (TQ_F32 or TQ_BF16), row t at
+ *              element t * ldl (ldl >= n_experts), aligned to its element.
+ *              -inf gives an expert probability 0; a row of -inf only adds 0.
+ *  n_experts   1 .. 512 (TQ_ERR_UNSUPPORTED above).
+ *  token_mask  device uint8 [M] or NULL: tokens whose byte is 0 take no part,
+ *              whatever their logits hold.
+ *  counts      device int32 [n_experts], none negative.
+ *  loss        device fp32 [1].
+ *  weights     device fp32 [n_experts]: w, which moe_balance_grad takes.
+ *  workspace   device memory of moe_balance_workspace_bytes(M, n_experts)
+ *              bytes, 8-byte aligned.  Overwritten; calls that share it must
+ *              not overlap.
+ *
+ * Softmax statistics are fp32, the sum over tokens is float64 in a fixed order.
+ */
+int moe_balance(const void* logits, int32_t l_dtype, int64_t M, int32_t n_experts, int64_t ldl,
+                const uint8_t* token_mask, const int32_t* counts, float* loss, float* weights,
+                void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of moe_balance's workspace; -1 for sizes moe_balance refuses. */
+int64_t moe_balance_workspace_bytes(int64_t M, int32_t n_experts);
+
+/*
+ * moe_balance_grad -- the gradient of moe_balance's loss with respect to the
+ * logits (the counts are constants), times *dloss:
+ *
+ *     dlogits[t, e] = *dloss * p_te * (w_e - sum_j w_j p_tj)
+ *
+ *  weights  device fp32 [n_experts] from moe_balance.
+ *  dloss    device fp32 [1].
+ *  dlogits  device [M, n_experts] of l_dtype, row t at element t * n_experts;
+ *           rows of masked tokens, and of -inf only, are 0.
+ */
+int moe_balance_grad(const void* logits, int32_t l_dtype, int64_t M, int32_t n_experts, int64_t ldl,
+                     const uint8_t* token_mask, const float* weights, const float* dloss,
+                     void* dlogits, void* stream);
 
 /* Human-readable name of a tq_status value. */
 const char* tq_status_string(int status);

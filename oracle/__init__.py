@@ -19,12 +19,14 @@ pages it follows:
   (section 8.1) and per-block code books (section 8.3).
 * "FUCINA - a general ternary forge for Mixture-of-Experts models": the
   two-plane sum W ~ d1*T1 + d2*T2 ("The method") and the expert matmul.
+* The OCP Microscaling Formats specification: MXFP4 blocks.  The experts'
+  routing lists and the router's balance loss are in the same module.
 
 Floating point is fp64 unless the pages fix a precision (fp16 group scales,
 bf16 activations and reconstructions, fp32 code-book entries).
 
-Parity status: every function is pinned by ``tests/test_oracle_pins.py``
-against worked examples, closed forms, exact rational arithmetic or brute
+Parity status: every function is pinned by ``tests/test_oracle_pins.py`` or
+``tests/test_mx_cpu.py`` against worked examples, closed forms, exact rational arithmetic or brute
 force.  No function is "parity unpinned".
 """
 
@@ -56,6 +58,14 @@ from .routeb import (
     unpack7,
     rb_weights7,
 )
+from .mx import (
+    E2M1,
+    mx_pack,
+    mx_unpack,
+    moe_route,
+    moe_balance,
+    moe_balance_grad,
+)
 from .matmul import (
     REL_BOUND,
     matmul_ref,
@@ -71,6 +81,7 @@ __all__ = [
     "unpack", "quantize_pack", "two_plane",
     "code_words", "rb_block_scales", "rb_encode", "rb_table", "rb_weights",
     "rb_truncate", "pack7", "unpack7", "rb_weights7",
+    "E2M1", "mx_pack", "mx_unpack", "moe_route", "moe_balance", "moe_balance_grad",
     "REL_BOUND", "matmul_ref", "ternary_weights", "grouped_ref", "hot_prefix_weights",
     "check_bound",
 ]
