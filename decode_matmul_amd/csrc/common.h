@@ -297,6 +297,9 @@ struct MxMatmulArgs {
     int y_dtype;
 };
 hipError_t launch_mx_matmul(const MxMatmulArgs& a, hipStream_t s);
+// Tiled form for many tokens; mx_gemm_takes: whether it can take the call.
+bool mx_gemm_takes(const MxMatmulArgs& a);
+hipError_t launch_mx_gemm(const MxMatmulArgs& a, hipStream_t s);
 
 // Most experts of moe_route and moe_balance.
 constexpr int kMoeMaxExperts = 512;

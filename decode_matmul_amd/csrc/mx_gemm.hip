@@ -1,0 +1,554 @@
+// MXFP4 products, tiled form for many tokens: y[m, n] = sum_k x[m, k] w_hat[n, k] (+ bias[n]).
+//
+// Mathematics.  As in mx_gemv.hip, a lane's 16 code bytes are the operand of
+// the 16x16x128 scaled matrix instruction (MXFP4 activations), and four
+// scaled conversions turn eight codes into eight exact bf16 values for the
+// 16x16x32 bf16 instruction (bf16 activations).  Any order of k may be taken
+// that is the same for both operands: with bf16 activations lane group g takes
+// octets 2 g and 2 g + 1 of each 64-wide slab, so its codes are 8 consecutive
+// bytes and one scale.
+//
+// Mapping.  A workgroup of 4 waves (2 x 2) owns BM tokens x 256 rows of W; a
+// wave owns BM / 2 x 128 as 16 x 16 tiles, up to 256 accumulators a lane, one
+// wave a SIMD: its own order of instructions has to hide every latency.  W is
+// the first operand, so a lane ends with four consecutive n of one token.  K is
+// cut into slabs of two steps of the matrix instruction.  Both tiles' rows are
+// 128 bytes (64 bf16 or 256 codes; with bf16 activations W's codes are 32 bytes
+// a slab) and go from global memory straight to LDS, two slabs ahead; fragments
+// go to registers one step ahead.  Chunk c (16 bytes) of row r sits at slot c ^
+// swizzle(r), which spreads the 16 rows of a fragment read over all banks.
+// Slabs take turns in distinct LDS arrays, so the compiler can tell a load in
+// flight to one from the reads of the other.
+#include <type_traits>
+
+#include "mx.h"
+
+namespace dmm {
+
+namespace {
+
+constexpr int kWaves = 8, kThreads = 64 * kWaves;
+constexpr int BN = 256;
+constexpr int kRow = 128;                       // bytes of an LDS tile row (activations; codes with MXFP4 ones)
+// Tiled form: at least 8 blocks (a lane fetches 8 scale bytes at once), and rows
+// whose 256 fit 32-bit offsets.
+constexpr int64_t kMinTiledK = 256, kMaxTiledBytes = (int64_t)1 << 24;
+constexpr int kWRow = 32;                       // bytes of codes a row with bf16 activations
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint64_t u64u __attribute__((aligned(1)));
+
+__device__ __forceinline__ int swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+
+// A uniform pointer the compiler keeps in scalar registers as it is, so that a
+// lane's address stays base + 32-bit offset (folded into per-lane pointers,
+// the slabs' addresses take more registers than there are).
+typedef const __attribute__((address_space(1))) uint8_t* GlobalBytes;
+__device__ __forceinline__ GlobalBytes scalar_base(const uint8_t* p) {
+    GlobalBytes q = (GlobalBytes)p;
+    asm("" : "+s"(q));
+    return q;
+}
+
+// A lane's offset from a scalar base, likewise kept as it is (widened ahead of
+// the loop it would take two registers).
+__device__ __forceinline__ uint32_t lane_offset(uint32_t o) {
+    asm("" : "+v"(o));
+    return o;
+}
+__device__ __forceinline__ int64_t lane_offset(int64_t o) { return o; }
+
+// 16 bytes a lane from global memory to LDS: lane l's land at lds + 16 l.
+__device__ __forceinline__ void load_lds16(GlobalBytes g, void* lds) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)g,
+                                     (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+}
+
+// No load and no LDS access of this wave outstanding (expcnt aside), then the
+// workgroup's barrier.
+__device__ __forceinline__ void wait_and_meet() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x70);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// Scale bytes b .. b + 7 of a row of nb (those past the row are 127).
+__device__ __forceinline__ uint64_t scales8(const uint8_t* row, int64_t b, int64_t nb) {
+    uint64_t v = 0x7f7f7f7f7f7f7f7full;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (b + i < nb) v ^= (uint64_t)(row[b + i] ^ 0x7fu) << (8 * i);
+    return v;
+}
+
+// Eight activations at column k of a row (past K they are 0).
+__device__ __forceinline__ u32x4 load_x8(const uint16_t* row, int64_t k, int64_t K) {
+    if (k + 8 <= K) return *(const u32x4h*)(row + k);
+    u32x4 v = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (k + i < K) v[i >> 1] |= (uint32_t)row[k + i] << (16 * (i & 1));
+    return v;
+}
+
+// The workgroup's tile: its tokens are positions [m0, m_end) of the batch or
+// of the order list, its rows of W start at n0.
+struct Place {
+    int64_t m0, m_end, n0, expert;
+};
+
+// Tile b of the experts' tiles: experts in turn, an expert's tiles of BM
+// positions in turn, the tiles along N innermost; each XCD gets a contiguous
+// share of the tiles that there are.  False when there are fewer.
+template <int BM>
+__device__ bool place_grouped(const MxMatmulArgs& a, Place& p) {
+    __shared__ int found[3];
+    __shared__ int sums[kThreads / 64];
+    const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int slots = (int)(a.M * a.top_k);
+    const int ntiles = (int)((a.N + BN - 1) / BN);
+    // bounds of the list of expert e, kept in range whatever the offsets hold
+    auto bound = [&](int e) {
+        const int o = a.offsets[e];
+        return o < 0 ? 0 : (o > slots ? slots : o);
+    };
+    int total = 0;
+    for (int e0 = 0; e0 < a.n_experts; e0 += kThreads) {
+        const int e = e0 + tid;
+        int t = 0;
+        if (e < a.n_experts) {
+            const int c = bound(e + 1) - bound(e);
+            t = c > 0 ? (c + BM - 1) / BM : 0;
+        }
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1) t += __shfl_xor(t, d);
+        if (lane == 0) sums[wave] = t;
+        __syncthreads();
+        for (int w = 0; w < kThreads / 64; ++w) total += sums[w];
+        __syncthreads();
+    }
+    total = readfirstlane(total);
+    const int64_t all = (int64_t)total * ntiles;
+    const int64_t b = blockIdx.x;
+    // XCD b % 8 takes tiles all * (b % 8) / 8 .. all * (b % 8 + 1) / 8 - 1
+    const int64_t x = b % 8, lo = all * x / 8, hi = all * (x + 1) / 8;
+    const int64_t t = lo + b / 8;
+    if (t >= hi) return false;
+    const int want = readfirstlane((int)(t / ntiles));
+    p.n0 = (t - (int64_t)want * ntiles) * BN;
+    int before = 0;
+    for (int e0 = 0; e0 < a.n_experts; e0 += kThreads) {
+        const int e = e0 + tid;
+        int n = 0, first = 0, last = 0;
+        if (e < a.n_experts) {
+            first = bound(e);
+            last = bound(e + 1);
+            n = last > first ? (last - first + BM - 1) / BM : 0;
+        }
+        int inc = n;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(inc, d);
+            if (lane >= d) inc += o;
+        }
+        if (lane == 63) sums[wave] = inc;
+        __syncthreads();
+        int base = before;
+        for (int w = 0; w < kThreads / 64; ++w) {
+            if (w < wave) base += sums[w];
+            before += sums[w];
+        }
+        const int mine = base + inc - n;
+        if (want >= mine && want < mine + n) {
+            found[0] = first + (want - mine) * BM;
+            found[1] = last;
+            found[2] = e;
+        }
+        __syncthreads();
+    }
+    p.m0 = readfirstlane(found[0]);
+    const int64_t last = readfirstlane(found[1]);
+    p.m_end = last < p.m0 + BM ? last : p.m0 + BM;
+    p.expert = readfirstlane(found[2]);
+    return true;
+}
+
+// MXX: activations in MXFP4.  DIRECT: whole slabs of bf16 activations go
+// straight to LDS (rows 16-byte aligned); otherwise through registers.
+template <bool MXX, bool DIRECT, int BM, bool GROUPED>
+__global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(MxMatmulArgs a) {
+    constexpr int kXBytes = BM * kRow, kWBytes = BN * (MXX ? kRow : kWRow);
+    constexpr int kSBytes = MXX ? (BM + BN) * 8 : 0;
+    constexpr int kStage = kXBytes + kWBytes + kSBytes;
+    constexpr int kSlab = MXX ? 256 : 64;       // columns of a slab
+    constexpr int TR = MXX ? 16 : 32;           // rows of a matrix instruction's tile
+    constexpr int MT = BM / 2 / TR, NT = BN / 4 / TR;   // tiles of a wave
+    constexpr int HT = MXX ? MT / 2 : MT;       // tiles along M of a step
+    constexpr int kXLoads = kXBytes / 1024 / kWaves, kWLoads = kWBytes / 1024 / kWaves;
+    __shared__ __attribute__((aligned(1024))) uint8_t stage0[kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t stage1[kStage];
+
+    const int tid = (int)threadIdx.x, lane = tid & 63, wave = readfirstlane(tid >> 6);
+    const int r = lane % TR, g = lane / TR;
+    const int wm = wave >> 2, wn = wave & 3;
+    const int64_t nb = (a.K + 31) / 32;
+
+    Place p;
+    if (GROUPED) {
+        if (!place_grouped<BM>(a, p)) return;
+    } else {
+        // groups of 8 tiles along M share the rows of W; each XCD takes a contiguous range
+        const int64_t mt = (a.M + BM - 1) / BM, nt = (a.N + BN - 1) / BN;
+        const int64_t t = xcd_block(blockIdx.x, mt * nt);
+        const int64_t grp = t / (8 * nt), m8 = grp * 8, gm = mt - m8 < 8 ? mt - m8 : 8;
+        const int64_t in = t - grp * 8 * nt;
+        p.m0 = (m8 + in % gm) * BM;
+        p.n0 = in / gm * BN;
+        p.m_end = p.m0 + BM < a.M ? p.m0 + BM : a.M;
+        p.expert = 0;
+    }
+    const int64_t slots = a.M * a.top_k;
+
+    // Row of tile row i, counted from the tile's first (in a list: the row of x);
+    // rows that are not there repeat one that is.
+    const int m_rows = (int)(p.m_end - p.m0), n_rows = (int)(a.N - p.n0 < BN ? a.N - p.n0 : BN);
+    auto x_row = [&](int i) -> int64_t {
+        const int m = i < m_rows ? i : m_rows - 1;
+        if (!GROUPED) return m;
+        const int64_t slot = a.order[p.m0 + m];
+        return slot >= 0 && slot < slots ? slot / a.top_k : 0;
+    };
+    auto w_row = [&](int i) { return i < n_rows ? i : n_rows - 1; };
+
+    // Loads to LDS: wave w fills 1024 bytes at a time; lane l brings the chunk
+    // whose slot is l % 8 of row l / 8 (or, of W's 32-byte rows, half l % 2 of row l / 2).
+    const int x_sub = lane >> 3;
+    auto x_chunk = [&](int j) { return (lane & 7) ^ swizzle((wave * kXLoads + j) * 8 + x_sub); };
+    // Offsets from the tile's first row fit 32 bits (mx_gemm_takes); the rows of a list have 64.
+    typedef typename std::conditional<GROUPED, int64_t, uint32_t>::type XOffset;
+    const uint8_t* const xbase = MXX ? a.x_codes + p.m0 * nb * 16 : (const uint8_t*)(a.x + (GROUPED ? 0 : p.m0) * a.ldx);
+    const int64_t xrow_bytes = MXX ? nb * 16 : a.ldx * 2;
+    XOffset xsrc[kXLoads];
+#pragma unroll
+    for (int j = 0; j < kXLoads; ++j)
+        xsrc[j] = (XOffset)(x_row((wave * kXLoads + j) * 8 + x_sub) * xrow_bytes) + (XOffset)(x_chunk(j) * 16);
+    auto w_chunk = [&](int j) { return MXX ? (lane & 7) ^ swizzle((wave * kWLoads + j) * 8 + x_sub) : lane & 1; };
+    const uint8_t* const wbase = a.codes + (p.expert * a.N + p.n0) * nb * 16;
+    uint32_t wsrc[kWLoads];
+#pragma unroll
+    for (int j = 0; j < kWLoads; ++j) {
+        const int row = MXX ? (wave * kWLoads + j) * 8 + x_sub : (wave * kWLoads + j) * 32 + (lane >> 1);
+        wsrc[j] = (uint32_t)(w_row(row) * (int)nb * 16 + w_chunk(j) * 16);
+    }
+    // Scales.  MXX: thread tid stages the eight bytes a slab of one row of W (the
+    // first 256 threads) or x.  Otherwise lane (r, g) keeps eight bytes, the scales of four
+    // slabs, of each of its rows of W.
+    const uint8_t* const wscales = a.scales + (p.expert * a.N + p.n0) * nb;
+    const uint8_t* const xscales = MXX ? a.x_scales + p.m0 * nb : nullptr;
+    uint32_t ssrc[NT];
+    const bool stages_w = wave < kWaves / 2;
+    if (MXX) {
+        ssrc[0] = (uint32_t)((stages_w ? w_row(tid) : x_row(tid & (BM - 1))) * nb);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) ssrc[i] = (uint32_t)(w_row(wn * (BN / 4) + TR * i + r) * (int)nb);
+    }
+
+    typedef typename std::conditional<MXX, f32x4, f32x16>::type Acc;
+    Acc acc[NT][MT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) acc[i][j] = (Acc)(0.f);
+
+    // ---- a slab on its way to LDS
+    u32x4 xr[kXLoads];                          // activations on the way through registers (!DIRECT)
+    auto store_x = [&](uint8_t* st) {
+#pragma unroll
+        for (int j = 0; j < kXLoads; ++j) *(u32x4*)(st + (wave * kXLoads + j) * 1024 + lane * 16) = xr[j];
+    };
+    uint64_t sreg = 0u;                         // MXX: scales on their way
+    auto start = [&](uint8_t* st, int64_t t) {  // slab t, a whole one
+        if (MXX)
+            sreg = *(const __attribute__((address_space(1))) u64u*)(scalar_base((stages_w ? wscales : xscales) + t * 8) +
+                                                                    lane_offset(ssrc[0]));
+        const GlobalBytes xb = scalar_base(xbase + t * kRow);
+        const GlobalBytes wb = scalar_base(wbase + t * (MXX ? kRow : kWRow));
+#pragma unroll
+        for (int j = 0; j < kXLoads; ++j) {
+            if (DIRECT) load_lds16(xb + lane_offset(xsrc[j]), st + (wave * kXLoads + j) * 1024);
+            else xr[j] = *(const __attribute__((address_space(1))) u32x4h*)(xb + lane_offset(xsrc[j]));
+        }
+#pragma unroll
+        for (int j = 0; j < kWLoads; ++j) load_lds16(wb + lane_offset(wsrc[j]), st + kXBytes + (wave * kWLoads + j) * 1024);
+    };
+    auto finish = [&](uint8_t* st) {            // what came to registers
+        if (MXX && tid < BM + BN) *(uint64_t*)(st + kXBytes + kWBytes + tid * 8) = sreg;
+        if (!DIRECT) store_x(st);
+    };
+    uint64_t sc[NT], sc_next[NT];               // bf16 activations: scales of the slabs at hand
+    auto fetch_scales = [&](int64_t t) {        // of slabs t .. t + 3, as far as there are any: the last eight
+        const int64_t b = 2 * t < nb - 8 ? 2 * t : nb - 8;
+        const GlobalBytes sb = scalar_base(wscales + b);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) sc_next[i] = *(const __attribute__((address_space(1))) u64u*)(sb + lane_offset(ssrc[i]));
+    };
+    auto take_scales = [&](int64_t t) {
+        const int64_t b = 2 * t < nb - 8 ? 2 * t : nb - 8;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) sc[i] = sc_next[i] >> (8 * (int)(2 * t - b));
+    };
+
+    // ---- fragments: step s (of four) of a slab from LDS to registers, then
+    // multiplied.  bf16 activations: 16 columns a step.  MXX: 128 columns, of
+    // half of the wave's tokens (fewer fragments at a time: 256 registers hold
+    // them beside 128 accumulators).
+    u32x4 wf[2][NT], xf[2][HT];                 // bf16 activations: wf[0] is a slab's codes
+    u32x4 wc[NT];                               // bf16 activations: the codes at hand
+    u32x2 sw_raw[NT], sx_raw[MT];
+    int sw[NT], sx[MT];
+    auto read = [&](const uint8_t* st, int s) {
+        const uint8_t* const xt = st + wm * (BM / 2) * kRow;
+        const uint8_t* const wt = st + kXBytes + wn * (BN / 4) * (MXX ? kRow : kWRow);
+        const int at = r * kRow + (((MXX ? 4 * (s >> 1) + g : 4 * g + s) ^ swizzle(r)) << 4);
+        if (MXX && s == 0) {
+            const uint8_t* const ws = st + kXBytes + kWBytes + wn * (BN / 4) * 8;
+            const uint8_t* const xs = st + kXBytes + kWBytes + BN * 8 + wm * (BM / 2) * 8;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) sw_raw[i] = *(const u32x2*)(ws + (TR * i + r) * 8);
+#pragma unroll
+            for (int j = 0; j < MT; ++j) sx_raw[j] = *(const u32x2*)(xs + (TR * j + r) * 8);
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            if (MXX && s % 2 == 0) wf[s >> 1][i] = *(const u32x4*)(wt + TR * i * kRow + at);
+            if (!MXX && s == 0) wf[0][i] = *(const u32x4*)(wt + (TR * i + r) * kWRow + g * 16);
+        }
+#pragma unroll
+        for (int j = 0; j < HT; ++j)
+            xf[s & 1][j] = *(const u32x4*)(xt + TR * ((MXX ? (s & 1) * HT : 0) + j) * kRow + at);
+    };
+    auto multiply = [&](auto step) {
+        constexpr int s = decltype(step)::value;
+        if constexpr (MXX) {
+            if (s == 0) {
+                // bytes g and 4 + g of a row's eight scales: this lane's blocks of the two halves of a slab
+                const uint32_t sel = 0x0c0c0400u + 0x0101u * (uint32_t)g;
+#pragma unroll
+                for (int i = 0; i < NT; ++i) sw[i] = (int)perm_b32(sw_raw[i].y, sw_raw[i].x, sel);
+#pragma unroll
+                for (int j = 0; j < MT; ++j) sx[j] = (int)perm_b32(sx_raw[j].y, sx_raw[j].x, sel);
+            }
+            constexpr int h = s >> 1, j0 = (s & 1) * HT;
+#pragma unroll
+            for (int j = 0; j < HT; ++j)
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+                    acc[i][j0 + j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        mx_operand(wf[h][i]), mx_operand(xf[s & 1][j]), acc[i][j0 + j], 4, 4, h, sw[i], h, sx[j0 + j]);
+        } else {
+            bf16x8 w[NT];
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                if (s == 0) wc[i] = wf[0][i];
+                const uint32_t b = (uint32_t)(sc[i] >> (8 * g)) & 0xffu;
+                w[i] = mx_decode8(wc[i][s], e8m0_bits(b));
+                if (s == 3) sc[i] >>= 16;
+            }
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[i], __builtin_bit_cast(bf16x8, xf[s & 1][j]),
+                                                                        acc[i][j], 0, 0, 0);
+        }
+    };
+    // Keep step s where it is: without this its matrix instructions, which touch
+    // no memory, may be put behind the reads of later steps, whose fragments then
+    // are all held at once.
+    auto hold = [&](int s) {
+#pragma unroll
+        for (int j = 0; j < HT; ++j)
+#pragma unroll
+            for (int i = 0; i < NT; ++i) asm volatile("" : "+v"(acc[i][(MXX ? (s & 1) * HT : 0) + j]));
+        asm volatile("" ::: "memory");
+    };
+    typedef std::integral_constant<int, 0> S0;
+    typedef std::integral_constant<int, 1> S1;
+    typedef std::integral_constant<int, 2> S2;
+    typedef std::integral_constant<int, 3> S3;
+
+    // Slab t in `cur`: its step 0 is in registers.  Step s + 1 is read while step
+    // s multiplies.  Before step 3 every wave has read `cur`, and slab t + 1 has
+    // landed in `other`: while step 3 multiplies, slab t + 2 starts into `cur`
+    // and step 0 of slab t + 1 is read.
+    const int64_t full = a.K / kSlab, slabs = (a.K + kSlab - 1) / kSlab;
+    auto slab = [&](uint8_t* cur, uint8_t* other, int64_t t) {
+        if (!MXX && t % 4 == 0) {
+            take_scales(t);
+            if (t + 4 < slabs) fetch_scales(t + 4);
+        }
+        read(cur, 1);
+        multiply(S0());
+        hold(0);
+        read(cur, 2);
+        multiply(S1());
+        hold(1);
+        read(cur, 3);
+        multiply(S2());
+        hold(2);
+        if (t + 1 < full) finish(other);
+        wait_and_meet();
+        if (t + 2 < full) start(cur, t + 2);
+        if (t + 1 < full) read(other, 0);
+        multiply(S3());
+        hold(3);
+    };
+
+    if (!MXX) fetch_scales(0);
+    if (full > 0) {
+        start(stage0, 0);
+        finish(stage0);
+        wait_and_meet();
+        if (full > 1) start(stage1, 1);
+        read(stage0, 0);
+        for (int64_t t = 0; t < full; t += 2) {
+            slab(stage0, stage1, t);
+            if (t + 1 < full) slab(stage1, stage0, t + 1);
+        }
+    }
+    if (full < slabs) {
+        // The slab that ends past K: activations through registers, zeros past
+        // K; W's chunks past its last block repeat it (their products are 0).
+        wait_and_meet();
+#pragma unroll
+        for (int j = 0; j < kXLoads; ++j) {
+            if (MXX) {
+                xr[j] = (u32x4){0u, 0u, 0u, 0u};
+                if (full * 8 + x_chunk(j) < nb) xr[j] = *(const u32x4*)(xbase + full * kRow + xsrc[j]);
+            } else {
+                const int64_t k = full * 64 + x_chunk(j) * 8;
+                xr[j] = load_x8((const uint16_t*)(xbase + xsrc[j] - x_chunk(j) * 16), k, a.K);
+            }
+        }
+        store_x(stage0);
+#pragma unroll
+        for (int j = 0; j < kWLoads; ++j) {
+            const int64_t c = w_chunk(j), b = full * (kSlab / 32) + c;
+            load_lds16((GlobalBytes)(wbase + wsrc[j] + ((b < nb ? b : nb - 1) - c) * 16),
+                       stage0 + kXBytes + (wave * kWLoads + j) * 1024);
+        }
+        if (MXX) {
+            if (tid < BM + BN)
+                *(uint64_t*)(stage0 + kXBytes + kWBytes + tid * 8) =
+                    scales8((stages_w ? wscales : xscales) + ssrc[0], full * 8, nb);
+        } else if (full % 4 == 0) {
+            take_scales(full);
+        }
+        wait_and_meet();
+        read(stage0, 0);
+        read(stage0, 1);
+        multiply(S0());
+        read(stage0, 2);
+        multiply(S1());
+        read(stage0, 3);
+        multiply(S2());
+        multiply(S3());
+    }
+
+    // lane (r, g) of tile (i, j): token TR j + r, four n from TR i + 8 q + 4 g for
+    // each q (16 x 16 tiles: from 4 g)
+    const int64_t n_left = a.N - p.n0;
+    const bool quads = a.N % 4 == 0 && ((uintptr_t)a.y & 15) == 0;
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+        const int64_t m = p.m0 + wm * (BM / 2) + TR * j + r;
+        if (m >= p.m_end) continue;
+        int64_t out = m;
+        if (GROUPED) {
+            out = a.order[m];
+            if (out < 0 || out >= slots) continue;
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int q = 0; q < TR * TR / 256; ++q) {
+                const int col = wn * (BN / 4) + TR * i + 8 * q + 4 * g;
+                if (col >= n_left) continue;
+                f32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+                if (a.bias) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (col + e < n_left) v[e] += a.bias[p.expert * a.N + p.n0 + col + e];
+                }
+                const int64_t at = out * a.N + p.n0 + col;
+                if (quads) {
+                    if (a.y_dtype == TQ_F32) {
+                        *(f32x4*)((float*)a.y + at) = v;
+                    } else {
+                        u32x2 d;
+                        d.x = (uint32_t)f32_to_bf16_rne(v.x) | (uint32_t)f32_to_bf16_rne(v.y) << 16;
+                        d.y = (uint32_t)f32_to_bf16_rne(v.z) | (uint32_t)f32_to_bf16_rne(v.w) << 16;
+                        *(u32x2*)((uint16_t*)a.y + at) = d;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (col + e >= n_left) continue;
+                        if (a.y_dtype == TQ_F32) ((float*)a.y)[at + e] = v[e];
+                        else ((uint16_t*)a.y)[at + e] = f32_to_bf16_rne(v[e]);
+                    }
+                }
+            }
+    }
+}
+
+// Rows of slots of no expert: NaN.
+__global__ void __launch_bounds__(256) nan_rows_kernel(MxMatmulArgs a) {
+    const int64_t slots = a.M * a.top_k;
+    int64_t begin = a.offsets[a.n_experts];
+    begin = begin < 0 ? 0 : begin;
+    for (int64_t i = begin + blockIdx.x; i < slots; i += gridDim.x) {
+        const int64_t slot = a.order[i];
+        if (slot < 0 || slot >= slots) continue;
+        for (int64_t n = threadIdx.x; n < a.N; n += 256) {
+            if (a.y_dtype == TQ_F32) ((float*)a.y)[slot * a.N + n] = __builtin_nanf("");
+            else ((uint16_t*)a.y)[slot * a.N + n] = 0x7fc0u;
+        }
+    }
+}
+
+template <bool MXX, bool DIRECT, int BM, bool GROUPED>
+hipError_t launch(const MxMatmulArgs& a, hipStream_t s) {
+    const int64_t nt = (a.N + BN - 1) / BN;
+    int64_t blocks = (a.M + BM - 1) / BM * nt;
+    if (GROUPED) {
+        // whole shares of the 8 XCDs: the largest share has a tile more than an eighth
+        const int64_t tiles = (a.M * a.top_k / BM + (a.n_experts < a.M * a.top_k ? a.n_experts : a.M * a.top_k)) * nt;
+        blocks = (tiles / 8 + 1) * 8;
+    }
+    if (!grid_fits(blocks, kThreads)) return hipErrorInvalidConfiguration;
+    mx_gemm_kernel<MXX, DIRECT, BM, GROUPED><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+    hipError_t e = hipGetLastError();
+    if (!GROUPED || e != hipSuccess) return e;
+    nan_rows_kernel<<<256, 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+bool mx_gemm_takes(const MxMatmulArgs& a) {
+    return a.K >= kMinTiledK && a.K * 2 < kMaxTiledBytes &&
+           (a.x_codes || a.n_experts > 0 || a.M == 1 || a.ldx * 2 < kMaxTiledBytes);
+}
+
+hipError_t launch_mx_gemm(const MxMatmulArgs& a, hipStream_t s) {
+    if (a.x_codes) return launch<true, true, 256, false>(a, s);
+    const bool direct = ((uintptr_t)a.x & 15) == 0 && a.ldx % 8 == 0;
+    if (a.n_experts > 0) return direct ? launch<false, true, 128, true>(a, s) : launch<false, false, 128, true>(a, s);
+    return direct ? launch<false, true, 256, false>(a, s) : launch<false, false, 256, false>(a, s);
+}
+
+}  // namespace dmm

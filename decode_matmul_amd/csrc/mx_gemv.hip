@@ -166,6 +166,8 @@ hipError_t launch(const MxMatmulArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_mx_matmul(const MxMatmulArgs& a, hipStream_t s) {
+    const bool many = a.n_experts > 0 ? a.M * a.top_k >= 32 * (int64_t)a.n_experts : a.M > 64 && a.M * a.N >= (int64_t)64 << 16;
+    if (many && mx_gemm_takes(a)) return launch_mx_gemm(a, s);
     if (a.n_experts > 0) return launch<false, 2, true>(a, s);
     if (a.x_codes) return a.M <= 16 ? launch<true, 1, false>(a, s) : launch<true, 4, false>(a, s);
     return a.M <= 16 ? launch<false, 1, false>(a, s) : launch<false, 4, false>(a, s);
