@@ -371,7 +371,7 @@ int mx_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t
 
 // Every MXFP4 product; a holds the call's arguments, x_any its activations.
 static int mx_matmul_common(dmm::MxMatmulArgs& a, const void* x_any, bool x_rows_ok, void* stream) {
-    if (a.M < 0 || a.K < 0 || a.N < 0 || a.M >= kMaxDim || a.K >= kMaxDim || a.N >= kMaxDim || !x_rows_ok)
+    if (a.M < 0 || a.K < 0 || a.N < 0 || a.M >= kMaxDim || a.K >= dmm::kMxMaxK || a.N >= kMaxDim || !x_rows_ok)
         return TQ_ERR_SHAPE;
     if (!is_dtype(a.y_dtype)) return TQ_ERR_DTYPE;
     if (a.M == 0 || a.N == 0) return TQ_OK;

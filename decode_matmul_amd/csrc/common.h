@@ -296,6 +296,8 @@ struct MxMatmulArgs {
     void* y;                  // [M, N] or [M, top_k, N]
     int y_dtype;
 };
+// Most columns of a product: a tile's rows lie within 32-bit offsets of its first.
+constexpr int64_t kMxMaxK = (int64_t)1 << 27;
 hipError_t launch_mx_matmul(const MxMatmulArgs& a, hipStream_t s);
 // Tiled form for many tokens; mx_gemm_takes: whether it can take the call.
 bool mx_gemm_takes(const MxMatmulArgs& a);

@@ -10,6 +10,9 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4a __attribute__((ext_vector_type(4), aligned(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint64_t u64u __attribute__((aligned(1)));
+typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(1)));
 
 // An E8M0 byte as the fp32 whose exponent field it is: what the scaled
 // conversions take (0 stands for 2^-127 and 255 for NaN there).
@@ -35,6 +38,73 @@ __device__ __forceinline__ bf16x8 mx_decode8(uint32_t c, float scale) {
 // half of the register group is not read for 4-bit types).
 __device__ __forceinline__ i32x8 mx_operand(u32x4 c) {
     return (i32x8){(int)c.x, (int)c.y, (int)c.z, (int)c.w, 0, 0, 0, 0};
+}
+
+// Scale bytes b .. b + 7 of a row of nb (those past the row are 127).
+__device__ __forceinline__ uint64_t scales8(const uint8_t* row, int64_t b, int64_t nb) {
+    if (b + 8 <= nb) return *(const u64u*)(row + b);
+    uint64_t v = 0x7f7f7f7f7f7f7f7full;
+#pragma unroll 1
+    for (int i = 0; b + i < nb; ++i) v ^= (uint64_t)(row[b + i] ^ 0x7fu) << (8 * i);
+    return v;
+}
+
+// Eight activations at column k of a row (past K they are 0).
+__device__ __forceinline__ u32x4 load_x8(const uint16_t* row, int64_t k, int64_t K) {
+    if (k + 8 <= K) return *(const u32x4h*)(row + k);
+    uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+    for (int i = 0; i < 7 && k + i < K; ++i) {
+        if (i < 4) lo |= (uint64_t)row[k + i] << (16 * i);
+        else hi |= (uint64_t)row[k + i] << (16 * (i - 4));
+    }
+    const u32x4 v = {(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+    return v;
+}
+
+// A uniform pointer the compiler keeps in scalar registers as it is, so that a
+// lane's address stays base + 32-bit offset (folded into per-lane pointers,
+// the slabs' addresses take more registers than there are).
+typedef const __attribute__((address_space(1))) uint8_t* GlobalBytes;
+__device__ __forceinline__ GlobalBytes scalar_base(const uint8_t* p) {
+    GlobalBytes q = (GlobalBytes)p;
+    asm("" : "+s"(q));
+    return q;
+}
+
+// A lane's value, likewise kept as it is where it stands: what is computed from
+// it is computed there (widened or added ahead of a loop, offsets take
+// registers all through it).
+__device__ __forceinline__ uint32_t lane_offset(uint32_t o) {
+    asm volatile("" : "+v"(o));
+    return o;
+}
+__device__ __forceinline__ int64_t lane_offset(int64_t o) {
+    asm volatile("" : "+v"(o));
+    return o;
+}
+
+// 16 bytes a lane from global memory to LDS: lane l's land at lds + 16 l.
+__device__ __forceinline__ void load_lds16(GlobalBytes g, void* lds) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)g,
+                                     (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+}
+
+// At most VM vector loads of this wave outstanding.
+template <int VM>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | 0xf70);
+    asm volatile("" ::: "memory");
+}
+
+// The workgroup's barrier for LDS accesses: this wave's are done, its loads
+// may be on their way.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xc07f);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
 }  // namespace dmm

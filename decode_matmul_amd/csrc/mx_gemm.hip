@@ -36,34 +36,8 @@ constexpr int64_t kMinTiledK = 256, kMaxTiledBytes = (int64_t)1 << 24;
 constexpr int kWRow = 32;                       // bytes of codes a row with bf16 activations
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint64_t u64u __attribute__((aligned(1)));
 
 __device__ __forceinline__ int swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
-
-// A uniform pointer the compiler keeps in scalar registers as it is, so that a
-// lane's address stays base + 32-bit offset (folded into per-lane pointers,
-// the slabs' addresses take more registers than there are).
-typedef const __attribute__((address_space(1))) uint8_t* GlobalBytes;
-__device__ __forceinline__ GlobalBytes scalar_base(const uint8_t* p) {
-    GlobalBytes q = (GlobalBytes)p;
-    asm("" : "+s"(q));
-    return q;
-}
-
-// A lane's offset from a scalar base, likewise kept as it is (widened ahead of
-// the loop it would take two registers).
-__device__ __forceinline__ uint32_t lane_offset(uint32_t o) {
-    asm("" : "+v"(o));
-    return o;
-}
-__device__ __forceinline__ int64_t lane_offset(int64_t o) { return o; }
-
-// 16 bytes a lane from global memory to LDS: lane l's land at lds + 16 l.
-__device__ __forceinline__ void load_lds16(GlobalBytes g, void* lds) {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)g,
-                                     (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
-}
 
 // No load and no LDS access of this wave outstanding (expcnt aside), then the
 // workgroup's barrier.
@@ -72,25 +46,6 @@ __device__ __forceinline__ void wait_and_meet() {
     __builtin_amdgcn_s_waitcnt(0x70);
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-}
-
-// Scale bytes b .. b + 7 of a row of nb (those past the row are 127).
-__device__ __forceinline__ uint64_t scales8(const uint8_t* row, int64_t b, int64_t nb) {
-    uint64_t v = 0x7f7f7f7f7f7f7f7full;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (b + i < nb) v ^= (uint64_t)(row[b + i] ^ 0x7fu) << (8 * i);
-    return v;
-}
-
-// Eight activations at column k of a row (past K they are 0).
-__device__ __forceinline__ u32x4 load_x8(const uint16_t* row, int64_t k, int64_t K) {
-    if (k + 8 <= K) return *(const u32x4h*)(row + k);
-    u32x4 v = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (k + i < K) v[i >> 1] |= (uint32_t)row[k + i] << (16 * (i & 1));
-    return v;
 }
 
 // The workgroup's tile: its tokens are positions [m0, m_end) of the batch or
@@ -178,7 +133,7 @@ __device__ bool place_grouped(const MxMatmulArgs& a, Place& p) {
 // MXX: activations in MXFP4.  DIRECT: whole slabs of bf16 activations go
 // straight to LDS (rows 16-byte aligned); otherwise through registers.
 template <bool MXX, bool DIRECT, int BM, bool GROUPED>
-__global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(MxMatmulArgs a) {
+__global__ void __launch_bounds__(kThreads, BM == 128 ? 4 : 1) mx_gemm_kernel(MxMatmulArgs a) {
     constexpr int kXBytes = BM * kRow, kWBytes = BN * (MXX ? kRow : kWRow);
     constexpr int kSBytes = MXX ? (BM + BN) * 8 : 0;
     constexpr int kStage = kXBytes + kWBytes + kSBytes;
@@ -218,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(MxMatmulArgs a) {
         const int m = i < m_rows ? i : m_rows - 1;
         if (!GROUPED) return m;
         const int64_t slot = a.order[p.m0 + m];
-        return slot >= 0 && slot < slots ? slot / a.top_k : 0;
+        return slot >= 0 && slot < slots ? (int64_t)((uint32_t)slot / (uint32_t)a.top_k) : 0;
     };
     auto w_row = [&](int i) { return i < n_rows ? i : n_rows - 1; };
 

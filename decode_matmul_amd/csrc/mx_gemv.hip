@@ -1,166 +1,339 @@
-// MXFP4 products, weight-streaming form: y[m, n] = sum_k x[m, k] w_hat[n, k] (+ bias[n]).
+// MXFP4 products, weight-streaming form for few tokens: y[m, n] = sum_k x[m, k] w_hat[n, k] (+ bias[n]).
 //
-// Mathematics.  A block of 32 weights is 16 code bytes and one scale byte, so
-// 128 weights of 16 rows are exactly one 16-byte load and one byte a lane:
-// lane (r, g) = (lane % 16, lane / 16) takes block 4 s + g of row n0 + r.  That
-// is the operand layout of the 16x16x128 scaled matrix instruction, which
-// takes MXFP4 activations loaded the same way (mx_matmul_mx).  For bf16
-// activations the hardware turns eight codes and their scale into eight exact
-// bf16 values (four conversions), and the four octets of the lane's block go
-// through four 16x16x32 bf16 matrix instructions; the sum over k may be taken
-// in any order, so octet j pairs w[n, 32 b + 8 j ..] with x[m, 32 b + 8 j ..].
+// Mathematics.  Lane (r, g) = (lane % 16, lane / 16) takes block 4 u + g of 128
+// columns of row r: with the block's 16 code bytes and one scale byte that is
+// the operand layout of the 16x16x128 scaled matrix instruction, which takes
+// MXFP4 activations loaded the same way (mx_matmul_mx).  For bf16 activations
+// the hardware turns eight codes and their scale into eight exact bf16 values
+// (four conversions), and the four octets of the lane's block go through four
+// 16x16x32 bf16 matrix instructions; the sum over k may be taken in any order,
+// so octet j pairs w[n, 32 b + 8 j ..] with x[m, 32 b + 8 j ..].
 //
-// Bound: the package's bytes.  The waves of a workgroup share 16 rows and
-// take the 128-wide steps of K in turn (few tokens leave no other work to
-// spread over the chip); their sums meet in LDS, in wave order.
+// Bound: the package's bytes.  Few tokens leave no other work to spread over
+// the chip, so a workgroup owns 16 NT rows and its W waves take the 256-wide
+// chunks of K in turn, each with two chunks' loads in flight; the waves' sums
+// meet in LDS, in wave order.  Everything read once goes through LDS:
+//  * Codes by loads straight to LDS, whole 128-byte lines of 8 rows an
+//    instruction.  Read in the matrix instruction's layout instead (16 rows x
+//    64 bytes), 31 MB took 7.4 us against 6.2 in a bare read.
+//  * Scales, 256 bytes a row for 8192 columns, loaded once by the workgroup:
+//    read by each wave, 8 bytes of 16 rows at a time, they cost 1.4 us of 8.8.
+//  * bf16 activations of a chunk, straight to a buffer of the wave's own.
+// 16-byte pieces are permuted within their rows so that the 16 rows of a
+// fragment read hit all banks.
 #include "mx.h"
 
 namespace dmm {
 
 namespace {
 
-constexpr int kWaves = 8;
-constexpr int kThreads = 64 * kWaves;
+constexpr int kChunk = 256;                     // columns: 8 blocks, 128 bytes of codes
+constexpr int kSegChunks = 32;                  // chunks whose scales are staged together: 256 bytes a row
 
-// One lane's eight activations at column k of a row (past K they are 0).
-__device__ __forceinline__ u32x4 load_x8(const uint16_t* row, int64_t k, int64_t K) {
-    if (k + 8 <= K) return *(const u32x4h*)(row + k);
-    u32x4 v = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (k + i < K) v[i >> 1] |= (uint32_t)row[k + i] << (16 * (i & 1));
-    return v;
+// An entry of the order list, wave-uniform.
+__device__ __forceinline__ int order_at(const int32_t* order, int64_t i) {
+    return ((const __attribute__((address_space(4))) int32_t*)order)[i];
 }
 
-// MXX: activations in MXFP4.  MT: 16-token tiles of a workgroup.
-template <bool MXX, int MT, bool GROUPED>
-__global__ void __launch_bounds__(kThreads) mx_gemv_kernel(MxMatmulArgs a) {
-    __shared__ f32x4 red[kWaves][MT][64];
-    const int lane = (int)threadIdx.x & 63, wave = readfirstlane((int)threadIdx.x >> 6);
+// MXX: activations in MXFP4.  TB: tokens of a pass.  NT: 16-row tiles.  W:
+// waves.  DIRECT: bf16 activations 16-byte aligned.
+template <bool MXX, int TB, int NT, int W, bool DIRECT, bool GROUPED>
+__global__ void __launch_bounds__(64 * W, 2) mx_gemv_kernel(MxMatmulArgs a, int scale_lines) {
+    constexpr int rows = 16 * NT;
+    constexpr int kThreads = 64 * W;
+    constexpr int kWBytes = NT * 2048, kXBytes = MXX ? 0 : TB * 512, kBuf = kWBytes + kXBytes;
+    constexpr int kXLoads = MXX ? 3 : DIRECT ? TB / 2 : 0, kLoads = 2 * NT + kXLoads;     // loads of a chunk
+    __shared__ __attribute__((aligned(1024))) uint8_t buf0[W][kBuf];
+    __shared__ __attribute__((aligned(1024))) uint8_t buf1[W][kBuf];
+    __shared__ __attribute__((aligned(1024))) uint8_t sbuf[NT * 4096];
+    const int tid = (int)threadIdx.x, lane = tid & 63, wave = readfirstlane(tid >> 6);
     const int r = lane & 15, g = lane >> 4;
-    const int64_t nb = (a.K + 31) / 32, steps = (nb + 3) / 4;
-    const int64_t ntiles = (a.N + 15) / 16, by = blockIdx.x / ntiles;
-    const int64_t n0 = (blockIdx.x - by * ntiles) * 16;
-    const int64_t n = n0 + r < a.N ? n0 + r : a.N - 1;          // rows past N repeat the last
-    const int64_t expert = GROUPED ? by : 0;
+    const int nb = (int)((a.K + 31) / 32);
+    const uint32_t ntiles = (uint32_t)((a.N + rows - 1) / rows), by = GROUPED ? blockIdx.x / ntiles : 0u;
+    const int64_t n0 = (int64_t)(blockIdx.x - by * ntiles) * rows;
+    const int nrows = (int)(a.N - n0 < rows ? a.N - n0 : rows);
+    const int64_t expert = by;
 
     int64_t begin = 0, end = a.M;                               // tokens, or positions in the order list
     const int64_t slots = a.M * a.top_k;
     if (GROUPED) {
-        begin = a.offsets[expert];
-        end = expert < a.n_experts ? (int64_t)a.offsets[expert + 1] : slots;
+        begin = order_at(a.offsets, expert);
+        end = expert < a.n_experts ? (int64_t)order_at(a.offsets, expert + 1) : slots;
         begin = begin < 0 ? 0 : begin;
         end = end > slots ? slots : end;
         if (expert == a.n_experts) {                            // slots of no expert
-            for (int64_t i = begin * 16 + threadIdx.x; i < end * 16; i += kThreads) {
-                const int64_t slot = a.order[i >> 4], col = n0 + (i & 15);
-                if (slot < 0 || slot >= slots || col >= a.N) continue;
-                if (a.y_dtype == TQ_F32) ((float*)a.y)[slot * a.N + col] = __builtin_nanf("");
-                else ((uint16_t*)a.y)[slot * a.N + col] = 0x7fc0u;
+            for (int64_t i = begin; i < end; ++i) {
+                const int64_t slot = a.order[i];
+                if (slot < 0 || slot >= slots || tid >= nrows) continue;
+                if (a.y_dtype == TQ_F32) ((float*)a.y)[slot * a.N + n0 + tid] = __builtin_nanf("");
+                else ((uint16_t*)a.y)[slot * a.N + n0 + tid] = 0x7fc0u;
             }
             return;
         }
-    } else {
-        begin = by * (16 * MT);
-        end = begin + 16 * MT < a.M ? begin + 16 * MT : a.M;
     }
-    const uint8_t* const wc = a.codes + (expert * a.N + n) * nb * 16;
-    const uint8_t* const ws = a.scales + (expert * a.N + n) * nb;
+    // offsets from the tile's first row (32 bits hold them: kMxMaxK); rows past the tile repeat its last
+    const uint8_t* const wbase = a.codes + (expert * a.N + n0) * nb * 16;
+    const uint8_t* const sbase = a.scales + (expert * a.N + n0) * nb;
+    auto piece = [&](int l) { return (l & 7) ^ ((l >> 3) & 7); };      // of row l / 8 of eight: see swizzle
+    uint32_t woff[2 * NT];
+#pragma unroll
+    for (int i = 0; i < 2 * NT; ++i) {
+        const int row = 8 * i + (lane >> 3);
+        woff[i] = (uint32_t)(row < nrows ? row : nrows - 1) * (uint32_t)nb * 16u;
+    }
+    const int full = (int)(a.K / kChunk), chunks = (int)((a.K + kChunk - 1) / kChunk);
+    const int segs = (chunks + kSegChunks - 1) / kSegChunks;
+    // Row of 128 bytes, 16-byte pieces: piece q of row i sits at q ^ swizzle(i).
+    auto swizzle = [](int i) { return (i & 7) ^ ((i >> 3) & 1); };
 
-    for (int64_t t0 = begin; t0 < end; t0 += 16 * MT) {
-        // this lane's tokens: row of x, and whether it is there
-        int64_t row[MT];
-        bool there[MT];
+    for (int64_t t0 = begin; t0 < end; t0 += TB) {
+        const int count = (int)(end - t0 < TB ? end - t0 : TB);
+        // Two tokens a load: lanes 0..31 and 32..63 bring 512 bytes each; piece q
+        // of token i sits at q ^ i.
+        int64_t xoff[TB / 2];
+        auto find_x = [&]() {
+            // by scalar loads: a vector load would be waited for behind those to LDS
+            int slot[TB];
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const int64_t t = t0 + 16 * i + r;
-            there[i] = t < end;
-            row[i] = there[i] ? t : 0;
-            if (GROUPED && there[i]) {
-                const int64_t slot = a.order[t];
-                there[i] = slot >= 0 && slot < slots;
-                row[i] = there[i] ? slot / a.top_k : 0;
-            }
-        }
-        f32x4 acc[MT];
+            for (int i = 0; i < TB; ++i) slot[i] = GROUPED ? order_at(a.order, t0 + (i < count ? i : count - 1)) : 0;
 #pragma unroll
-        for (int i = 0; i < MT; ++i) acc[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
-        for (int64_t s = wave; s < steps; s += kWaves) {
-            const int64_t b = 4 * s + g;
-            const bool in = b < nb;
-            u32x4 c = {0u, 0u, 0u, 0u};
-            uint32_t sb = 127u;
-            if (in) {
-                c = *(const u32x4*)(wc + b * 16);
-                sb = ws[b];
+            for (int j = 0; j < TB / 2; ++j) {
+                const int i = 2 * j + (lane >> 5);
+                int64_t row = t0 + (i < count ? i : count - 1);     // tokens past the pass repeat its last
+                if (GROUPED) {
+                    const uint32_t s = (uint32_t)(lane < 32 ? slot[2 * j] : slot[2 * j + 1]);
+                    row = (int64_t)((s < (uint32_t)slots ? s : 0u) / (uint32_t)a.top_k);
+                }
+                xoff[j] = (row * a.ldx + (((lane & 31) ^ i) << 3)) * 2;
             }
+        };
+        const uint8_t* const xcbase = MXX ? a.x_codes + t0 * nb * 16 : nullptr;
+        const uint8_t* const xsbase = MXX ? a.x_scales + t0 * nb : nullptr;
+        const uint32_t xr = (uint32_t)(r < count ? r : count - 1) * (uint32_t)nb;
+        // where the lane's four octets of a token's 128 columns, and its two blocks of a row, sit
+        uint32_t xat[4], wat[2];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) xat[j] = (uint32_t)((r & (TB - 1)) * 512 + (((4 * g + j) ^ (r & (TB - 1))) << 4));
+#pragma unroll
+        for (int u = 0; u < 2; ++u) wat[u] = (uint32_t)(r * 128 + (((4 * u + g) ^ swizzle(r)) << 4));
+
+        // MXX: activations of the chunks in flight
+        u32x4 xc0[2], xc1[2];
+        uint64_t xs0 = 0, xs1 = 0;
+        auto load_w = [&](uint8_t* b, int c) {
+            const GlobalBytes cb = scalar_base(wbase + (int64_t)c * 128);
+#pragma unroll
+            for (int i = 0; i < 2 * NT; ++i)
+                load_lds16(cb + lane_offset(woff[i] + (uint32_t)((piece(lane) ^ (i & 1)) << 4)), b + i * 1024);
+        };
+        auto load_x = [&](uint8_t* b, u32x4* xc, uint64_t& xs, int c) {
             if (MXX) {
-                const i32x8 A = mx_operand(c);
+                const GlobalBytes xb = scalar_base(xcbase + (int64_t)c * 128), sb = scalar_base(xsbase + (int64_t)c * 8);
 #pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    u32x4 xc = {0u, 0u, 0u, 0u};
-                    uint32_t xs = 127u;
-                    if (in && there[i]) {
-                        xc = *(const u32x4*)(a.x_codes + (row[i] * nb + b) * 16);
-                        xs = a.x_scales[row[i] * nb + b];
-                    }
-                    acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, mx_operand(xc), acc[i], 4, 4, 0,
-                                                                              (int)sb, 0, (int)xs);
-                }
+                for (int u = 0; u < 2; ++u)
+                    xc[u] = *(const __attribute__((address_space(1))) u32x4*)(xb + lane_offset((xr + (uint32_t)g) * 16u) + u * 64);
+                xs = *(const __attribute__((address_space(1))) u64u*)(sb + lane_offset(xr));
             } else {
-                const float scale = e8m0_bits(sb);
+                const GlobalBytes xb = scalar_base((const uint8_t*)a.x + (int64_t)c * (2 * kChunk));
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const bf16x8 w = mx_decode8(c[j], scale);
-                    const int64_t k = b * 32 + j * 8;
+                for (int j = 0; j < TB / 2; ++j) {
+                    if (DIRECT) load_lds16(xb + lane_offset(xoff[j]), b + kWBytes + j * 1024);
+                    else
+                        *(u32x4*)(b + kWBytes + j * 1024 + lane * 16) =
+                            *(const __attribute__((address_space(1))) u32x4h*)(xb + lane_offset(xoff[j]));
+                }
+            }
+        };
+        auto load = [&](uint8_t* b, u32x4* xc, uint64_t& xs, int c) {
+            load_w(b, c);
+            load_x(b, xc, xs, c);
+        };
+        // the chunk that ends past K: zeros for the activations that are not
+        // there; W's blocks past the last repeat it
+        auto load_tail = [&](uint8_t* b, u32x4* xc, uint64_t& xs, int c) {
+            const int l = (int)lane_offset((uint32_t)lane), lg = l >> 4;
+            if (MXX) {
 #pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        u32x4 xv = {0u, 0u, 0u, 0u};
-                        if (there[i] && k < a.K) xv = load_x8(a.x + row[i] * a.ldx, k, a.K);
-                        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, xv), acc[i],
-                                                                         0, 0, 0);
+                for (int u = 0; u < 2; ++u) {
+                    xc[u] = (u32x4){0u, 0u, 0u, 0u};
+                    if (8 * c + 4 * u + lg < nb)
+                        xc[u] = *(const u32x4*)(xcbase + lane_offset((xr + (uint32_t)lg) * 16u) + (int64_t)c * 128 + u * 64);
+                }
+                xs = scales8(xsbase + lane_offset(xr), 8 * (int64_t)c, nb);
+            } else {
+#pragma unroll
+                for (int j = 0; j < TB / 2; ++j) {
+                    const int q = ((l & 31) ^ (2 * j + (l >> 5))) << 3;
+                    *(u32x4*)(b + kWBytes + j * 1024 + l * 16) =
+                        load_x8(a.x + (lane_offset(xoff[j]) >> 1) - q, (int64_t)c * kChunk + q, a.K);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2 * NT; ++i) {
+                int q = 8 * c + (piece(l) ^ (i & 1));
+                q = q < nb ? q : nb - 1;
+                load_lds16((GlobalBytes)wbase + lane_offset(woff[i] + (uint32_t)q * 16u), b + i * 1024);
+            }
+        };
+        f32x4 acc[NT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) acc[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+        auto multiply = [&](const uint8_t* b, const u32x4* xc, uint64_t xs, int c) {
+            uint64_t sc[NT];
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+                sc[i] = *(const uint64_t*)(sbuf + (16 * i + r) * 256 + ((((c & 31) >> 1) ^ r) << 4) + (c & 1) * 8);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                u32x4 w[NT];
+#pragma unroll
+                for (int i = 0; i < NT; ++i) w[i] = *(const u32x4*)(b + i * 2048 + wat[u]);
+                if (MXX) {
+                    const int s = (int)((uint32_t)(xs >> (32 * u)) >> (8 * g));
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+                        acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                            mx_operand(w[i]), mx_operand(xc[u]), acc[i], 4, 4, 0,
+                            (int)((uint32_t)(sc[i] >> (32 * u)) >> (8 * g)), 0, s);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        // tokens past the pass read another's: their columns are not stored
+                        const bf16x8 x = *(const bf16x8*)(b + kWBytes + xat[j] + u * 256);
+#pragma unroll
+                        for (int i = 0; i < NT; ++i) {
+                            const uint32_t s = ((uint32_t)(sc[i] >> (32 * u)) >> (8 * g)) & 0xffu;
+                            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(mx_decode8(w[i][j], e8m0_bits(s)), x, acc[i],
+                                                                             0, 0, 0);
+                        }
                     }
                 }
+                // keeps each half's operands to that half
+#pragma unroll
+                for (int i = 0; i < NT; ++i) asm volatile("" : "+v"(acc[i]));
+                asm volatile("" ::: "memory");
+            }
+        };
+        // Scales of segment s, 16 pieces of 16 bytes a row: piece q of row i sits at
+        // q ^ (i % 16).  With scale_lines (rows of whole, aligned pieces) wave w
+        // brings them straight to LDS, four rows a load; what lies past the row
+        // repeats its last piece.  Otherwise a thread brings a row's piece through
+        // registers.  Bytes behind a row multiply zeros.
+        constexpr int kScaleLoads = 4 * NT;
+        auto start_scales = [&](int s) {
+#pragma unroll
+            for (int j = 0; j < (kScaleLoads + W - 1) / W; ++j) {
+                const int i = wave + j * W;
+                if (i >= kScaleLoads) break;
+                const int l = (int)lane_offset((uint32_t)lane), row = 4 * i + (l >> 4);
+                const int b = s * (8 * kSegChunks) + (((l ^ row) & 15) << 4);
+                load_lds16((GlobalBytes)sbase + ((int64_t)(row < nrows ? row : nrows - 1) * nb + (b < nb ? b : nb - 16)),
+                           sbuf + i * 1024);
+            }
+        };
+        auto copy_scales = [&](int s) {
+#pragma unroll 1
+            for (int q = tid; q < 256 * NT; q += kThreads) {
+                const int row = q >> 4, b = s * (8 * kSegChunks) + (q & 15) * 16;
+                if (b >= nb) continue;
+                const uint8_t* const p = sbase + (int64_t)(row < nrows ? row : nrows - 1) * nb;
+                const uint64_t lo = scales8(p, b, nb), hi = scales8(p, b + 8, nb);
+                *(u32x4*)(sbuf + row * 256 + (((q ^ row) & 15) << 4)) =
+                    (u32x4){(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+            }
+        };
+
+        // This wave's chunks are wave, wave + W, ..: two in flight, waited for by
+        // count (at most the loads issued after them outstanding; the first two
+        // send for their codes before their activations, whose addresses come later).
+        uint8_t* const b0 = buf0[wave];
+        uint8_t* const b1 = buf1[wave];
+        if (segs > 0) {                                             // K = 0: nothing to read
+            if (scale_lines) start_scales(0);
+            else copy_scales(0);
+        }
+        asm volatile("" ::: "memory");
+        if (wave < full) load_w(b0, wave);
+        if (wave + W < full) load_w(b1, wave + W);
+        asm volatile("" ::: "memory");
+        if (!MXX) find_x();
+        if (wave < full) load_x(b0, xc0, xs0, wave);
+        asm volatile("" ::: "memory");
+        if (wave + W < full) load_x(b1, xc1, xs1, wave + W);
+        if (wave + W < full) wait_loads<2 * kLoads>();
+        else if (wave < full) wait_loads<kLoads>();
+        else wait_loads<0>();
+        for (int s = 0; s < segs; ++s) {
+            if (s > 0) {
+                lds_barrier();                                      // every wave has read the segment before
+                if (scale_lines) start_scales(s);
+                else copy_scales(s);
+                wait_loads<0>();
+            }
+            lds_barrier();
+            const int c_end = (s + 1) * kSegChunks < full ? (s + 1) * kSegChunks : full;
+            for (int c = s * kSegChunks + wave; c < c_end; c += 2 * W) {
+                if (c == wave && c + W < full) wait_loads<kXLoads>();
+                else if (c + W < full) wait_loads<kLoads>();
+                else wait_loads<0>();
+                multiply(b0, xc0, xs0, c);
+                if (c + 2 * W < full) load(b0, xc0, xs0, c + 2 * W);
+                if (c + W >= c_end) break;
+                if (c + 2 * W < full) wait_loads<kLoads>();
+                else wait_loads<0>();
+                multiply(b1, xc1, xs1, c + W);
+                if (c + 3 * W < full) load(b1, xc1, xs1, c + 3 * W);
             }
         }
+        if (full < chunks && full % W == wave) {
+            load_tail(b0, xc0, xs0, full);
+            wait_loads<0>();
+            multiply(b0, xc0, xs0, full);
+        }
+        lds_barrier();
+        f32x4* const red = (f32x4*)&buf0[0][0];                     // [W][NT][64]: the buffers are free now
 #pragma unroll
-        for (int i = 0; i < MT; ++i) red[wave][i][lane] = acc[i];
-        __syncthreads();
-        // lane (m, q) of tile i holds y[m, n0 + 4 q ..]
-        if ((int)threadIdx.x < 64 * MT) {
-            const int i = (int)threadIdx.x >> 6;
-            f32x4 v = red[0][i][lane];
+        for (int i = 0; i < NT; ++i) red[(wave * NT + i) * 64 + lane] = acc[i];
+        lds_barrier();
+        // lane (m, q) of tile i holds y[m, n0 + 16 i + 4 q ..]
+        const int l = (int)lane_offset((uint32_t)lane), m = l & 15;
+        if (wave < NT && m < count) {
+            const int i = wave;
+            f32x4 v = red[i * 64 + l];
 #pragma unroll
-            for (int w = 1; w < kWaves; ++w) v += red[w][i][lane];
-            const int64_t t = t0 + 16 * i + r;
-            int64_t out = t;
-            bool store = t < end;
-            if (GROUPED && store) {
-                out = a.order[t];
-                store = out >= 0 && out < slots;
-            }
-            if (store) {
+            for (int w = 1; w < W; ++w) v += red[(w * NT + i) * 64 + l];
+            int64_t out = t0 + m;
+            if (GROUPED) out = a.order[out];
+            if (out >= 0 && out < slots) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int64_t col = n0 + 4 * g + q;
-                    if (col >= a.N) continue;
-                    const float u = a.bias ? v[q] + a.bias[expert * a.N + col] : v[q];
-                    if (a.y_dtype == TQ_F32) ((float*)a.y)[out * a.N + col] = u;
-                    else ((uint16_t*)a.y)[out * a.N + col] = f32_to_bf16_rne(u);
+                    const int row = 16 * i + 4 * (l >> 4) + q;
+                    if (row >= nrows) continue;
+                    const int64_t col = n0 + row;
+                    const float y = a.bias ? v[q] + a.bias[expert * a.N + col] : v[q];
+                    if (a.y_dtype == TQ_F32) ((float*)a.y)[out * a.N + col] = y;
+                    else ((uint16_t*)a.y)[out * a.N + col] = f32_to_bf16_rne(y);
                 }
             }
         }
-        __syncthreads();
+        lds_barrier();
     }
 }
 
-template <bool MXX, int MT, bool GROUPED>
+template <bool MXX, int TB, int NT, int W, bool DIRECT, bool GROUPED>
 hipError_t launch(const MxMatmulArgs& a, hipStream_t s) {
-    const int64_t tiles = GROUPED ? a.n_experts + 1 : (a.M + 16 * MT - 1) / (16 * MT);
-    const int64_t blocks = (a.N + 15) / 16 * tiles;
-    if (!grid_fits(blocks, kThreads)) return hipErrorInvalidConfiguration;
-    mx_gemv_kernel<MXX, MT, GROUPED><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+    constexpr int rows = 16 * NT;
+    const int64_t blocks = (a.N + rows - 1) / rows * (GROUPED ? a.n_experts + 1 : 1);
+    if (!grid_fits(blocks, 64 * W)) return hipErrorInvalidConfiguration;
+    const int scale_lines = a.K % 512 == 0 && ((uintptr_t)a.scales & 15) == 0;
+    mx_gemv_kernel<MXX, TB, NT, W, DIRECT, GROUPED><<<(unsigned)blocks, 64 * W, 0, s>>>(a, scale_lines);
     return hipGetLastError();
+}
+
+template <int TB, int NT, int W, bool GROUPED>
+hipError_t launch_bf16(const MxMatmulArgs& a, hipStream_t s) {
+    const bool direct = ((uintptr_t)a.x & 15) == 0 && (a.ldx % 8 == 0 || a.M == 1);
+    return direct ? launch<false, TB, NT, W, true, GROUPED>(a, s) : launch<false, TB, NT, W, false, GROUPED>(a, s);
 }
 
 }  // namespace
@@ -168,9 +341,27 @@ hipError_t launch(const MxMatmulArgs& a, hipStream_t s) {
 hipError_t launch_mx_matmul(const MxMatmulArgs& a, hipStream_t s) {
     const bool many = a.n_experts > 0 ? a.M * a.top_k >= 32 * (int64_t)a.n_experts : a.M > 64 && a.M * a.N >= (int64_t)64 << 16;
     if (many && mx_gemm_takes(a)) return launch_mx_gemm(a, s);
-    if (a.n_experts > 0) return launch<false, 2, true>(a, s);
-    if (a.x_codes) return a.M <= 16 ? launch<true, 1, false>(a, s) : launch<true, 4, false>(a, s);
-    return a.M <= 16 ? launch<false, 1, false>(a, s) : launch<false, 4, false>(a, s);
+    if (a.n_experts > 0)
+        return launch_bf16<8, 2, 4, true>(a, s);
+    // Tiles of 16 rows a compute unit decide the shape: few tiles take 8 waves each
+    // (K is what there is to spread), more share a workgroup, so that its
+    // activations are read once for them.  us at 14336 x 4096 (3.5 tiles a unit) /
+    // 8192 x 8192 (2) / 4096 x 4096 (1), by (tiles, waves) of a workgroup:
+    //   M = 1:  (1, 8) 10.3 / 10.6 / 5.2   (2, 4)  9.3 / 12.1 / 6.2   (4, 4) 11.3 / 21.5 / 11.0
+    //   M = 8:  (1, 8) 18.1 / 14.8 / 5.5   (2, 8) 13.2 / 12.0 / 6.1   (2, 4) 10.6 / 13.0 / 6.7
+    //   M = 16: (1, 4) 24.3 / 20.9 / 6.9   (2, 4) 16.2 / 14.9 / 7.5   (4, 4) 12.4 / 17.8 / 9.2
+    const int64_t tiles = (a.N + 15) / 16, cus = compute_unit_count();
+    if (a.x_codes)
+        return tiles <= 2 * cus ? launch<true, 16, 1, 8, true, false>(a, s) : launch<true, 16, 2, 4, true, false>(a, s);
+    if (a.M <= 2) return tiles <= 2 * cus ? launch_bf16<2, 1, 8, false>(a, s) : launch_bf16<2, 2, 4, false>(a, s);
+    if (a.M <= 4) return tiles <= 2 * cus ? launch_bf16<4, 1, 8, false>(a, s) : launch_bf16<4, 2, 4, false>(a, s);
+    if (a.M <= 8)
+        return tiles <= cus ? launch_bf16<8, 1, 8, false>(a, s)
+               : tiles <= 2 * cus ? launch_bf16<8, 2, 8, false>(a, s)
+                                  : launch_bf16<8, 2, 4, false>(a, s);
+    return tiles <= cus ? launch_bf16<16, 1, 4, false>(a, s)
+           : tiles <= 2 * cus ? launch_bf16<16, 2, 4, false>(a, s)
+                              : launch_bf16<16, 4, 4, false>(a, s);
 }
 
 }  // namespace dmm

@@ -511,7 +511,7 @@ int mx_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t
  * fp32, in an order fixed by the shape (two calls give the same bits).  A NaN
  * block makes its output column NaN.  What x holds past K, and codes past K,
  * take no part.  M = 0 or N = 0 is a no-op; with K = 0, x and the package may
- * be NULL and y = bias (or 0).  Sizes below 2^31.
+ * be NULL and y = bias (or 0).  M and N are below 2^31, K is below 2^27.
  */
 int mx_matmul(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint8_t* codes,
               const uint8_t* scales, int64_t N, const float* bias, void* y, int32_t y_dtype,
