@@ -90,6 +90,15 @@ __device__ __forceinline__ void load_lds16(GlobalBytes g, void* lds) {
                                      (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
 }
 
+// Keeps an accumulator's matrix instructions ahead of what follows.  A kernel
+// with one wave a SIMD has its accumulators in the accumulation registers;
+// asking for them elsewhere would copy them there and back.
+template <bool ONE_WAVE, class T>
+__device__ __forceinline__ void hold_acc(T& acc) {
+    if constexpr (ONE_WAVE) asm volatile("" : "+a"(acc));
+    else asm volatile("" : "+v"(acc));
+}
+
 // At most VM vector loads of this wave outstanding.
 template <int VM>
 __device__ __forceinline__ void wait_loads() {

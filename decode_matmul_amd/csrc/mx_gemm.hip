@@ -8,17 +8,18 @@
 // octets 2 g and 2 g + 1 of each 64-wide slab, so its codes are 8 consecutive
 // bytes and one scale.
 //
-// Mapping.  A workgroup of 4 waves (2 x 2) owns BM tokens x 256 rows of W; a
-// wave owns BM / 2 x 128 as 16 x 16 tiles, up to 256 accumulators a lane, one
-// wave a SIMD: its own order of instructions has to hide every latency.  W is
-// the first operand, so a lane ends with four consecutive n of one token.  K is
-// cut into slabs of two steps of the matrix instruction.  Both tiles' rows are
-// 128 bytes (64 bf16 or 256 codes; with bf16 activations W's codes are 32 bytes
-// a slab) and go from global memory straight to LDS, two slabs ahead; fragments
-// go to registers one step ahead.  Chunk c (16 bytes) of row r sits at slot c ^
-// swizzle(r), which spreads the 16 rows of a fragment read over all banks.
-// Slabs take turns in distinct LDS arrays, so the compiler can tell a load in
-// flight to one from the reads of the other.
+// Mapping.  A workgroup owns BM tokens x BN rows of W, its waves equal parts of
+// that (the largest tile: 256 x 256, 8 waves of 128 x 64, 128 accumulators a
+// lane).  W is the first operand, so a lane ends with four consecutive n of one
+// token.  K is cut into slabs, which take turns in two LDS arrays: distinct
+// ones, so the compiler can tell a load in flight to one from the reads of the
+// other.  Activations' rows are 128 bytes a unit (64 bf16 or 256 codes), W's 128
+// or 32, and go from global memory straight to LDS, a slab ahead; fragments go
+// to registers a step ahead.  Chunk c (16 bytes) of a 128-byte row r sits at slot
+// c ^ swizzle(r), which spreads the 16 rows of a fragment read over all banks.
+//
+// Bound: the matrix instructions for the largest tile, the slabs' way from L2
+// (and its latency, where a compute unit has one tile) for the smaller ones.
 #include <type_traits>
 
 #include "mx.h"
@@ -27,8 +28,6 @@ namespace dmm {
 
 namespace {
 
-constexpr int kWaves = 8, kThreads = 64 * kWaves;
-constexpr int BN = 256;
 constexpr int kRow = 128;                       // bytes of an LDS tile row (activations; codes with MXFP4 ones)
 // Tiled form: at least 8 blocks (a lane fetches 8 scale bytes at once), and rows
 // whose 256 fit 32-bit offsets.
@@ -57,7 +56,7 @@ struct Place {
 // Tile b of the experts' tiles: experts in turn, an expert's tiles of BM
 // positions in turn, the tiles along N innermost; each XCD gets a contiguous
 // share of the tiles that there are.  False when there are fewer.
-template <int BM>
+template <int BM, int BN, int kThreads>
 __device__ bool place_grouped(const MxMatmulArgs& a, Place& p) {
     __shared__ int found[3];
     __shared__ int sums[kThreads / 64];
@@ -131,28 +130,35 @@ __device__ bool place_grouped(const MxMatmulArgs& a, Place& p) {
 }
 
 // MXX: activations in MXFP4.  DIRECT: whole slabs of bf16 activations go
-// straight to LDS (rows 16-byte aligned); otherwise through registers.
-template <bool MXX, bool DIRECT, int BM, bool GROUPED>
-__global__ void __launch_bounds__(kThreads, BM == 128 ? 4 : 1) mx_gemm_kernel(MxMatmulArgs a) {
-    constexpr int kXBytes = BM * kRow, kWBytes = BN * (MXX ? kRow : kWRow);
-    constexpr int kSBytes = MXX ? (BM + BN) * 8 : 0;
+// straight to LDS (rows 16-byte aligned); otherwise through registers.  BM x BN
+// tile of WM x WN waves; KD units (64 columns, or 256 with MXX) a slab.
+template <bool MXX, bool DIRECT, int BM, int BN, int WM, int WN, int KD, bool GROUPED>
+__global__ void __launch_bounds__(64 * WM * WN, BM * BN == 128 * 256 ? 4 : 2) mx_gemm_kernel(MxMatmulArgs a) {
+    constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+    constexpr int kUnit = MXX ? 256 : 64, kSlab = KD * kUnit;
+    constexpr int kXUnit = BM * kRow, kWUnit = BN * (MXX ? kRow : kWRow);   // bytes of a unit
+    constexpr int kXBytes = KD * kXUnit, kWBytes = KD * kWUnit;
+    constexpr int kSRow = 8 * KD, kSBytes = MXX ? (BM + BN) * kSRow : 0;
     constexpr int kStage = kXBytes + kWBytes + kSBytes;
-    constexpr int kSlab = MXX ? 256 : 64;       // columns of a slab
     constexpr int TR = MXX ? 16 : 32;           // rows of a matrix instruction's tile
-    constexpr int MT = BM / 2 / TR, NT = BN / 4 / TR;   // tiles of a wave
+    constexpr int MT = BM / WM / TR, NT = BN / WN / TR; // tiles of a wave
     constexpr int HT = MXX ? MT / 2 : MT;       // tiles along M of a step
     constexpr int kXLoads = kXBytes / 1024 / kWaves, kWLoads = kWBytes / 1024 / kWaves;
+    constexpr bool kOneWave = kWaves <= 4 && 2 * (2 * kStage + (GROUPED ? 256 : 0)) > 160 * 1024;   // a SIMD
+    static_assert(kXLoads * 1024 * kWaves == kXBytes && kWLoads * 1024 * kWaves == kWBytes, "whole loads");
+    static_assert(kXUnit % 1024 == 0 && kWUnit % 1024 == 0 && kXLoads % KD == 0, "a load stays in a unit");
+    static_assert(!MXX || BM + BN <= kThreads, "a thread for each row's scales");
     __shared__ __attribute__((aligned(1024))) uint8_t stage0[kStage];
     __shared__ __attribute__((aligned(1024))) uint8_t stage1[kStage];
 
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = readfirstlane(tid >> 6);
     const int r = lane % TR, g = lane / TR;
-    const int wm = wave >> 2, wn = wave & 3;
+    const int wm = wave / WN, wn = wave % WN;
     const int64_t nb = (a.K + 31) / 32;
 
     Place p;
     if (GROUPED) {
-        if (!place_grouped<BM>(a, p)) return;
+        if (!place_grouped<BM, BN, kThreads>(a, p)) return;
     } else {
         // groups of 8 tiles along M share the rows of W; each XCD takes a contiguous range
         const int64_t mt = (a.M + BM - 1) / BM, nt = (a.N + BN - 1) / BN;
@@ -177,38 +183,47 @@ __global__ void __launch_bounds__(kThreads, BM == 128 ? 4 : 1) mx_gemm_kernel(Mx
     };
     auto w_row = [&](int i) { return i < n_rows ? i : n_rows - 1; };
 
-    // Loads to LDS: wave w fills 1024 bytes at a time; lane l brings the chunk
-    // whose slot is l % 8 of row l / 8 (or, of W's 32-byte rows, half l % 2 of row l / 2).
+    // Loads to LDS fill 1024 bytes at a time: eight rows of 128 bytes, lane l the
+    // chunk whose slot is l % 8 of row l / 8 (or 32 of W's 32-byte rows, lane l half
+    // l % 2 of row l / 2).  Load j of wave w is row group (w kXLoads + j) of all of
+    // the slab's units; a wave's row groups repeat from unit to unit.
     const int x_sub = lane >> 3;
-    auto x_chunk = [&](int j) { return (lane & 7) ^ swizzle((wave * kXLoads + j) * 8 + x_sub); };
+    constexpr int kXGroups = kXUnit / 1024, kWGroups = kWUnit / 1024;
+    auto x_group = [&](int j) { return wave + (j % (kXLoads / KD)) * kWaves; };         // of kXGroups
+    auto x_unit = [&](int j) { return j / (kXLoads / KD); };
+    auto x_chunk = [&](int j) { return (lane & 7) ^ swizzle(x_group(j) * 8 + x_sub); };
+    // W's groups are dealt over the whole slab (a unit may have fewer than there are waves)
+    auto w_all = [&](int j) { return wave + j * kWaves; };
+    auto w_group = [&](int j) { return w_all(j) % kWGroups; };
+    auto w_unit = [&](int j) { return w_all(j) / kWGroups; };
+    auto w_chunk = [&](int j) { return MXX ? (lane & 7) ^ swizzle(w_group(j) * 8 + x_sub) : lane & 1; };
     // Offsets from the tile's first row fit 32 bits (mx_gemm_takes); the rows of a list have 64.
     typedef typename std::conditional<GROUPED, int64_t, uint32_t>::type XOffset;
     const uint8_t* const xbase = MXX ? a.x_codes + p.m0 * nb * 16 : (const uint8_t*)(a.x + (GROUPED ? 0 : p.m0) * a.ldx);
     const int64_t xrow_bytes = MXX ? nb * 16 : a.ldx * 2;
-    XOffset xsrc[kXLoads];
+    XOffset xsrc[kXLoads / KD];
 #pragma unroll
-    for (int j = 0; j < kXLoads; ++j)
-        xsrc[j] = (XOffset)(x_row((wave * kXLoads + j) * 8 + x_sub) * xrow_bytes) + (XOffset)(x_chunk(j) * 16);
-    auto w_chunk = [&](int j) { return MXX ? (lane & 7) ^ swizzle((wave * kWLoads + j) * 8 + x_sub) : lane & 1; };
+    for (int j = 0; j < kXLoads / KD; ++j)
+        xsrc[j] = lane_offset((XOffset)x_row(x_group(j) * 8 + x_sub) * (XOffset)xrow_bytes + (XOffset)(x_chunk(j) * 16));
     const uint8_t* const wbase = a.codes + (p.expert * a.N + p.n0) * nb * 16;
     uint32_t wsrc[kWLoads];
 #pragma unroll
     for (int j = 0; j < kWLoads; ++j) {
-        const int row = MXX ? (wave * kWLoads + j) * 8 + x_sub : (wave * kWLoads + j) * 32 + (lane >> 1);
-        wsrc[j] = (uint32_t)(w_row(row) * (int)nb * 16 + w_chunk(j) * 16);
+        const int row = MXX ? w_group(j) * 8 + x_sub : w_group(j) * 32 + (lane >> 1);
+        wsrc[j] = lane_offset((uint32_t)w_row(row) * ((uint32_t)nb * 16u) + (uint32_t)(w_chunk(j) * 16 + w_unit(j) * (kUnit / 2)));
     }
-    // Scales.  MXX: thread tid stages the eight bytes a slab of one row of W (the
-    // first 256 threads) or x.  Otherwise lane (r, g) keeps eight bytes, the scales of four
-    // slabs, of each of its rows of W.
+    // Scales.  MXX: thread tid stages a slab's bytes of one row of W (the first BN
+    // threads) or x.  Otherwise lane (r, g) keeps eight bytes, the scales of four
+    // units, of each of its rows of W.
     const uint8_t* const wscales = a.scales + (p.expert * a.N + p.n0) * nb;
     const uint8_t* const xscales = MXX ? a.x_scales + p.m0 * nb : nullptr;
     uint32_t ssrc[NT];
-    const bool stages_w = wave < kWaves / 2;
+    const bool stages_w = wave < BN / 64;
     if (MXX) {
-        ssrc[0] = (uint32_t)((stages_w ? w_row(tid) : x_row(tid & (BM - 1))) * nb);
+        ssrc[0] = lane_offset((uint32_t)(stages_w ? w_row(tid) : (int)x_row((tid - BN) & (BM - 1))) * (uint32_t)nb);
     } else {
 #pragma unroll
-        for (int i = 0; i < NT; ++i) ssrc[i] = (uint32_t)(w_row(wn * (BN / 4) + TR * i + r) * (int)nb);
+        for (int i = 0; i < NT; ++i) ssrc[i] = lane_offset((uint32_t)w_row(wn * (BN / WN) + TR * i + r) * (uint32_t)nb);
     }
 
     typedef typename std::conditional<MXX, f32x4, f32x16>::type Acc;
@@ -220,61 +235,72 @@ __global__ void __launch_bounds__(kThreads, BM == 128 ? 4 : 1) mx_gemm_kernel(Mx
 
     // ---- a slab on its way to LDS
     u32x4 xr[kXLoads];                          // activations on the way through registers (!DIRECT)
+    auto x_lds = [&](int j) { return x_unit(j) * kXUnit + x_group(j) * 1024; };
+    auto w_lds = [&](int j) { return kXBytes + w_all(j) * 1024; };
     auto store_x = [&](uint8_t* st) {
 #pragma unroll
-        for (int j = 0; j < kXLoads; ++j) *(u32x4*)(st + (wave * kXLoads + j) * 1024 + lane * 16) = xr[j];
+        for (int j = 0; j < kXLoads; ++j) *(u32x4*)(st + x_lds(j) + lane * 16) = xr[j];
     };
-    uint64_t sreg = 0u;                         // MXX: scales on their way
+    uint64_t sreg[KD];                          // MXX: scales on their way
     auto start = [&](uint8_t* st, int64_t t) {  // slab t, a whole one
-        if (MXX)
-            sreg = *(const __attribute__((address_space(1))) u64u*)(scalar_base((stages_w ? wscales : xscales) + t * 8) +
-                                                                    lane_offset(ssrc[0]));
-        const GlobalBytes xb = scalar_base(xbase + t * kRow);
-        const GlobalBytes wb = scalar_base(wbase + t * (MXX ? kRow : kWRow));
+        if (MXX) {
+            const GlobalBytes sb = scalar_base((stages_w ? wscales : xscales) + t * kSRow);
+#pragma unroll
+            for (int k = 0; k < KD; ++k)
+                sreg[k] = *(const __attribute__((address_space(1))) u64u*)(sb + lane_offset(ssrc[0]) + 8 * k);
+        }
+        const GlobalBytes xb = scalar_base(xbase + t * (KD * kRow));
+        const GlobalBytes wb = scalar_base(wbase + t * (kSlab / 2));
 #pragma unroll
         for (int j = 0; j < kXLoads; ++j) {
-            if (DIRECT) load_lds16(xb + lane_offset(xsrc[j]), st + (wave * kXLoads + j) * 1024);
-            else xr[j] = *(const __attribute__((address_space(1))) u32x4h*)(xb + lane_offset(xsrc[j]));
+            const GlobalBytes from = xb + lane_offset(xsrc[j % (kXLoads / KD)]) + x_unit(j) * kRow;
+            if (DIRECT) load_lds16(from, st + x_lds(j));
+            else xr[j] = *(const __attribute__((address_space(1))) u32x4h*)from;
         }
 #pragma unroll
-        for (int j = 0; j < kWLoads; ++j) load_lds16(wb + lane_offset(wsrc[j]), st + kXBytes + (wave * kWLoads + j) * 1024);
+        for (int j = 0; j < kWLoads; ++j) load_lds16(wb + lane_offset(wsrc[j]), st + w_lds(j));
     };
     auto finish = [&](uint8_t* st) {            // what came to registers
-        if (MXX && tid < BM + BN) *(uint64_t*)(st + kXBytes + kWBytes + tid * 8) = sreg;
+        if (MXX && tid < BM + BN) {
+#pragma unroll
+            for (int k = 0; k < KD; ++k) *(uint64_t*)(st + kXBytes + kWBytes + tid * kSRow + 8 * k) = sreg[k];
+        }
         if (!DIRECT) store_x(st);
     };
-    uint64_t sc[NT], sc_next[NT];               // bf16 activations: scales of the slabs at hand
-    auto fetch_scales = [&](int64_t t) {        // of slabs t .. t + 3, as far as there are any: the last eight
-        const int64_t b = 2 * t < nb - 8 ? 2 * t : nb - 8;
+    uint64_t sc[NT], sc_next[NT];               // bf16 activations: scales of the units at hand
+    auto fetch_scales = [&](int64_t q) {        // of units q .. q + 3, as far as there are any: the last eight
+        const int64_t b = 2 * q < nb - 8 ? 2 * q : nb - 8;
         const GlobalBytes sb = scalar_base(wscales + b);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) sc_next[i] = *(const __attribute__((address_space(1))) u64u*)(sb + lane_offset(ssrc[i]));
+        for (int i = 0; i < NT; ++i)
+            sc_next[i] = *(const __attribute__((address_space(1))) u64u*)(sb + lane_offset(ssrc[i]));
     };
-    auto take_scales = [&](int64_t t) {
-        const int64_t b = 2 * t < nb - 8 ? 2 * t : nb - 8;
+    auto take_scales = [&](int64_t q) {
+        const int64_t b = 2 * q < nb - 8 ? 2 * q : nb - 8;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) sc[i] = sc_next[i] >> (8 * (int)(2 * t - b));
+        for (int i = 0; i < NT; ++i) sc[i] = sc_next[i] >> (8 * (int)(2 * q - b));
+        if (2 * q + 8 < nb) fetch_scales(q + 4);
     };
 
-    // ---- fragments: step s (of four) of a slab from LDS to registers, then
+    // ---- fragments: step s (of four) of a unit from LDS to registers, then
     // multiplied.  bf16 activations: 16 columns a step.  MXX: 128 columns, of
     // half of the wave's tokens (fewer fragments at a time: 256 registers hold
     // them beside 128 accumulators).
-    u32x4 wf[2][NT], xf[2][HT];                 // bf16 activations: wf[0] is a slab's codes
+    u32x4 wf[2][NT], xf[2][HT];                 // bf16 activations: wf[0] is a unit's codes
     u32x4 wc[NT];                               // bf16 activations: the codes at hand
     u32x2 sw_raw[NT], sx_raw[MT];
     int sw[NT], sx[MT];
-    auto read = [&](const uint8_t* st, int s) {
-        const uint8_t* const xt = st + wm * (BM / 2) * kRow;
-        const uint8_t* const wt = st + kXBytes + wn * (BN / 4) * (MXX ? kRow : kWRow);
+    auto read = [&](const uint8_t* st, int k, int s) {
+        const uint8_t* const xt = st + k * kXUnit + wm * (BM / WM) * kRow;
+        const uint8_t* const wt = st + kXBytes + k * kWUnit + wn * (BN / WN) * (MXX ? kRow : kWRow);
         const int at = r * kRow + (((MXX ? 4 * (s >> 1) + g : 4 * g + s) ^ swizzle(r)) << 4);
         if (MXX && s == 0) {
-            const uint8_t* const ws = st + kXBytes + kWBytes + wn * (BN / 4) * 8;
-            const uint8_t* const xs = st + kXBytes + kWBytes + BN * 8 + wm * (BM / 2) * 8;
+            const uint8_t* const ws = st + kXBytes + kWBytes + wn * (BN / WN) * kSRow + 8 * k;
+            const uint8_t* const xs = st + kXBytes + kWBytes + (BN + wm * (BM / WM)) * kSRow + 8 * k;
 #pragma unroll
-            for (int i = 0; i < NT; ++i) sw_raw[i] = *(const u32x2*)(ws + (TR * i + r) * 8);
+            for (int i = 0; i < NT; ++i) sw_raw[i] = *(const u32x2*)(ws + (TR * i + r) * kSRow);
 #pragma unroll
-            for (int j = 0; j < MT; ++j) sx_raw[j] = *(const u32x2*)(xs + (TR * j + r) * 8);
+            for (int j = 0; j < MT; ++j) sx_raw[j] = *(const u32x2*)(xs + (TR * j + r) * kSRow);
         }
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
@@ -289,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, BM == 128 ? 4 : 1) mx_gemm_kernel(Mx
         constexpr int s = decltype(step)::value;
         if constexpr (MXX) {
             if (s == 0) {
-                // bytes g and 4 + g of a row's eight scales: this lane's blocks of the two halves of a slab
+                // bytes g and 4 + g of a row's eight scales: this lane's blocks of the two halves of a unit
                 const uint32_t sel = 0x0c0c0400u + 0x0101u * (uint32_t)g;
 #pragma unroll
                 for (int i = 0; i < NT; ++i) sw[i] = (int)perm_b32(sw_raw[i].y, sw_raw[i].x, sel);
@@ -319,15 +345,13 @@ __global__ void __launch_bounds__(kThreads, BM == 128 ? 4 : 1) mx_gemm_kernel(Mx
                     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[i], __builtin_bit_cast(bf16x8, xf[s & 1][j]),
                                                                         acc[i][j], 0, 0, 0);
         }
-    };
-    // Keep step s where it is: without this its matrix instructions, which touch
-    // no memory, may be put behind the reads of later steps, whose fragments then
-    // are all held at once.
-    auto hold = [&](int s) {
+        // Keep the step where it is: without this its matrix instructions, which
+        // touch no memory, may be put behind the reads of later steps, whose
+        // fragments then are all held at once.
 #pragma unroll
         for (int j = 0; j < HT; ++j)
 #pragma unroll
-            for (int i = 0; i < NT; ++i) asm volatile("" : "+v"(acc[i][(MXX ? (s & 1) * HT : 0) + j]));
+            for (int i = 0; i < NT; ++i) hold_acc<kOneWave>(acc[i][(MXX ? (s & 1) * HT : 0) + j]);
         asm volatile("" ::: "memory");
     };
     typedef std::integral_constant<int, 0> S0;
@@ -335,82 +359,90 @@ __global__ void __launch_bounds__(kThreads, BM == 128 ? 4 : 1) mx_gemm_kernel(Mx
     typedef std::integral_constant<int, 2> S2;
     typedef std::integral_constant<int, 3> S3;
 
-    // Slab t in `cur`: its step 0 is in registers.  Step s + 1 is read while step
-    // s multiplies.  Before step 3 every wave has read `cur`, and slab t + 1 has
-    // landed in `other`: while step 3 multiplies, slab t + 2 starts into `cur`
-    // and step 0 of slab t + 1 is read.
-    const int64_t full = a.K / kSlab, slabs = (a.K + kSlab - 1) / kSlab;
+    // Slab t in `cur`: its first step is in registers.  A step is read while the
+    // one before multiplies.  Before the last step every wave has read `cur`, and
+    // slab t + 1 has landed in `other` (what of it came to registers is stored
+    // there): while the last step multiplies, slab t + 2 starts into `cur` and the
+    // first step of slab t + 1 is read.
+    const int64_t full = a.K / kSlab;
     auto slab = [&](uint8_t* cur, uint8_t* other, int64_t t) {
-        if (!MXX && t % 4 == 0) {
-            take_scales(t);
-            if (t + 4 < slabs) fetch_scales(t + 4);
+#pragma unroll
+        for (int k = 0; k < KD; ++k) {
+            if (!MXX && (KD % 4 == 0 ? k % 4 == 0 : (t * KD + k) % 4 == 0)) take_scales(t * KD + k);
+            read(cur, k, 1);
+            multiply(S0());
+            read(cur, k, 2);
+            multiply(S1());
+            read(cur, k, 3);
+            multiply(S2());
+            if (k + 1 < KD) {
+                read(cur, k + 1, 0);
+                multiply(S3());
+            }
         }
-        read(cur, 1);
-        multiply(S0());
-        hold(0);
-        read(cur, 2);
-        multiply(S1());
-        hold(1);
-        read(cur, 3);
-        multiply(S2());
-        hold(2);
         if (t + 1 < full) finish(other);
-        wait_and_meet();
+        wait_loads<0>();
+        lds_barrier();
         if (t + 2 < full) start(cur, t + 2);
-        if (t + 1 < full) read(other, 0);
+        if (t + 1 < full) read(other, 0, 0);
         multiply(S3());
-        hold(3);
     };
 
     if (!MXX) fetch_scales(0);
     if (full > 0) {
         start(stage0, 0);
         finish(stage0);
-        wait_and_meet();
+        wait_loads<0>();
+        lds_barrier();
         if (full > 1) start(stage1, 1);
-        read(stage0, 0);
+        read(stage0, 0, 0);
         for (int64_t t = 0; t < full; t += 2) {
             slab(stage0, stage1, t);
             if (t + 1 < full) slab(stage1, stage0, t + 1);
         }
     }
-    if (full < slabs) {
-        // The slab that ends past K: activations through registers, zeros past
-        // K; W's chunks past its last block repeat it (their products are 0).
-        wait_and_meet();
+    const int64_t rest = (nb * 32 - full * kSlab + kUnit - 1) / kUnit;     // units that are left, the last one maybe cut
+    if (rest > 0) {
+        // The slab that ends past K: activations through registers, zeros past K;
+        // W's chunks past its last block repeat it (their products are 0).
+        lds_barrier();
 #pragma unroll
         for (int j = 0; j < kXLoads; ++j) {
+            const int64_t u = full * KD + x_unit(j);
+            const uint8_t* const row = xbase + lane_offset(xsrc[j % (kXLoads / KD)]) - x_chunk(j) * 16;
             if (MXX) {
                 xr[j] = (u32x4){0u, 0u, 0u, 0u};
-                if (full * 8 + x_chunk(j) < nb) xr[j] = *(const u32x4*)(xbase + full * kRow + xsrc[j]);
+                if (u * 8 + x_chunk(j) < nb) xr[j] = *(const u32x4*)(row + (u * 8 + x_chunk(j)) * 16);
             } else {
-                const int64_t k = full * 64 + x_chunk(j) * 8;
-                xr[j] = load_x8((const uint16_t*)(xbase + xsrc[j] - x_chunk(j) * 16), k, a.K);
+                xr[j] = load_x8((const uint16_t*)row, u * 64 + x_chunk(j) * 8, a.K);
             }
         }
         store_x(stage0);
 #pragma unroll
         for (int j = 0; j < kWLoads; ++j) {
-            const int64_t c = w_chunk(j), b = full * (kSlab / 32) + c;
-            load_lds16((GlobalBytes)(wbase + wsrc[j] + ((b < nb ? b : nb - 1) - c) * 16),
-                       stage0 + kXBytes + (wave * kWLoads + j) * 1024);
+            const int64_t c = w_unit(j) * (kUnit / 32) + w_chunk(j), b = full * (kSlab / 32) + c;
+            load_lds16((GlobalBytes)(wbase + lane_offset(wsrc[j]) + ((b < nb ? b : nb - 1) - c) * 16), stage0 + w_lds(j));
         }
-        if (MXX) {
-            if (tid < BM + BN)
-                *(uint64_t*)(stage0 + kXBytes + kWBytes + tid * 8) =
-                    scales8((stages_w ? wscales : xscales) + ssrc[0], full * 8, nb);
-        } else if (full % 4 == 0) {
-            take_scales(full);
+        if (MXX && tid < BM + BN) {
+#pragma unroll
+            for (int k = 0; k < KD; ++k)
+                *(uint64_t*)(stage0 + kXBytes + kWBytes + tid * kSRow + 8 * k) =
+                    scales8((stages_w ? wscales : xscales) + ssrc[0], (full * KD + k) * 8, nb);
         }
-        wait_and_meet();
-        read(stage0, 0);
-        read(stage0, 1);
-        multiply(S0());
-        read(stage0, 2);
-        multiply(S1());
-        read(stage0, 3);
-        multiply(S2());
-        multiply(S3());
+        wait_loads<0>();
+        lds_barrier();
+#pragma unroll 1
+        for (int k = 0; k < (int)rest; ++k) {
+            if (!MXX && (full * KD + k) % 4 == 0) take_scales(full * KD + k);
+            read(stage0, k, 0);
+            read(stage0, k, 1);
+            multiply(S0());
+            read(stage0, k, 2);
+            multiply(S1());
+            read(stage0, k, 3);
+            multiply(S2());
+            multiply(S3());
+        }
     }
 
     // lane (r, g) of tile (i, j): token TR j + r, four n from TR i + 8 q + 4 g for
@@ -419,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, BM == 128 ? 4 : 1) mx_gemm_kernel(Mx
     const bool quads = a.N % 4 == 0 && ((uintptr_t)a.y & 15) == 0;
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
-        const int64_t m = p.m0 + wm * (BM / 2) + TR * j + r;
+        const int64_t m = p.m0 + wm * (BM / WM) + TR * j + r;
         if (m >= p.m_end) continue;
         int64_t out = m;
         if (GROUPED) {
@@ -430,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, BM == 128 ? 4 : 1) mx_gemm_kernel(Mx
         for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int q = 0; q < TR * TR / 256; ++q) {
-                const int col = wn * (BN / 4) + TR * i + 8 * q + 4 * g;
+                const int col = wn * (BN / WN) + TR * i + 8 * q + 4 * g;
                 if (col >= n_left) continue;
                 f32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
                 if (a.bias) {
@@ -475,21 +507,30 @@ __global__ void __launch_bounds__(256) nan_rows_kernel(MxMatmulArgs a) {
     }
 }
 
-template <bool MXX, bool DIRECT, int BM, bool GROUPED>
+template <bool MXX, bool DIRECT, int BM, int BN, int WM, int WN, int KD, bool GROUPED>
 hipError_t launch(const MxMatmulArgs& a, hipStream_t s) {
+    constexpr int kThreads = 64 * WM * WN;
     const int64_t nt = (a.N + BN - 1) / BN;
     int64_t blocks = (a.M + BM - 1) / BM * nt;
     if (GROUPED) {
         // whole shares of the 8 XCDs: the largest share has a tile more than an eighth
-        const int64_t tiles = (a.M * a.top_k / BM + (a.n_experts < a.M * a.top_k ? a.n_experts : a.M * a.top_k)) * nt;
+        const int64_t slots = a.M * a.top_k;
+        const int64_t tiles = (slots / BM + (a.n_experts < slots ? a.n_experts : slots)) * nt;
         blocks = (tiles / 8 + 1) * 8;
     }
     if (!grid_fits(blocks, kThreads)) return hipErrorInvalidConfiguration;
-    mx_gemm_kernel<MXX, DIRECT, BM, GROUPED><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+    mx_gemm_kernel<MXX, DIRECT, BM, BN, WM, WN, KD, GROUPED><<<(unsigned)blocks, kThreads, 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (!GROUPED || e != hipSuccess) return e;
     nan_rows_kernel<<<256, 256, 0, s>>>(a);
     return hipGetLastError();
+}
+
+template <int BM, int BN, int WM, int WN, int KD, bool GROUPED>
+hipError_t launch_bf16(const MxMatmulArgs& a, hipStream_t s) {
+    const bool direct = ((uintptr_t)a.x & 15) == 0 && (a.ldx % 8 == 0 || a.M == 1);
+    return direct ? launch<false, true, BM, BN, WM, WN, KD, GROUPED>(a, s)
+                  : launch<false, false, BM, BN, WM, WN, KD, GROUPED>(a, s);
 }
 
 }  // namespace
@@ -499,11 +540,32 @@ bool mx_gemm_takes(const MxMatmulArgs& a) {
            (a.x_codes || a.n_experts > 0 || a.M == 1 || a.ldx * 2 < kMaxTiledBytes);
 }
 
+// The largest tile that still gives every compute unit one (its rate is the
+// highest, 1.2 PFLOP/s with bf16 and 3.5 with MXFP4 activations, but a wave of
+// tiles costs its time whether it fills the chip or not).  us by tile:
+//   bf16    256 x 256 / 128 x 128 / 64 x 64
+//     M = 2048, 8192 x 8192   221 /  242 /  353
+//     M = 1024, 4096 x 4096    90 /   41 /   46
+//     M =  512, 4096 x 4096    89 /   37 /   26
+//     M =   64, 8192 x 8192   158 /   69 /   37
+//   MXFP4
+//     M = 2048, 8192 x 8192    79 /  108 /  176
+//     M = 1024, 4096 x 4096    38 /   21 /   26
+//     M =  512, 4096 x 4096    37 /   19 /   15
+// Experts: by the slots an expert has on average, 32 x 128 / 64 x 256 / 128 x 256
+//     (64 experts of 2048 x 4096)
+//     25   102 / 122 / 132       251   444 / 350 / 350
 hipError_t launch_mx_gemm(const MxMatmulArgs& a, hipStream_t s) {
-    if (a.x_codes) return launch<true, true, 256, false>(a, s);
-    const bool direct = ((uintptr_t)a.x & 15) == 0 && a.ldx % 8 == 0;
-    if (a.n_experts > 0) return direct ? launch<false, true, 128, true>(a, s) : launch<false, false, 128, true>(a, s);
-    return direct ? launch<false, true, 256, false>(a, s) : launch<false, false, 256, false>(a, s);
+    if (a.n_experts > 0)
+        return a.M * a.top_k < 48 * (int64_t)a.n_experts ? launch_bf16<32, 128, 1, 4, 4, true>(a, s)
+                                                         : launch_bf16<64, 256, 2, 4, 2, true>(a, s);
+    const int64_t cus = compute_unit_count();
+    auto tiles = [&](int64_t side) { return ((a.M + side - 1) / side) * ((a.N + side - 1) / side); };
+    if (4 * tiles(256) >= 3 * cus)
+        return a.x_codes ? launch<true, true, 256, 256, 2, 4, 1, false>(a, s) : launch_bf16<256, 256, 2, 4, 2, false>(a, s);
+    if (4 * tiles(128) >= 3 * cus)
+        return a.x_codes ? launch<true, true, 128, 128, 2, 2, 1, false>(a, s) : launch_bf16<128, 128, 2, 2, 2, false>(a, s);
+    return a.x_codes ? launch<true, true, 64, 64, 2, 2, 2, false>(a, s) : launch_bf16<64, 64, 2, 2, 4, false>(a, s);
 }
 
 }  // namespace dmm
