@@ -464,9 +464,10 @@ def _rows(t, name, dtypes, rows, cols, device):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if tuple(t.shape) != (rows, cols):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
-    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+    ld, step = t.stride()
+    if (cols > 1 and step != 1) or (rows > 1 and ld < cols):
         raise ValueError(f"{name}: strides {t.stride()} are not those of rows of {cols} elements")
-    return t.stride(0) if rows > 1 else cols
+    return ld if rows > 1 else cols
 
 
 def _float_dtype(t, name):
@@ -477,11 +478,22 @@ def _float_dtype(t, name):
     raise TypeError(f"{name} dtype {t.dtype} must be float32 or bfloat16")
 
 
-def _on_gpu(device, what):
-    """The device as a context: kernels are launched with it current."""
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(what, device, *args):
+    """The C entry point `what` on the device's current stream, with the device current."""
     if device.type != "cuda":
         raise ValueError(f"{what}: tensors are on {device}, not on a GPU")
-    return torch.cuda.device(device)
+    fn = getattr(_lib, what)
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if rc != TQ_OK:
+        _raise(rc, what)
 
 
 def _package(codes, scales, rows, K, device, prefix=""):
@@ -502,10 +514,7 @@ def mx_pack(W, codes, scales, status=None):
     _package(codes, scales, rows, K, dev)
     if status is not None:
         _need(status, "status", _I32, 1, dev)
-    with _on_gpu(dev, "mx_pack"):
-        rc = _lib.mx_pack(_ptr(W), wdt, rows, K, ldw, _ptr(codes), _ptr(scales), _ptr(status),
-                          _stream(dev))
-    _raise(rc, "mx_pack")
+    _call("mx_pack", dev, _at(W), wdt, rows, K, ldw, _at(codes), _at(scales), _at(status))
     return status
 
 
@@ -518,10 +527,7 @@ def mx_unpack(codes, scales, rows, K, W_out, status=None):
     _need(W_out, "W_out", (W_out.dtype,), rows * K, dev)
     if status is not None:
         _need(status, "status", _I32, 1, dev)
-    with _on_gpu(dev, "mx_unpack"):
-        rc = _lib.mx_unpack(_ptr(codes), _ptr(scales), rows, K, _ptr(W_out), odt, _ptr(status),
-                            _stream(dev))
-    _raise(rc, "mx_unpack")
+    _call("mx_unpack", dev, _at(codes), _at(scales), rows, K, _at(W_out), odt, _at(status))
     return status
 
 
@@ -536,10 +542,7 @@ def mx_matmul(x, codes, scales, N, y, bias=None):
         _need(bias, "bias", _F32, N, dev)
     _need(y, "y", (y.dtype,), M * N, dev)
     ydt = _ydtype(y)
-    with _on_gpu(dev, "mx_matmul"):
-        rc = _lib.mx_matmul(_ptr(x), M, K, ldx, _ptr(codes), _ptr(scales), N, _ptr(bias), _ptr(y),
-                            ydt, _stream(dev))
-    _raise(rc, "mx_matmul")
+    _call("mx_matmul", dev, _at(x), M, K, ldx, _at(codes), _at(scales), N, _at(bias), _at(y), ydt)
 
 
 def mx_matmul_mx(x_codes, x_scales, M, K, codes, scales, N, y, bias=None):
@@ -551,10 +554,8 @@ def mx_matmul_mx(x_codes, x_scales, M, K, codes, scales, N, y, bias=None):
         _need(bias, "bias", _F32, N, dev)
     _need(y, "y", (y.dtype,), M * N, dev)
     ydt = _ydtype(y)
-    with _on_gpu(dev, "mx_matmul_mx"):
-        rc = _lib.mx_matmul_mx(_ptr(x_codes), _ptr(x_scales), M, K, _ptr(codes), _ptr(scales), N,
-                               _ptr(bias), _ptr(y), ydt, _stream(dev))
-    _raise(rc, "mx_matmul_mx")
+    _call("mx_matmul_mx", dev, _at(x_codes), _at(x_scales), M, K, _at(codes), _at(scales), N,
+          _at(bias), _at(y), ydt)
 
 
 def moe_route_workspace_bytes(M, top_k, n_experts):
@@ -570,7 +571,7 @@ def _workspace(workspace, dev):
     if workspace is None:
         return None, 0
     _need(workspace, "workspace", _U8, workspace.numel(), dev)
-    return _ptr(workspace), workspace.numel()
+    return _at(workspace), workspace.numel()
 
 
 def moe_route(expert_ids, n_experts, counts, offsets, order, workspace=None):
@@ -584,10 +585,8 @@ def moe_route(expert_ids, n_experts, counts, offsets, order, workspace=None):
     _need(offsets, "offsets", _I32, n_experts + 1, dev)
     _need(order, "order", _I32, M * top_k, dev)
     ws, nbytes = _workspace(workspace, dev)
-    with _on_gpu(dev, "moe_route"):
-        rc = _lib.moe_route(_ptr(expert_ids), M, top_k, n_experts, _ptr(counts), _ptr(offsets),
-                            _ptr(order), ws, nbytes, _stream(dev))
-    _raise(rc, "moe_route")
+    _call("moe_route", dev, _at(expert_ids), M, top_k, n_experts, _at(counts), _at(offsets),
+          _at(order), ws, nbytes)
 
 
 def mx_matmul_experts(x, codes, scales, N, y, n_experts, offsets, order, top_k, bias=None):
@@ -603,11 +602,8 @@ def mx_matmul_experts(x, codes, scales, N, y, n_experts, offsets, order, top_k, 
     _need(order, "order", _I32, M * top_k, dev)
     _need(y, "y", (y.dtype,), M * top_k * N, dev)
     ydt = _ydtype(y)
-    with _on_gpu(dev, "mx_matmul_experts"):
-        rc = _lib.mx_matmul_experts(_ptr(x), M, K, ldx, _ptr(codes), _ptr(scales), N, n_experts,
-                                    _ptr(bias), _ptr(offsets), _ptr(order), top_k, _ptr(y), ydt,
-                                    _stream(dev))
-    _raise(rc, "mx_matmul_experts")
+    _call("mx_matmul_experts", dev, _at(x), M, K, ldx, _at(codes), _at(scales), N, n_experts,
+          _at(bias), _at(offsets), _at(order), top_k, _at(y), ydt)
 
 
 def moe_balance_workspace_bytes(M, n_experts):
@@ -633,10 +629,8 @@ def moe_balance(logits, counts, loss, weights, token_mask=None, workspace=None):
     if token_mask is not None:
         _need(token_mask, "token_mask", (torch.uint8, torch.bool), M, dev)
     ws, nbytes = _workspace(workspace, dev)
-    with _on_gpu(dev, "moe_balance"):
-        rc = _lib.moe_balance(_ptr(logits), ldt, M, E, ldl, _ptr(token_mask), _ptr(counts), _ptr(loss),
-                              _ptr(weights), ws, nbytes, _stream(dev))
-    _raise(rc, "moe_balance")
+    _call("moe_balance", dev, _at(logits), ldt, M, E, ldl, _at(token_mask), _at(counts), _at(loss),
+          _at(weights), ws, nbytes)
 
 
 def moe_balance_grad(logits, weights, dloss, dlogits, token_mask=None):
@@ -651,10 +645,8 @@ def moe_balance_grad(logits, weights, dloss, dlogits, token_mask=None):
     _need(dlogits, "dlogits", (logits.dtype,), M * E, dev)
     if token_mask is not None:
         _need(token_mask, "token_mask", (torch.uint8, torch.bool), M, dev)
-    with _on_gpu(dev, "moe_balance_grad"):
-        rc = _lib.moe_balance_grad(_ptr(logits), ldt, M, E, ldl, _ptr(token_mask), _ptr(weights),
-                                   _ptr(dloss), _ptr(dlogits), _stream(dev))
-    _raise(rc, "moe_balance_grad")
+    _call("moe_balance_grad", dev, _at(logits), ldt, M, E, ldl, _at(token_mask), _at(weights),
+          _at(dloss), _at(dlogits))
 
 
 def raw():

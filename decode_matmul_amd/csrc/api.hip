@@ -446,11 +446,11 @@ int moe_balance(const void* logits, int32_t l_dtype, int64_t M, int32_t n_expert
     const int64_t need = moe_balance_workspace_bytes(M, n_experts);
     if (need < 0 || !rows_ok(M, n_experts, ldl)) return TQ_ERR_SHAPE;
     if (!is_dtype(l_dtype)) return TQ_ERR_DTYPE;
-    if (!counts || !loss || !weights || (M > 0 && (!logits || !workspace))) return TQ_ERR_NULL;
+    if (!counts || !loss || !weights || (M > 0 && !logits) || (need > 0 && !workspace)) return TQ_ERR_NULL;
     if (!aligned(logits, bytes_of(l_dtype)) || !aligned(counts, 4) || !aligned(loss, 4) ||
         !aligned(weights, 4) || !aligned(workspace, 8))
         return TQ_ERR_ALIGN;
-    if (workspace_bytes < need) return TQ_ERR_SHAPE;
+    if (need > 0 && workspace_bytes < need) return TQ_ERR_SHAPE;
     return hip_status(dmm::launch_moe_balance(logits, l_dtype, M, n_experts, ldl, token_mask, counts, loss,
                                               weights, workspace, (hipStream_t)stream));
 }

@@ -1,6 +1,8 @@
 // The router's side of the grouped experts: moe_route (counts and lists of the
 // slots of each expert) and moe_balance / moe_balance_grad.
-#include "common.h"
+#include <type_traits>
+
+#include "mx.h"
 
 namespace dmm {
 
@@ -18,12 +20,14 @@ namespace {
 // bit of the id, and a count per (wave, expert) in LDS carries on from row to
 // row.  No place depends on the order in which anything runs.
 //
-// One chunk is one launch.  More take three: counts per chunk, their running
-// sums over the chunks, places.
+// Bound: latency.  Up to kSelfChunks chunks take one launch, in which every
+// workgroup counts all chunks for itself; more take three: counts per chunk,
+// their running sums over the chunks, places.
 constexpr int kRouteThreads = 1024;
 constexpr int kRouteWaves = kRouteThreads / 64;
 constexpr int kRows = 4;                        // rows of 64 slots a wave
 constexpr int kChunk = kRouteThreads * kRows;
+constexpr int kSelfChunks = 8;
 constexpr int kScanThreads = 256;
 static_assert(kMoeMaxExperts < kRouteThreads, "a thread for each expert and one for no expert");
 
@@ -60,17 +64,18 @@ __device__ __forceinline__ int exclusive_sum(int v, int* sums) {
     return before + inc - v;
 }
 
-// SINGLE: the only chunk.  Otherwise `before` [chunks + 1][E + 1] holds each
-// chunk's running sums, the last row the totals.
-template <bool SINGLE>
+// SELF: this workgroup counts the other chunks itself.  Otherwise `before`
+// [chunks + 1][E + 1] holds each chunk's running sums, the last row the totals.
+template <bool SELF>
 __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const int32_t* ids, int64_t slots, int E,
                                                                     int bits, const int32_t* before,
                                                                     int64_t chunks, int32_t* counts,
                                                                     int32_t* offsets, int32_t* order) {
-    extern __shared__ int lds[];                // [kRouteWaves][E + 1] counts, then places; kRouteWaves sums
-    int* const sums = lds + kRouteWaves * (E + 1);
+    extern __shared__ int lds[];                // [kRouteWaves][E + 1] counts, then places; two more such rows; sums
+    int* const rest = lds + kRouteWaves * (E + 1);      // SELF: slots in earlier chunks, and in later ones
+    int* const sums = rest + 2 * (E + 1);
     const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6, tid = (int)threadIdx.x;
-    for (int i = tid; i < kRouteWaves * (E + 1); i += kRouteThreads) lds[i] = 0;
+    for (int i = tid; i < (kRouteWaves + 2) * (E + 1); i += kRouteThreads) lds[i] = 0;
     __syncthreads();
     const int64_t first = (int64_t)blockIdx.x * kChunk + wave * (64 * kRows) + lane;
     int id[kRows], rank[kRows];
@@ -78,6 +83,22 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const int32_
     volatile int* const mine = lds + wave * (E + 1);
 #pragma unroll
     for (int i = 0; i < kRows; ++i) id[i] = expert_of(ids, first + 64 * i, slots, E);
+    if (SELF) {
+        for (int64_t c = 0; c < chunks; ++c) {
+            if (c == (int64_t)blockIdx.x) continue;
+            int other[kRows];
+#pragma unroll
+            for (int i = 0; i < kRows; ++i)
+                other[i] = expert_of(ids, c * kChunk + wave * (64 * kRows) + lane + 64 * i, slots, E);
+            int* const row = rest + (c < (int64_t)blockIdx.x ? 0 : E + 1);
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const uint64_t same = same_id(other[i], __ballot(other[i] >= 0), bits);
+                // one lane for each expert of the row; whole numbers, so any order gives the same count
+                if (other[i] >= 0 && (same & ((1ull << lane) - 1ull)) == 0) atomicAdd(&row[other[i]], __popcll(same));
+            }
+        }
+    }
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         const uint64_t same = same_id(id[i], __ballot(id[i] >= 0), bits);
@@ -87,11 +108,13 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const int32_
         if (id[i] >= 0 && below == 0) mine[id[i]] = base + __popcll(same);
     }
     __syncthreads();
-    // thread e: the chunk's count of expert e, its total, and what earlier chunks hold
+    // thread e: the count of expert e over all chunks, and what earlier chunks hold
     int total = 0, earlier = 0;
     if (tid <= E) {
-        if (SINGLE) {
+        if (SELF) {
             for (int w = 0; w < kRouteWaves; ++w) total += lds[w * (E + 1) + tid];
+            earlier = rest[tid];
+            total += earlier + rest[E + 1 + tid];
         } else {
             total = before[chunks * (E + 1) + tid];
             earlier = before[(int64_t)blockIdx.x * (E + 1) + tid];
@@ -162,180 +185,285 @@ __global__ void __launch_bounds__(kScanThreads) route_scan_kernel(int32_t* cc, i
 
 // ---------------------------------------------------------------- balance
 //
-// loss = sum_t s_t with s_t = sum_e w_e p_te; the gradient of s_t is
-// p_te (w_e - s_t).  A wave takes a row: lane l holds logits l, l + 64, ..
-// (at most 8), so the row is read once; the maximum and the two sums are
-// exchanged over the wave.  Bound: the logits' bytes.
+// With c'_e = E c_e / n the loss is the sum over tokens of s_t / T, s_t = sum_e
+// c'_e p_te, so tokens and T are counted in one pass; w = c' / T, and the gradient
+// of s_t is p_te (w_e - s_t) with that w.  A row's E logits lie with L lanes (a
+// power of two, 64 / L rows a wave at a time), eight consecutive ones each, read
+// once; the maximum and the two sums are exchanged among the L lanes.
+// Bound: the logits' bytes, and the launches for few tokens.
 constexpr int kBalThreads = 256;
 constexpr int kBalWaves = kBalThreads / 64;
-constexpr int kWeightThreads = 1024;
-constexpr int kBalRows = 16;                    // rows a wave of the loss takes
 
-__device__ __forceinline__ float wave_max(float v) {
+template <int L>
+__device__ __forceinline__ float group_max(float v) {
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
+    for (int d = L / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
     return v;
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
+template <int L, class T>
+__device__ __forceinline__ T group_sum(T v) {
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
+    for (int d = L / 2; d > 0; d >>= 1) v += __shfl_xor(v, d);
     return v;
 }
 
-__device__ __forceinline__ double wave_sum(double v) {
+// Eight logits at p, `have` of them there; the others are -inf.
+template <bool BF16>
+__device__ __forceinline__ void load_logits(const void* base, int64_t at, int have, float* z) {
+    if (have >= 8) {
+        if (BF16) {
+            const u32x4 d = *(const u32x4h*)((const uint16_t*)base + at);
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
-    return v;
+            for (int i = 0; i < 4; ++i) {
+                z[2 * i] = __builtin_bit_cast(float, d[i] << 16);
+                z[2 * i + 1] = __builtin_bit_cast(float, d[i] & 0xffff0000u);
+            }
+        } else {
+            const f32x4 a = *(const f32x4a*)((const float*)base + at), b = *(const f32x4a*)((const float*)base + at + 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                z[i] = a[i];
+                z[4 + i] = b[i];
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        z[i] = -__builtin_inff();
+        if (i < have)
+            z[i] = BF16 ? bf16_bits_to_f32(((const uint16_t*)base)[at + i]) : ((const float*)base)[at + i];
+    }
 }
 
-// A row's softmax p (PER values a lane) and s = sum_e w_e p_e.  Rows of -inf give p = 0.
-template <bool BF16, int PER>
-__device__ __forceinline__ float row_softmax(const void* logits, int64_t at, int E, const float* w, float* p) {
-    const int lane = (int)threadIdx.x & 63;
+// A row's softmax, in place of its logits, and sum_e w_e p_e.  Rows of -inf give p = 0.
+template <int L>
+__device__ __forceinline__ float row_softmax(float* p, const float* w) {
     float top = -__builtin_inff();
     bool nan = false;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = lane + 64 * i;
-        p[i] = -__builtin_inff();
-        if (e < E)
-            p[i] = BF16 ? bf16_bits_to_f32(((const uint16_t*)logits)[at + e]) : ((const float*)logits)[at + e];
+    for (int i = 0; i < 8; ++i) {
         nan |= p[i] != p[i];
         top = fmaxf(top, p[i]);
     }
-    top = wave_max(top);
-    if (__ballot(nan) != 0ull) top = __builtin_nanf("");
-    if (top == -__builtin_inff()) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) p[i] = 0.f;
-        return 0.f;
-    }
+    if (nan) top = __builtin_inff();            // inf - inf: every p of the row becomes NaN
+    top = group_max<L>(top);
     float sum = 0.f, ws = 0.f;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
+    for (int i = 0; i < 8; ++i) {
         p[i] = expf(p[i] - top);
         sum += p[i];
         ws += w[i] * p[i];
     }
-    sum = wave_sum(sum);
-    ws = wave_sum(ws);
+    sum = group_sum<L>(sum);
+    ws = group_sum<L>(ws);
+    if (top == -__builtin_inff()) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = 0.f;
+        return 0.f;
+    }
+    if (top == __builtin_inff()) sum = __builtin_nanf("");
     const float inv = 1.f / sum;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) p[i] *= inv;
+    for (int i = 0; i < 8; ++i) p[i] *= inv;
     return ws * inv;
 }
 
-// w_e from the counts and the number of tokens that take part.
-__global__ void __launch_bounds__(kWeightThreads) balance_weights_kernel(const uint8_t* mask, int64_t M, int E,
-                                                                      const int32_t* counts, float* weights) {
-    __shared__ double part[2][kWeightThreads / 64];
-    const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    double T = 0.0, n = tid < E ? (double)counts[tid] : 0.0;
-    if (mask)
-        for (int64_t t = tid; t < M; t += kWeightThreads) T += mask[t] != 0 ? 1.0 : 0.0;
-    T = wave_sum(T);
-    n = wave_sum(n);
-    if (lane == 0) {
-        part[0][wave] = T;
-        part[1][wave] = n;
-    }
-    __syncthreads();
-    T = n = 0.0;
-    for (int w = 0; w < kWeightThreads / 64; ++w) {
-        T += part[0][w];
-        n += part[1][w];
-    }
-    if (!mask) T = (double)M;
-    if (tid < E) weights[tid] = T > 0.0 && n > 0.0 ? (float)((double)E / T * ((double)counts[tid] / n)) : 0.f;
+// loss and weights from the sum over tokens, their number, and the counts.
+__device__ __forceinline__ void finish_balance(double sum, int64_t T, double n, int E, const int32_t* counts,
+                                               float* loss, float* weights) {
+    const bool some = T > 0 && n > 0.0;
+    for (int e = (int)threadIdx.x; e < E; e += kBalThreads)
+        weights[e] = some ? (float)((double)E * ((double)counts[e] / n) / (double)T) : 0.f;
+    if (threadIdx.x == 0) loss[0] = some ? (float)(sum / (double)T) : 0.f;
 }
 
-template <bool BF16, int PER>
+// A workgroup's tokens: `rows` from blockIdx.x * rows on.  partial [blocks][2]:
+// their sum and how many take part; the only workgroup finishes by itself.
+template <bool BF16, int L>
 __global__ void __launch_bounds__(kBalThreads) balance_loss_kernel(const void* logits, int64_t M, int E, int64_t ldl,
-                                                                   const uint8_t* mask, const float* weights,
+                                                                   const uint8_t* mask, const int32_t* counts,
+                                                                   int rows, float* loss, float* weights,
                                                                    double* partial) {
-    __shared__ double part[kBalWaves];
+    __shared__ double part[3][kBalWaves];
     const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
-    float w[PER], p[PER];
+    const int e0 = (lane % L) * 8, have = E - e0;
+    double n = 0.0;
+    for (int e = (int)threadIdx.x; e < E; e += kBalThreads) n += (double)counts[e];
+    n = group_sum<64>(n);
+    if (lane == 0) part[2][wave] = n;
+    __syncthreads();
+    n = 0.0;
+    for (int i = 0; i < kBalWaves; ++i) n += part[2][i];
+    float w[8], p[8];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) w[i] = lane + 64 * i < E ? weights[lane + 64 * i] : 0.f;
-    double sum = 0.0;
-    const int64_t t0 = ((int64_t)blockIdx.x * kBalWaves + wave) * kBalRows;
-    for (int i = 0; i < kBalRows; ++i) {
+    for (int i = 0; i < 8; ++i) w[i] = i < have && n > 0.0 ? (float)((double)E * ((double)counts[e0 + i] / n)) : 0.f;
+    double sum = 0.0, tokens = 0.0;
+    const int64_t t0 = (int64_t)blockIdx.x * rows;
+    for (int i = wave * (64 / L) + lane / L; i < rows; i += kBalThreads / L) {
         const int64_t t = t0 + i;
         if (t >= M || (mask && mask[t] == 0)) continue;
-        sum += (double)row_softmax<BF16, PER>(logits, t * ldl, E, w, p);
+        load_logits<BF16>(logits, t * ldl + e0, have, p);
+        const float s = row_softmax<L>(p, w);
+        if (lane % L == 0) {
+            sum += (double)s;
+            tokens += 1.0;
+        }
     }
-    if (lane == 0) part[wave] = sum;
+    sum = group_sum<64>(sum);
+    tokens = group_sum<64>(tokens);
+    if (lane == 0) {
+        part[0][wave] = sum;
+        part[1][wave] = tokens;
+    }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        double s = 0.0;
-        for (int i = 0; i < kBalWaves; ++i) s += part[i];
-        partial[blockIdx.x] = s;
+    sum = tokens = 0.0;
+    for (int i = 0; i < kBalWaves; ++i) {
+        sum += part[0][i];
+        tokens += part[1][i];
+    }
+    if (gridDim.x == 1) {
+        finish_balance(sum, (int64_t)tokens, n, E, counts, loss, weights);
+    } else if (threadIdx.x == 0) {
+        partial[2 * (int64_t)blockIdx.x] = sum;
+        partial[2 * (int64_t)blockIdx.x + 1] = tokens;
     }
 }
 
-__global__ void __launch_bounds__(kBalThreads) balance_sum_kernel(const double* partial, int64_t n, float* loss) {
-    __shared__ double part[kBalWaves];
-    double s = 0.0;
-    for (int64_t i = threadIdx.x; i < n; i += kBalThreads) s += partial[i];
-    s = wave_sum(s);
-    if (((int)threadIdx.x & 63) == 0) part[(int)threadIdx.x >> 6] = s;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        s = 0.0;
-        for (int i = 0; i < kBalWaves; ++i) s += part[i];
-        loss[0] = (float)s;
+__global__ void __launch_bounds__(kBalThreads) balance_finish_kernel(const double* partial, int64_t blocks, int E,
+                                                                     const int32_t* counts, float* loss,
+                                                                     float* weights) {
+    __shared__ double part[3][kBalWaves];
+    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+    double v[3] = {0.0, 0.0, 0.0};
+    for (int64_t i = threadIdx.x; i < blocks; i += kBalThreads) {
+        v[0] += partial[2 * i];
+        v[1] += partial[2 * i + 1];
     }
+    for (int e = (int)threadIdx.x; e < E; e += kBalThreads) v[2] += (double)counts[e];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        v[k] = group_sum<64>(v[k]);
+        if (lane == 0) part[k][wave] = v[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        v[k] = 0.0;
+        for (int i = 0; i < kBalWaves; ++i) v[k] += part[k][i];
+    }
+    finish_balance(v[0], (int64_t)v[1], v[2], E, counts, loss, weights);
 }
 
-template <bool BF16, int PER>
+template <bool BF16, int L>
 __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const void* logits, int64_t M, int E, int64_t ldl,
                                                                    const uint8_t* mask, const float* weights,
                                                                    const float* dloss, void* dlogits) {
-    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
-    const int64_t t = (int64_t)blockIdx.x * kBalWaves + wave;
+    const int lane = (int)threadIdx.x & 63;
+    const int64_t t = ((int64_t)blockIdx.x * kBalThreads + threadIdx.x) / L;
+    const int e0 = (lane % L) * 8, have = E - e0;
     if (t >= M) return;
-    float w[PER], p[PER];
+    float w[8], p[8], s = 0.f, up = 0.f;
+    const bool live = !mask || mask[t] != 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        w[i] = lane + 64 * i < E ? weights[lane + 64 * i] : 0.f;
+    for (int i = 0; i < 8; ++i) {
+        w[i] = i < have ? weights[e0 + i] : 0.f;
         p[i] = 0.f;
     }
-    float s = 0.f, up = 0.f;
-    if (!mask || mask[t] != 0) {
-        s = row_softmax<BF16, PER>(logits, t * ldl, E, w, p);
+    if (live) {
+        load_logits<BF16>(logits, t * ldl + e0, have, p);
+        s = row_softmax<L>(p, w);
         up = dloss[0];
     }
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = lane + 64 * i;
-        if (e >= E) continue;
-        const float d = up * p[i] * (w[i] - s);
-        if (BF16) ((uint16_t*)dlogits)[t * E + e] = f32_to_bf16_rne(d);
-        else ((float*)dlogits)[t * E + e] = d;
+    for (int i = 0; i < 8; ++i) p[i] = live ? up * p[i] * (w[i] - s) : 0.f;
+    const int64_t at = t * E + e0;
+    if (BF16) {
+        uint16_t* const d = (uint16_t*)dlogits + at;
+        if (have >= 8) {
+            u32x4 v;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = (uint32_t)f32_to_bf16_rne(p[2 * i]) | (uint32_t)f32_to_bf16_rne(p[2 * i + 1]) << 16;
+            *(u32x4h*)d = v;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < have) d[i] = f32_to_bf16_rne(p[i]);
+        }
+    } else {
+        float* const d = (float*)dlogits + at;
+        if (have >= 8) {
+            *(f32x4a*)d = (f32x4){p[0], p[1], p[2], p[3]};
+            *(f32x4a*)(d + 4) = (f32x4){p[4], p[5], p[6], p[7]};
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < have) d[i] = p[i];
+        }
     }
 }
 
 int64_t route_chunks(int64_t slots) { return (slots + kChunk - 1) / kChunk; }
 
-int64_t loss_blocks(int64_t M) { return (M + kBalWaves * kBalRows - 1) / (kBalWaves * kBalRows); }
+// Tokens of a workgroup of the loss: few enough to fill the chip, and enough to
+// keep the partial sums few.
+int loss_rows(int64_t M) { return M <= 64 * 256 ? 64 : 256; }
+
+int64_t loss_blocks(int64_t M) { return M == 0 ? 1 : (M + loss_rows(M) - 1) / loss_rows(M); }
+
+template <bool BF16, int L>
+hipError_t balance(const void* logits, int64_t M, int E, int64_t ldl, const uint8_t* mask, const int32_t* counts,
+                   float* loss, float* weights, double* partial, hipStream_t s) {
+    const int64_t blocks = loss_blocks(M);
+    balance_loss_kernel<BF16, L><<<(unsigned)blocks, kBalThreads, 0, s>>>(logits, M, E, ldl, mask, counts, loss_rows(M),
+                                                                         loss, weights, partial);
+    hipError_t e = hipGetLastError();
+    if (blocks == 1 || e != hipSuccess) return e;
+    balance_finish_kernel<<<1, kBalThreads, 0, s>>>(partial, blocks, E, counts, loss, weights);
+    return hipGetLastError();
+}
+
+template <bool BF16, int L>
+hipError_t grad(const void* logits, int64_t M, int E, int64_t ldl, const uint8_t* mask, const float* weights,
+                const float* dloss, void* dlogits, hipStream_t s) {
+    const int64_t blocks = (M * L + kBalThreads - 1) / kBalThreads;
+    if (!grid_fits(blocks, kBalThreads)) return hipErrorInvalidConfiguration;
+    balance_grad_kernel<BF16, L><<<(unsigned)blocks, kBalThreads, 0, s>>>(logits, M, E, ldl, mask, weights, dloss,
+                                                                         dlogits);
+    return hipGetLastError();
+}
+
+// f(integral constant L) for the lanes a row of E logits takes.
+template <class F>
+hipError_t with_lanes(int E, F f) {
+    if (E <= 8) return f(std::integral_constant<int, 1>());
+    if (E <= 16) return f(std::integral_constant<int, 2>());
+    if (E <= 32) return f(std::integral_constant<int, 4>());
+    if (E <= 64) return f(std::integral_constant<int, 8>());
+    if (E <= 128) return f(std::integral_constant<int, 16>());
+    if (E <= 256) return f(std::integral_constant<int, 32>());
+    return f(std::integral_constant<int, 64>());
+}
+static_assert(kMoeMaxExperts <= 64 * 8, "a row fits a wave");
 
 }  // namespace
 
 int64_t moe_route_ws_bytes(int64_t slots, int E) {
     const int64_t chunks = route_chunks(slots);
-    return chunks <= 1 ? 0 : (chunks + 1) * (E + 1) * 4;
+    return chunks <= kSelfChunks ? 0 : (chunks + 1) * (E + 1) * 4;
 }
 
 hipError_t launch_moe_route(const int32_t* ids, int64_t slots, int E, int32_t* counts, int32_t* offsets,
                             int32_t* order, void* workspace, hipStream_t s) {
     const int64_t chunks = route_chunks(slots);
     const int bits = 32 - __builtin_clz((unsigned)E);
-    const size_t lds = (size_t)(kRouteWaves * (E + 1) + kRouteWaves) * 4;
-    if (chunks <= 1) {
-        route_place_kernel<true><<<1, kRouteThreads, lds, s>>>(ids, slots, E, bits, nullptr, 1, counts, offsets,
-                                                              order);
+    const size_t lds = (size_t)((kRouteWaves + 2) * (E + 1) + kRouteWaves) * 4;
+    if (chunks <= kSelfChunks) {
+        const unsigned blocks = chunks == 0 ? 1u : (unsigned)chunks;
+        route_place_kernel<true><<<blocks, kRouteThreads, lds, s>>>(ids, slots, E, bits, nullptr, chunks, counts,
+                                                                   offsets, order);
         return hipGetLastError();
     }
     int32_t* const cc = (int32_t*)workspace;
@@ -350,58 +478,26 @@ hipError_t launch_moe_route(const int32_t* ids, int64_t slots, int E, int32_t* c
     return hipGetLastError();
 }
 
-int64_t moe_balance_ws_bytes(int64_t M, int) { return loss_blocks(M) * 8; }
-
-template <bool BF16, int PER>
-static hipError_t balance(const void* logits, int64_t M, int E, int64_t ldl, const uint8_t* mask, float* weights,
-                          double* partial, float* loss, hipStream_t s) {
-    const int64_t blocks = loss_blocks(M);
-    if (blocks > 0) {
-        balance_loss_kernel<BF16, PER><<<(unsigned)blocks, kBalThreads, 0, s>>>(logits, M, E, ldl, mask, weights,
-                                                                               partial);
-        hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    balance_sum_kernel<<<1, kBalThreads, 0, s>>>(partial, blocks, loss);
-    return hipGetLastError();
-}
-
-template <bool BF16, int PER>
-static hipError_t grad(const void* logits, int64_t M, int E, int64_t ldl, const uint8_t* mask, const float* weights,
-                       const float* dloss, void* dlogits, hipStream_t s) {
-    if (!grid_fits((M + kBalWaves - 1) / kBalWaves, kBalThreads)) return hipErrorInvalidConfiguration;
-    balance_grad_kernel<BF16, PER><<<(unsigned)((M + kBalWaves - 1) / kBalWaves), kBalThreads, 0, s>>>(
-        logits, M, E, ldl, mask, weights, dloss, dlogits);
-    return hipGetLastError();
-}
+int64_t moe_balance_ws_bytes(int64_t M, int) { return loss_blocks(M) == 1 ? 0 : loss_blocks(M) * 16; }
 
 hipError_t launch_moe_balance(const void* logits, int l_dtype, int64_t M, int E, int64_t ldl, const uint8_t* mask,
                               const int32_t* counts, float* loss, float* weights, void* workspace, hipStream_t s) {
-    balance_weights_kernel<<<1, kWeightThreads, 0, s>>>(mask, M, E, counts, weights);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
     double* const part = (double*)workspace;
-    const bool bf = l_dtype == TQ_BF16;
-#define DMM_BALANCE(PER)                                                                     \
-    return bf ? balance<true, PER>(logits, M, E, ldl, mask, weights, part, loss, s)          \
-              : balance<false, PER>(logits, M, E, ldl, mask, weights, part, loss, s)
-    if (E <= 64) DMM_BALANCE(1);
-    if (E <= 256) DMM_BALANCE(4);
-    DMM_BALANCE(8);
-#undef DMM_BALANCE
+    return with_lanes(E, [&](auto lanes) {
+        constexpr int L = decltype(lanes)::value;
+        return l_dtype == TQ_BF16 ? balance<true, L>(logits, M, E, ldl, mask, counts, loss, weights, part, s)
+                                  : balance<false, L>(logits, M, E, ldl, mask, counts, loss, weights, part, s);
+    });
 }
 
 hipError_t launch_moe_balance_grad(const void* logits, int l_dtype, int64_t M, int E, int64_t ldl,
                                    const uint8_t* mask, const float* weights, const float* dloss, void* dlogits,
                                    hipStream_t s) {
-    const bool bf = l_dtype == TQ_BF16;
-#define DMM_GRAD(PER)                                                                        \
-    return bf ? grad<true, PER>(logits, M, E, ldl, mask, weights, dloss, dlogits, s)         \
-              : grad<false, PER>(logits, M, E, ldl, mask, weights, dloss, dlogits, s)
-    if (E <= 64) DMM_GRAD(1);
-    if (E <= 256) DMM_GRAD(4);
-    DMM_GRAD(8);
-#undef DMM_GRAD
+    return with_lanes(E, [&](auto lanes) {
+        constexpr int L = decltype(lanes)::value;
+        return l_dtype == TQ_BF16 ? grad<true, L>(logits, M, E, ldl, mask, weights, dloss, dlogits, s)
+                                  : grad<false, L>(logits, M, E, ldl, mask, weights, dloss, dlogits, s);
+    });
 }
 
 }  // namespace dmm

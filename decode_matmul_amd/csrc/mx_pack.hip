@@ -10,7 +10,8 @@
 // they are bound by memory.  Four lanes share a block, eight values each, so a
 // wave reads 1 KiB (bf16) or 2 KiB (fp32) of consecutive values with 16-byte
 // loads and writes 256 consecutive code bytes; the block maximum takes two
-// exchanges within the four lanes.
+// exchanges within the four lanes.  A matrix without gaps and with whole blocks
+// is one long row, and a lane takes eight values at kPer places.
 #include "mx.h"
 
 namespace dmm {
@@ -49,19 +50,8 @@ __device__ __forceinline__ void load8(const void* base, int64_t at, int have, fl
     }
 }
 
-// Grid: one lane per eight values of the padded rows.
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads) mx_pack_kernel(const void* W, int64_t K, int64_t ldw, int64_t nb,
-                                                           int64_t blocks, uint8_t* codes, uint8_t* scales,
-                                                           int32_t* status) {
-    const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int64_t blk = t >> 2;
-    const int part = (int)t & 3;
-    const bool live = blk < blocks;
-    const int64_t row = live ? blk / nb : 0;
-    const int64_t k = (live ? blk - row * nb : 0) * 32 + part * 8;
-    float v[8];
-    load8<BF16>(W, row * ldw + k, live ? (int)(K - k < 8 ? K - k : 8) : 0, v);
+// Eight values to their codes; the block's scale byte goes to s.
+__device__ __forceinline__ uint32_t encode8(float* v, int& s) {
     // the largest magnitude: bit patterns of nonnegative floats order as integers
     uint32_t a = 0u;
 #pragma unroll
@@ -74,44 +64,70 @@ __global__ void __launch_bounds__(kThreads) mx_pack_kernel(const void* W, int64_
     o = (uint32_t)__shfl_xor((int)a, 2);
     a = a > o ? a : o;
     const int field = (int)(a >> 23);
-    const bool bad = field == 255;
-    const int s = bad ? 255 : (field > 2 ? field - 2 : 0);
-    uint32_t c = 0u;
-    if (!bad) {
+    s = field == 255 ? 255 : (field > 2 ? field - 2 : 0);
+    if (field == 255) return 0u;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __builtin_amdgcn_ldexpf(v[i], 127 - s);
-        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[0], v[1], 1.f, 0);
-        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2], v[3], 1.f, 1);
-        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4], v[5], 1.f, 2);
-        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6], v[7], 1.f, 3);
-    }
+    for (int i = 0; i < 8; ++i) v[i] = __builtin_amdgcn_ldexpf(v[i], 127 - s);
+    uint32_t c = 0u;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[0], v[1], 1.f, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2], v[3], 1.f, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4], v[5], 1.f, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6], v[7], 1.f, 3);
+    return c;
+}
+
+// Rows with gaps or cut blocks: one lane per eight values of the padded rows.
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads) mx_pack_rows_kernel(const void* W, int64_t K, int64_t ldw, int64_t nb,
+                                                                int64_t blocks, uint8_t* codes, uint8_t* scales,
+                                                                int32_t* status) {
+    const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int64_t blk = t >> 2;
+    const int part = (int)t & 3;
+    const bool live = blk < blocks;
+    const int64_t row = live ? blk / nb : 0;
+    const int64_t k = (live ? blk - row * nb : 0) * 32 + part * 8;
+    float v[8];
+    load8<BF16>(W, row * ldw + k, live ? (int)(K - k < 8 ? K - k : 8) : 0, v);
+    int s;
+    const uint32_t c = encode8(v, s);
     if (!live) return;
     ((uint32_t*)codes)[t] = c;
     if (part == 0) {
         scales[blk] = (uint8_t)s;
-        if (bad) atomic_or_status(status, TQ_DATA_RANGE);
+        if (s == 255) atomic_or_status(status, TQ_DATA_RANGE);
     }
 }
 
-// Grid: one lane per eight values of the padded rows.
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads) mx_unpack_kernel(const uint8_t* codes, const uint8_t* scales,
-                                                             int64_t K, int64_t nb, int64_t blocks, void* out,
-                                                             int32_t* status) {
-    const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int64_t blk = t >> 2;
-    if (blk >= blocks) return;
-    const int64_t row = blk / nb;
-    const int64_t k = (blk - row * nb) * 32 + ((int)t & 3) * 8;
-    const uint32_t c = ((const uint32_t*)codes)[t];
-    const uint32_t s = scales[blk];
-    const float scale = e8m0_bits(s);
-    const int have = (int)(K - k < 8 ? K - k : 8);
-    if (status) {
-        if (s == 255u) atomic_or_status(status, TQ_DATA_RANGE);
-        if (have < 8 && (have <= 0 ? c : c >> (4 * have)) != 0u) atomic_or_status(status, TQ_DATA_PADDING);
+// One row of n8 eighths of a block (n8 a multiple of 4).
+template <bool BF16, int PER>
+__global__ void __launch_bounds__(kThreads) mx_pack_flat_kernel(const void* W, int64_t n8, uint8_t* codes,
+                                                                uint8_t* scales, int32_t* status) {
+    const int64_t t0 = (int64_t)blockIdx.x * (kThreads * PER) + threadIdx.x;
+    float v[PER][8];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int64_t t = t0 + i * kThreads;
+        load8<BF16>(W, t * 8, t < n8 ? 8 : 0, v[i]);
     }
-    if (have <= 0) return;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int64_t t = t0 + i * kThreads;
+        int s;
+        const uint32_t c = encode8(v[i], s);
+        if (t >= n8) continue;
+        ((uint32_t*)codes)[t] = c;
+        if ((t & 3) == 0) {
+            scales[t >> 2] = (uint8_t)s;
+            if (s == 255) atomic_or_status(status, TQ_DATA_RANGE);
+        }
+    }
+}
+
+// Eight codes and their scale to `have` values of row `out`, from column k.
+template <bool BF16>
+__device__ __forceinline__ void decode8(uint32_t c, uint32_t s, void* out, int64_t at, int have) {
+    const float scale = e8m0_bits(s);
     if (BF16) {
         union {
             bf16x8 v;
@@ -119,9 +135,9 @@ __global__ void __launch_bounds__(kThreads) mx_unpack_kernel(const uint8_t* code
             uint16_t h[8];
         } u;
         u.v = mx_decode8(c, scale);
-        uint16_t* p = (uint16_t*)out + row * K + k;
+        uint16_t* p = (uint16_t*)out + at;
         if (have >= 8) {
-            *(u32x4h*)p = u.d;
+            __builtin_nontemporal_store(u.d, (u32x4h*)p);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -137,10 +153,10 @@ __global__ void __launch_bounds__(kThreads) mx_unpack_kernel(const uint8_t* code
         u.h[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 1);
         u.h[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 2);
         u.h[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 3);
-        float* p = (float*)out + row * K + k;
+        float* p = (float*)out + at;
         if (have >= 8) {
-            *(u32x4a*)p = u.d[0];
-            *(u32x4a*)(p + 4) = u.d[1];
+            __builtin_nontemporal_store(u.d[0], (u32x4a*)p);
+            __builtin_nontemporal_store(u.d[1], (u32x4a*)(p + 4));
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -149,32 +165,107 @@ __global__ void __launch_bounds__(kThreads) mx_unpack_kernel(const uint8_t* code
     }
 }
 
+// Rows with cut blocks: one lane per eight values of the padded rows.
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads) mx_unpack_rows_kernel(const uint8_t* codes, const uint8_t* scales,
+                                                                  int64_t K, int64_t nb, int64_t blocks, void* out,
+                                                                  int32_t* status) {
+    const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int64_t blk = t >> 2;
+    if (blk >= blocks) return;
+    const int64_t row = blk / nb;
+    const int64_t k = (blk - row * nb) * 32 + ((int)t & 3) * 8;
+    const uint32_t c = ((const uint32_t*)codes)[t];
+    const uint32_t s = scales[blk];
+    const int have = (int)(K - k < 8 ? K - k : 8);
+    if (status) {
+        if (s == 255u) atomic_or_status(status, TQ_DATA_RANGE);
+        if (have < 8 && (have <= 0 ? c : c >> (4 * have)) != 0u) atomic_or_status(status, TQ_DATA_PADDING);
+    }
+    if (have > 0) decode8<BF16>(c, s, out, row * K + k, have);
+}
+
+// Whole blocks: one row of n8 eighths of a block.
+template <bool BF16, int PER>
+__global__ void __launch_bounds__(kThreads) mx_unpack_flat_kernel(const uint8_t* codes, const uint8_t* scales,
+                                                                  int64_t n8, void* out, int32_t* status) {
+    const int64_t t0 = (int64_t)blockIdx.x * (kThreads * PER) + threadIdx.x;
+    uint32_t c[PER], s[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int64_t t = t0 + i * kThreads;
+        c[i] = t < n8 ? ((const uint32_t*)codes)[t] : 0u;
+        s[i] = t < n8 ? scales[t >> 2] : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int64_t t = t0 + i * kThreads;
+        if (t >= n8) continue;
+        if (status && s[i] == 255u) atomic_or_status(status, TQ_DATA_RANGE);
+        decode8<BF16>(c[i], s[i], out, t * 8, 8);
+    }
+}
+
+#ifndef DMM_PP
+#define DMM_PP 4
+#endif
+constexpr int kPer = DMM_PP;
+
+template <bool BF16>
+hipError_t pack(const void* W, int64_t rows, int64_t K, int64_t ldw, uint8_t* codes, uint8_t* scales, int32_t* status,
+                hipStream_t s) {
+    const int64_t nb = (K + 31) / 32, blocks = rows * nb, n8 = blocks * 4;
+    if (K % 32 == 0 && (rows == 1 || ldw == K)) {
+        // a lane of a small matrix takes one place, so that all of them start at once
+        if (n8 <= (int64_t)compute_unit_count() * 2048)
+            mx_pack_flat_kernel<BF16, 1><<<(unsigned)((n8 + kThreads - 1) / kThreads), kThreads, 0, s>>>(W, n8, codes,
+                                                                                                    scales, status);
+        else
+            mx_pack_flat_kernel<BF16, kPer><<<(unsigned)((n8 + kThreads * kPer - 1) / (kThreads * kPer)), kThreads, 0,
+                                              s>>>(W, n8, codes, scales, status);
+    } else {
+        mx_pack_rows_kernel<BF16><<<(unsigned)((n8 + kThreads - 1) / kThreads), kThreads, 0, s>>>(
+            W, K, ldw, nb, blocks, codes, scales, status);
+    }
+    return hipGetLastError();
+}
+
+template <bool BF16>
+hipError_t unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, void* out, int32_t* status,
+                  hipStream_t s) {
+    const int64_t nb = (K + 31) / 32, blocks = rows * nb, n8 = blocks * 4;
+    if (K % 32 == 0) {
+        if (n8 <= (int64_t)compute_unit_count() * 2048)
+            mx_unpack_flat_kernel<BF16, 1><<<(unsigned)((n8 + kThreads - 1) / kThreads), kThreads, 0, s>>>(
+                codes, scales, n8, out, status);
+        else
+            mx_unpack_flat_kernel<BF16, kPer><<<(unsigned)((n8 + kThreads * kPer - 1) / (kThreads * kPer)), kThreads,
+                                                0, s>>>(codes, scales, n8, out, status);
+    } else {
+        mx_unpack_rows_kernel<BF16><<<(unsigned)((n8 + kThreads - 1) / kThreads), kThreads, 0, s>>>(
+            codes, scales, K, nb, blocks, out, status);
+    }
+    return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_mx_pack(const void* W, int w_dtype, int64_t rows, int64_t K, int64_t ldw, uint8_t* codes,
                           uint8_t* scales, int32_t* status, hipStream_t s) {
-    const int64_t nb = (K + 31) / 32, blocks = rows * nb;
+    const int64_t blocks = rows * ((K + 31) / 32);
     if (blocks == 0) return hipSuccess;
     if (!grid_fits((blocks * 4 + kThreads - 1) / kThreads, kThreads)) return hipErrorInvalidConfiguration;
-    const dim3 grid((unsigned)((blocks * 4 + kThreads - 1) / kThreads));
-    if (w_dtype == TQ_BF16)
-        mx_pack_kernel<true><<<grid, kThreads, 0, s>>>(W, K, ldw, nb, blocks, codes, scales, status);
-    else
-        mx_pack_kernel<false><<<grid, kThreads, 0, s>>>(W, K, ldw, nb, blocks, codes, scales, status);
-    return hipGetLastError();
+    return w_dtype == TQ_BF16 ? pack<true>(W, rows, K, ldw, codes, scales, status, s)
+                              : pack<false>(W, rows, K, ldw, codes, scales, status, s);
 }
 
 hipError_t launch_mx_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, void* out,
                             int out_dtype, int32_t* status, hipStream_t s) {
-    const int64_t nb = (K + 31) / 32, blocks = rows * nb;
+    const int64_t blocks = rows * ((K + 31) / 32);
     if (blocks == 0) return hipSuccess;
     if (!grid_fits((blocks * 4 + kThreads - 1) / kThreads, kThreads)) return hipErrorInvalidConfiguration;
-    const dim3 grid((unsigned)((blocks * 4 + kThreads - 1) / kThreads));
-    if (out_dtype == TQ_BF16)
-        mx_unpack_kernel<true><<<grid, kThreads, 0, s>>>(codes, scales, K, nb, blocks, out, status);
-    else
-        mx_unpack_kernel<false><<<grid, kThreads, 0, s>>>(codes, scales, K, nb, blocks, out, status);
-    return hipGetLastError();
+    return out_dtype == TQ_BF16 ? unpack<true>(codes, scales, rows, K, out, status, s)
+                                : unpack<false>(codes, scales, rows, K, out, status, s);
 }
 
 }  // namespace dmm

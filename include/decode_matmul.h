@@ -603,8 +603,8 @@ int mx_matmul_experts(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, cons
  *  loss        device fp32 [1].
  *  weights     device fp32 [n_experts]: w, which moe_balance_grad takes.
  *  workspace   device memory of moe_balance_workspace_bytes(M, n_experts)
- *              bytes, 8-byte aligned.  Overwritten; calls that share it must
- *              not overlap.
+ *              bytes, 8-byte aligned; NULL where that is 0 (few tokens).
+ *              Overwritten; calls that share it must not overlap.
  *
  * Softmax statistics are fp32, the sum over tokens is float64 in a fixed order.
  */

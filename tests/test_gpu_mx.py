@@ -186,6 +186,8 @@ SHAPES = [
     (64, 100, 256, 0, True), (65, 300, 1023, 1, False), (127, 129, 320, 0, True), (128, 256, 512, 8, False),
     (129, 513, 2048, 0, True), (200, 77, 4100, 4, False), (255, 256, 64, 0, False), (257, 511, 384, 0, True),
     (300, 1001, 1000, 24, True), (513, 260, 1184, 0, False), (1, 7, 9000, 0, True),
+    # enough tiles for the larger ones
+    (700, 4300, 330, 0, True), (650, 4404, 1155, 3, False), (1030, 12500, 264, 0, True), (1027, 12403, 577, 1, False),
 ]
 IDS = ["x".join(map(str, s[:3])) for s in SHAPES]
 
