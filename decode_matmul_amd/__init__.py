@@ -487,11 +487,12 @@ def _call(what, device, *args):
     if device.type != "cuda":
         raise ValueError(f"{what}: tensors are on {device}, not on a GPU")
     fn = getattr(_lib, what)
+    stream = torch._C._cuda_getCurrentRawStream(device.index)
     if torch.cuda.current_device() == device.index:
-        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+        rc = fn(*args, stream)
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+            rc = fn(*args, stream)
     if rc != TQ_OK:
         _raise(rc, what)
 

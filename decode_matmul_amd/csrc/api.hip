@@ -363,7 +363,7 @@ int mx_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t
     if (rows > 0 && K > 0 && (!W_out || !codes || !scales)) return TQ_ERR_NULL;
     if (!aligned(W_out, bytes_of(out_dtype)) || !aligned(codes, 16) || !aligned(d_status, 4))
         return TQ_ERR_ALIGN;
-    if (!dmm::grid_fits(rows * ((K + 31) / 32) / 64 + 1, 256)) return TQ_ERR_SHAPE;
+    if (!dmm::grid_fits(rows * ((K + 31) / 32) / 32 + 1, 256)) return TQ_ERR_SHAPE;
     hipStream_t s = (hipStream_t)stream;
     if (d_status && dmm::launch_status_clear(d_status, s) != hipSuccess) return TQ_ERR_HIP;
     return grid_status(dmm::launch_mx_unpack(codes, scales, rows, K, W_out, out_dtype, d_status, s));
@@ -451,8 +451,8 @@ int moe_balance(const void* logits, int32_t l_dtype, int64_t M, int32_t n_expert
         !aligned(weights, 4) || !aligned(workspace, 8))
         return TQ_ERR_ALIGN;
     if (need > 0 && workspace_bytes < need) return TQ_ERR_SHAPE;
-    return hip_status(dmm::launch_moe_balance(logits, l_dtype, M, n_experts, ldl, token_mask, counts, loss,
-                                              weights, workspace, (hipStream_t)stream));
+    return grid_status(dmm::launch_moe_balance(logits, l_dtype, M, n_experts, ldl, token_mask, counts, loss,
+                                               weights, workspace, (hipStream_t)stream));
 }
 
 int moe_balance_grad(const void* logits, int32_t l_dtype, int64_t M, int32_t n_experts, int64_t ldl,

@@ -15,21 +15,22 @@ namespace {
 // workgroup each, and a slot's place is
 //     offset of its expert + slots of that expert in earlier chunks
 //     + slots of that expert earlier in its chunk.
-// Within a chunk wave w holds the w-th sixteenth, in rows of 64 consecutive
+// Within a chunk wave w holds the w-th quarter, in rows of 64 consecutive
 // slots: lanes with the same expert find each other by one ballot for each
 // bit of the id, and a count per (wave, expert) in LDS carries on from row to
 // row.  No place depends on the order in which anything runs.
 //
-// Bound: latency.  Up to kSelfChunks chunks take one launch, in which every
-// workgroup counts all chunks for itself; more take three: counts per chunk,
-// their running sums over the chunks, places.
-constexpr int kRouteThreads = 1024;
+// Bound: latency.  One chunk takes one launch.  Up to kSumChunks take two, the
+// counts of each chunk and the places, for which a workgroup sums the counts
+// itself; more take three, the counts' running sums over the chunks in between.
+// (16384 slots of 64 experts: 15.2 us with one launch of 4 workgroups that each
+// count everything.)
+constexpr int kRouteThreads = 256;
 constexpr int kRouteWaves = kRouteThreads / 64;
 constexpr int kRows = 4;                        // rows of 64 slots a wave
 constexpr int kChunk = kRouteThreads * kRows;
-constexpr int kSelfChunks = 8;
+constexpr int kSumChunks = 64;
 constexpr int kScanThreads = 256;
-static_assert(kMoeMaxExperts < kRouteThreads, "a thread for each expert and one for no expert");
 
 __device__ __forceinline__ int expert_of(const int32_t* ids, int64_t slot, int64_t slots, int E) {
     if (slot >= slots) return -1;               // behind the last slot: counted nowhere
@@ -47,9 +48,9 @@ __device__ __forceinline__ uint64_t same_id(int id, uint64_t live, int bits) {
     return m;
 }
 
-// Exclusive sums of v over the workgroup's threads (kRouteThreads >= E + 1);
-// `sums` holds kRouteWaves words.
-__device__ __forceinline__ int exclusive_sum(int v, int* sums) {
+// Exclusive sums of v over the workgroup's threads, and the sum of all; `sums`
+// holds kRouteWaves words and is free again after the next barrier.
+__device__ __forceinline__ int exclusive_sum(int v, int* sums, int& all) {
     const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
     int inc = v;
 #pragma unroll
@@ -60,45 +61,36 @@ __device__ __forceinline__ int exclusive_sum(int v, int* sums) {
     if (lane == 63) sums[wave] = inc;
     __syncthreads();
     int before = 0;
-    for (int w = 0; w < wave; ++w) before += sums[w];
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < kRouteWaves; ++w) {
+        if (w < wave) before += sums[w];
+        all += sums[w];
+    }
     return before + inc - v;
 }
 
-// SELF: this workgroup counts the other chunks itself.  Otherwise `before`
-// [chunks + 1][E + 1] holds each chunk's running sums, the last row the totals.
-template <bool SELF>
+enum RouteChunks { kOnly, kSummed, kScanned };
+
+// kOnly: the only chunk.  kSummed: cc [chunks][E + 1] holds the chunks' counts.
+// kScanned: cc [chunks + 1][E + 1] holds each chunk's running sums, the last row
+// the totals.
+template <RouteChunks MODE>
 __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const int32_t* ids, int64_t slots, int E,
-                                                                    int bits, const int32_t* before,
-                                                                    int64_t chunks, int32_t* counts,
-                                                                    int32_t* offsets, int32_t* order) {
-    extern __shared__ int lds[];                // [kRouteWaves][E + 1] counts, then places; two more such rows; sums
-    int* const rest = lds + kRouteWaves * (E + 1);      // SELF: slots in earlier chunks, and in later ones
-    int* const sums = rest + 2 * (E + 1);
+                                                                    int bits, const int32_t* cc, int chunks,
+                                                                    int32_t* counts, int32_t* offsets,
+                                                                    int32_t* order) {
+    extern __shared__ int lds[];                // [kRouteWaves][E + 1] counts, then places; kRouteWaves sums
+    int* const sums = lds + kRouteWaves * (E + 1);
     const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6, tid = (int)threadIdx.x;
-    for (int i = tid; i < (kRouteWaves + 2) * (E + 1); i += kRouteThreads) lds[i] = 0;
-    __syncthreads();
     const int64_t first = (int64_t)blockIdx.x * kChunk + wave * (64 * kRows) + lane;
     int id[kRows], rank[kRows];
-    // volatile: a row's places are read after the row before wrote them, by other lanes of the wave
-    volatile int* const mine = lds + wave * (E + 1);
 #pragma unroll
     for (int i = 0; i < kRows; ++i) id[i] = expert_of(ids, first + 64 * i, slots, E);
-    if (SELF) {
-        for (int64_t c = 0; c < chunks; ++c) {
-            if (c == (int64_t)blockIdx.x) continue;
-            int other[kRows];
-#pragma unroll
-            for (int i = 0; i < kRows; ++i)
-                other[i] = expert_of(ids, c * kChunk + wave * (64 * kRows) + lane + 64 * i, slots, E);
-            int* const row = rest + (c < (int64_t)blockIdx.x ? 0 : E + 1);
-#pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                const uint64_t same = same_id(other[i], __ballot(other[i] >= 0), bits);
-                // one lane for each expert of the row; whole numbers, so any order gives the same count
-                if (other[i] >= 0 && (same & ((1ull << lane) - 1ull)) == 0) atomicAdd(&row[other[i]], __popcll(same));
-            }
-        }
-    }
+    for (int i = tid; i < kRouteWaves * (E + 1); i += kRouteThreads) lds[i] = 0;
+    __syncthreads();
+    // volatile: a row's places are read after the row before wrote them, by other lanes of the wave
+    volatile int* const mine = lds + wave * (E + 1);
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         const uint64_t same = same_id(id[i], __ballot(id[i] >= 0), bits);
@@ -108,50 +100,65 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const int32_
         if (id[i] >= 0 && below == 0) mine[id[i]] = base + __popcll(same);
     }
     __syncthreads();
-    // thread e: the count of expert e over all chunks, and what earlier chunks hold
-    int total = 0, earlier = 0;
-    if (tid <= E) {
-        if (SELF) {
-            for (int w = 0; w < kRouteWaves; ++w) total += lds[w * (E + 1) + tid];
-            earlier = rest[tid];
-            total += earlier + rest[E + 1 + tid];
-        } else {
-            total = before[chunks * (E + 1) + tid];
-            earlier = before[(int64_t)blockIdx.x * (E + 1) + tid];
+    int carry = 0;                              // slots of the experts below e0
+    for (int e0 = 0; e0 <= E; e0 += kRouteThreads) {
+        // expert e's slots in all chunks, and in earlier ones
+        const int e = e0 + tid;
+        int total = 0, earlier = 0;
+        if (e <= E) {
+            if (MODE == kOnly) {
+#pragma unroll
+                for (int w = 0; w < kRouteWaves; ++w) total += lds[w * (E + 1) + e];
+            } else if (MODE == kSummed) {
+#pragma unroll 8
+                for (int c = 0; c < chunks; ++c) {
+                    const int v = cc[c * (E + 1) + e];
+                    total += v;
+                    if (c < (int)blockIdx.x) earlier += v;
+                }
+            } else {
+                total = cc[(int64_t)chunks * (E + 1) + e];
+                earlier = cc[(int64_t)blockIdx.x * (E + 1) + e];
+            }
         }
+        int all;
+        const int offset = carry + exclusive_sum(total, sums, all);
+        carry += all;
+        if (e <= E) {
+            if (blockIdx.x == 0) {
+                offsets[e] = offset;
+                if (e < E) counts[e] = total;
+            }
+            int at = offset + earlier;
+#pragma unroll
+            for (int w = 0; w < kRouteWaves; ++w) {
+                const int v = lds[w * (E + 1) + e];
+                lds[w * (E + 1) + e] = at;
+                at += v;
+            }
+        }
+        __syncthreads();
     }
-    const int offset = exclusive_sum(total, sums);
-    if (tid <= E) {
-        if (blockIdx.x == 0) {
-            offsets[tid] = offset;
-            if (tid < E) counts[tid] = total;
-        }
-        int at = offset + earlier;
-        for (int w = 0; w < kRouteWaves; ++w) {
-            const int v = lds[w * (E + 1) + tid];
-            lds[w * (E + 1) + tid] = at;
-            at += v;
-        }
-    }
-    __syncthreads();
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
         if (id[i] >= 0) order[mine[id[i]] + rank[i]] = (int32_t)(first + 64 * i);
 }
 
 __global__ void __launch_bounds__(kRouteThreads) route_count_kernel(const int32_t* ids, int64_t slots, int E,
-                                                                    int32_t* chunk_counts) {
+                                                                    int32_t* cc) {
     extern __shared__ int lds[];                // [E + 1]
     const int tid = (int)threadIdx.x;
+    int id[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+        id[i] = expert_of(ids, (int64_t)blockIdx.x * kChunk + i * kRouteThreads + tid, slots, E);
     for (int i = tid; i <= E; i += kRouteThreads) lds[i] = 0;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int id = expert_of(ids, (int64_t)blockIdx.x * kChunk + i * kRouteThreads + tid, slots, E);
-        if (id >= 0) atomicAdd(&lds[id], 1);    // whole numbers: any order gives the same count
-    }
+    for (int i = 0; i < kRows; ++i)
+        if (id[i] >= 0) atomicAdd(&lds[id[i]], 1);      // whole numbers: any order gives the same count
     __syncthreads();
-    for (int i = tid; i <= E; i += kRouteThreads) chunk_counts[(int64_t)blockIdx.x * (E + 1) + i] = lds[i];
+    for (int i = tid; i <= E; i += kRouteThreads) cc[(int64_t)blockIdx.x * (E + 1) + i] = lds[i];
 }
 
 // Column e = blockIdx.x of the chunks' counts -> its running sums, the total
@@ -252,7 +259,8 @@ __device__ __forceinline__ float row_softmax(float* p, const float* w) {
     float sum = 0.f, ws = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        p[i] = expf(p[i] - top);
+        // off by about (top - z) 2^-24 of itself, the rounding of its argument, and a unit
+        p[i] = __builtin_amdgcn_exp2f((p[i] - top) * 1.44269504088896340736f);
         sum += p[i];
         ws += w[i] * p[i];
     }
@@ -279,16 +287,29 @@ __device__ __forceinline__ void finish_balance(double sum, int64_t T, double n, 
     if (threadIdx.x == 0) loss[0] = some ? (float)(sum / (double)T) : 0.f;
 }
 
-// A workgroup's tokens: `rows` from blockIdx.x * rows on.  partial [blocks][2]:
-// their sum and how many take part; the only workgroup finishes by itself.
+// Tokens of a workgroup of the loss: kTokens for each group of L lanes, all of
+// their logits on their way before the first is used.
+constexpr int kTokens = 4;
+constexpr int loss_rows(int L) { return kTokens * kBalThreads / L; }
+
+// partial [blocks][2]: the sum over a workgroup's tokens and how many take part;
+// the only workgroup finishes by itself.
 template <bool BF16, int L>
 __global__ void __launch_bounds__(kBalThreads) balance_loss_kernel(const void* logits, int64_t M, int E, int64_t ldl,
                                                                    const uint8_t* mask, const int32_t* counts,
-                                                                   int rows, float* loss, float* weights,
-                                                                   double* partial) {
+                                                                   float* loss, float* weights, double* partial) {
     __shared__ double part[3][kBalWaves];
     const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
     const int e0 = (lane % L) * 8, have = E - e0;
+    float z[kTokens][8];
+    bool live[kTokens];
+    const int64_t t0 = (int64_t)blockIdx.x * loss_rows(L) + (int)threadIdx.x / L;
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        const int64_t t = t0 + i * (kBalThreads / L);
+        live[i] = t < M && !(mask && mask[t] == 0);
+        load_logits<BF16>(logits, live[i] ? t * ldl + e0 : 0, live[i] ? have : 0, z[i]);
+    }
     double n = 0.0;
     for (int e = (int)threadIdx.x; e < E; e += kBalThreads) n += (double)counts[e];
     n = group_sum<64>(n);
@@ -296,17 +317,14 @@ __global__ void __launch_bounds__(kBalThreads) balance_loss_kernel(const void* l
     __syncthreads();
     n = 0.0;
     for (int i = 0; i < kBalWaves; ++i) n += part[2][i];
-    float w[8], p[8];
+    float w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = i < have && n > 0.0 ? (float)((double)E * ((double)counts[e0 + i] / n)) : 0.f;
     double sum = 0.0, tokens = 0.0;
-    const int64_t t0 = (int64_t)blockIdx.x * rows;
-    for (int i = wave * (64 / L) + lane / L; i < rows; i += kBalThreads / L) {
-        const int64_t t = t0 + i;
-        if (t >= M || (mask && mask[t] == 0)) continue;
-        load_logits<BF16>(logits, t * ldl + e0, have, p);
-        const float s = row_softmax<L>(p, w);
-        if (lane % L == 0) {
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        const float s = row_softmax<L>(z[i], w);        // 0 for the -inf of a token that takes no part
+        if (live[i] && lane % L == 0) {
             sum += (double)s;
             tokens += 1.0;
         }
@@ -384,8 +402,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const void* l
         if (have >= 8) {
             u32x4 v;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[i] = (uint32_t)f32_to_bf16_rne(p[2 * i]) | (uint32_t)f32_to_bf16_rne(p[2 * i + 1]) << 16;
+            for (int i = 0; i < 4; ++i) v[i] = bf16_pair(p[2 * i], p[2 * i + 1]);
             *(u32x4h*)d = v;
         } else {
 #pragma unroll
@@ -407,18 +424,26 @@ __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const void* l
 
 int64_t route_chunks(int64_t slots) { return (slots + kChunk - 1) / kChunk; }
 
-// Tokens of a workgroup of the loss: few enough to fill the chip, and enough to
-// keep the partial sums few.
-int loss_rows(int64_t M) { return M <= 64 * 256 ? 64 : 256; }
+// Lanes of a row of E logits, eight each.
+int row_lanes(int E) {
+    int L = 1;
+    while (8 * L < E) L *= 2;
+    return L;
+}
+static_assert(kMoeMaxExperts <= 64 * 8, "a row fits a wave");
 
-int64_t loss_blocks(int64_t M) { return M == 0 ? 1 : (M + loss_rows(M) - 1) / loss_rows(M); }
+int64_t loss_blocks(int64_t M, int E) {
+    const int rows = loss_rows(row_lanes(E));
+    return M == 0 ? 1 : (M + rows - 1) / rows;
+}
 
 template <bool BF16, int L>
 hipError_t balance(const void* logits, int64_t M, int E, int64_t ldl, const uint8_t* mask, const int32_t* counts,
                    float* loss, float* weights, double* partial, hipStream_t s) {
-    const int64_t blocks = loss_blocks(M);
-    balance_loss_kernel<BF16, L><<<(unsigned)blocks, kBalThreads, 0, s>>>(logits, M, E, ldl, mask, counts, loss_rows(M),
-                                                                         loss, weights, partial);
+    const int64_t blocks = loss_blocks(M, E);
+    if (!grid_fits(blocks, kBalThreads)) return hipErrorInvalidConfiguration;
+    balance_loss_kernel<BF16, L><<<(unsigned)blocks, kBalThreads, 0, s>>>(logits, M, E, ldl, mask, counts, loss,
+                                                                         weights, partial);
     hipError_t e = hipGetLastError();
     if (blocks == 1 || e != hipSuccess) return e;
     balance_finish_kernel<<<1, kBalThreads, 0, s>>>(partial, blocks, E, counts, loss, weights);
@@ -438,47 +463,52 @@ hipError_t grad(const void* logits, int64_t M, int E, int64_t ldl, const uint8_t
 // f(integral constant L) for the lanes a row of E logits takes.
 template <class F>
 hipError_t with_lanes(int E, F f) {
-    if (E <= 8) return f(std::integral_constant<int, 1>());
-    if (E <= 16) return f(std::integral_constant<int, 2>());
-    if (E <= 32) return f(std::integral_constant<int, 4>());
-    if (E <= 64) return f(std::integral_constant<int, 8>());
-    if (E <= 128) return f(std::integral_constant<int, 16>());
-    if (E <= 256) return f(std::integral_constant<int, 32>());
-    return f(std::integral_constant<int, 64>());
+    switch (row_lanes(E)) {
+        case 1: return f(std::integral_constant<int, 1>());
+        case 2: return f(std::integral_constant<int, 2>());
+        case 4: return f(std::integral_constant<int, 4>());
+        case 8: return f(std::integral_constant<int, 8>());
+        case 16: return f(std::integral_constant<int, 16>());
+        case 32: return f(std::integral_constant<int, 32>());
+        default: return f(std::integral_constant<int, 64>());
+    }
 }
-static_assert(kMoeMaxExperts <= 64 * 8, "a row fits a wave");
 
 }  // namespace
 
 int64_t moe_route_ws_bytes(int64_t slots, int E) {
     const int64_t chunks = route_chunks(slots);
-    return chunks <= kSelfChunks ? 0 : (chunks + 1) * (E + 1) * 4;
+    return chunks <= 1 ? 0 : (chunks + 1) * (E + 1) * 4;
 }
 
 hipError_t launch_moe_route(const int32_t* ids, int64_t slots, int E, int32_t* counts, int32_t* offsets,
                             int32_t* order, void* workspace, hipStream_t s) {
     const int64_t chunks = route_chunks(slots);
     const int bits = 32 - __builtin_clz((unsigned)E);
-    const size_t lds = (size_t)((kRouteWaves + 2) * (E + 1) + kRouteWaves) * 4;
-    if (chunks <= kSelfChunks) {
-        const unsigned blocks = chunks == 0 ? 1u : (unsigned)chunks;
-        route_place_kernel<true><<<blocks, kRouteThreads, lds, s>>>(ids, slots, E, bits, nullptr, chunks, counts,
-                                                                   offsets, order);
+    const size_t lds = (size_t)(kRouteWaves * (E + 1) + kRouteWaves) * 4;
+    if (chunks <= 1) {
+        route_place_kernel<kOnly><<<1, kRouteThreads, lds, s>>>(ids, slots, E, bits, nullptr, 1, counts, offsets,
+                                                               order);
         return hipGetLastError();
     }
     int32_t* const cc = (int32_t*)workspace;
     route_count_kernel<<<(unsigned)chunks, kRouteThreads, (size_t)(E + 1) * 4, s>>>(ids, slots, E, cc);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    if (chunks <= kSumChunks) {
+        route_place_kernel<kSummed><<<(unsigned)chunks, kRouteThreads, lds, s>>>(ids, slots, E, bits, cc, (int)chunks,
+                                                                                counts, offsets, order);
+        return hipGetLastError();
+    }
     route_scan_kernel<<<(unsigned)(E + 1), kScanThreads, 0, s>>>(cc, chunks, E);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    route_place_kernel<false><<<(unsigned)chunks, kRouteThreads, lds, s>>>(ids, slots, E, bits, cc, chunks, counts,
-                                                                          offsets, order);
+    route_place_kernel<kScanned><<<(unsigned)chunks, kRouteThreads, lds, s>>>(ids, slots, E, bits, cc, (int)chunks,
+                                                                             counts, offsets, order);
     return hipGetLastError();
 }
 
-int64_t moe_balance_ws_bytes(int64_t M, int) { return loss_blocks(M) == 1 ? 0 : loss_blocks(M) * 16; }
+int64_t moe_balance_ws_bytes(int64_t M, int E) { return loss_blocks(M, E) == 1 ? 0 : loss_blocks(M, E) * 16; }
 
 hipError_t launch_moe_balance(const void* logits, int l_dtype, int64_t M, int E, int64_t ldl, const uint8_t* mask,
                               const int32_t* counts, float* loss, float* weights, void* workspace, hipStream_t s) {

@@ -34,6 +34,11 @@ __device__ __forceinline__ bf16x8 mx_decode8(uint32_t c, float scale) {
     return u.v;
 }
 
+// Two fp32 values as bf16, nearest-even, in one dword.
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
+}
+
 // The scaled matrix instruction's operand of 32 codes (16 bytes; the upper
 // half of the register group is not read for 4-bit types).
 __device__ __forceinline__ i32x8 mx_operand(u32x4 c) {

@@ -476,8 +476,8 @@ __global__ void __launch_bounds__(64 * WM * WN, BM * BN == 128 * 256 ? 4 : 2) mx
                         *(f32x4*)((float*)a.y + at) = v;
                     } else {
                         u32x2 d;
-                        d.x = (uint32_t)f32_to_bf16_rne(v.x) | (uint32_t)f32_to_bf16_rne(v.y) << 16;
-                        d.y = (uint32_t)f32_to_bf16_rne(v.z) | (uint32_t)f32_to_bf16_rne(v.w) << 16;
+                        d.x = bf16_pair(v.x, v.y);
+                        d.y = bf16_pair(v.z, v.w);
                         *(u32x2*)((uint16_t*)a.y + at) = d;
                     }
                 } else {

@@ -171,8 +171,9 @@ def test_moe_route_refusals():
 
 
 def test_moe_balance_refusals():
-    need = lib.moe_balance_workspace_bytes(100, 8)
-    f, ok = lib.moe_balance, [FAKE, 0, 100, 8, 8, None, FAKE, FAKE, FAKE, FAKE, need, None]
+    need = lib.moe_balance_workspace_bytes(1 << 16, 8)
+    assert need > 0 and lib.moe_balance_workspace_bytes(16, 64) == 0
+    f, ok = lib.moe_balance, [FAKE, 0, 1 << 16, 8, 8, None, FAKE, FAKE, FAKE, FAKE, need, None]
     for i, v, want in ((0, None, NULL), (6, None, NULL), (7, None, NULL), (8, None, NULL), (9, None, NULL),
                        (1, 5, DTYPE), (2, -1, SHAPE), (3, 0, SHAPE), (3, 600, UNSUPPORTED), (4, 7, SHAPE),
                        (10, need - 1, SHAPE), (0, ODD, ALIGN), (9, ctypes.c_void_p(0x10004), ALIGN)):
