@@ -201,18 +201,55 @@ __global__ void __launch_bounds__(kScanThreads) route_scan_kernel(int32_t* cc, i
 constexpr int kBalThreads = 256;
 constexpr int kBalWaves = kBalThreads / 64;
 
-template <int L>
-__device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-    for (int d = L / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
+// A value of another lane of 16, by the data-parallel moves: 0xb1 and 0x4e are
+// lanes ^ 1 and ^ 2; 0x141 and 0x140 mirror 8 and 16 lanes, which brings the other
+// half's value once all lanes of a half have the same.
+template <int CTRL>
+__device__ __forceinline__ float moved(float v) {
+    return __builtin_bit_cast(
+        float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+
+template <int L, class F>
+__device__ __forceinline__ float over_group(float v, F f) {
+    if (L >= 2) v = f(v, moved<0xb1>(v));
+    if (L >= 4) v = f(v, moved<0x4e>(v));
+    if (L >= 8) v = f(v, moved<0x141>(v));
+    if (L >= 16) v = f(v, moved<0x140>(v));
+    if (L >= 32) v = f(v, __shfl_xor(v, 16));
+    if (L >= 64) v = f(v, __shfl_xor(v, 32));
     return v;
 }
 
-template <int L, class T>
-__device__ __forceinline__ T group_sum(T v) {
+template <int L>
+__device__ __forceinline__ float group_max(float v) {
+    return over_group<L>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+
+template <int L>
+__device__ __forceinline__ float group_sum(float v) {
+    return over_group<L>(v, [](float a, float b) { return a + b; });
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
-    for (int d = L / 2; d > 0; d >>= 1) v += __shfl_xor(v, d);
+    for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
     return v;
+}
+
+// Eight weights from w[0] on, `have` of them there; the others are 0.
+__device__ __forceinline__ void load_weights(const float* w, int have, float* v) {
+    if (have >= 8) {
+        const f32x4 a = *(const f32x4a*)w, b = *(const f32x4a*)(w + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = a[i];
+            v[4 + i] = b[i];
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < have ? w[i] : 0.f;
 }
 
 // Eight logits at p, `have` of them there; the others are -inf.
@@ -307,30 +344,36 @@ __global__ void __launch_bounds__(kBalThreads) balance_loss_kernel(const void* l
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) {
         const int64_t t = t0 + i * (kBalThreads / L);
-        live[i] = t < M && !(mask && mask[t] == 0);
+        live[i] = t < M;
         load_logits<BF16>(logits, live[i] ? t * ldl + e0 : 0, live[i] ? have : 0, z[i]);
+        if (mask && live[i]) live[i] = mask[t] != 0;
     }
+    __shared__ float wt[kMoeMaxExperts];
     double n = 0.0;
-    for (int e = (int)threadIdx.x; e < E; e += kBalThreads) n += (double)counts[e];
-    n = group_sum<64>(n);
+    for (int e = (int)threadIdx.x; e < E; e += kBalThreads) {
+        n += (double)counts[e];
+        wt[e] = (float)counts[e];               // within 2^-24, like the other factors of a weight here
+    }
+    n = wave_sum(n);
     if (lane == 0) part[2][wave] = n;
     __syncthreads();
     n = 0.0;
     for (int i = 0; i < kBalWaves; ++i) n += part[2][i];
     float w[8];
+    const float scale = n > 0.0 ? (float)((double)E / n) : 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = i < have && n > 0.0 ? (float)((double)E * ((double)counts[e0 + i] / n)) : 0.f;
+    for (int i = 0; i < 8; ++i) w[i] = i < have ? scale * wt[e0 + i] : 0.f;
     double sum = 0.0, tokens = 0.0;
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) {
-        const float s = row_softmax<L>(z[i], w);        // 0 for the -inf of a token that takes no part
+        const float s = row_softmax<L>(z[i], w);
         if (live[i] && lane % L == 0) {
             sum += (double)s;
             tokens += 1.0;
         }
     }
-    sum = group_sum<64>(sum);
-    tokens = group_sum<64>(tokens);
+    sum = wave_sum(sum);
+    tokens = wave_sum(tokens);
     if (lane == 0) {
         part[0][wave] = sum;
         part[1][wave] = tokens;
@@ -362,7 +405,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_finish_kernel(const doubl
     for (int e = (int)threadIdx.x; e < E; e += kBalThreads) v[2] += (double)counts[e];
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-        v[k] = group_sum<64>(v[k]);
+        v[k] = wave_sum(v[k]);
         if (lane == 0) part[k][wave] = v[k];
     }
     __syncthreads();
@@ -382,18 +425,11 @@ __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const void* l
     const int64_t t = ((int64_t)blockIdx.x * kBalThreads + threadIdx.x) / L;
     const int e0 = (lane % L) * 8, have = E - e0;
     if (t >= M) return;
-    float w[8], p[8], s = 0.f, up = 0.f;
+    float w[8], p[8];
+    load_logits<BF16>(logits, t * ldl + e0, have, p);
+    load_weights(weights + e0, have, w);
     const bool live = !mask || mask[t] != 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        w[i] = i < have ? weights[e0 + i] : 0.f;
-        p[i] = 0.f;
-    }
-    if (live) {
-        load_logits<BF16>(logits, t * ldl + e0, have, p);
-        s = row_softmax<L>(p, w);
-        up = dloss[0];
-    }
+    const float up = dloss[0], s = row_softmax<L>(p, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) p[i] = live ? up * p[i] * (w[i] - s) : 0.f;
     const int64_t at = t * E + e0;
