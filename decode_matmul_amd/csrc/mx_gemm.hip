@@ -29,14 +29,10 @@ namespace dmm {
 namespace {
 
 constexpr int kRow = 128;                       // bytes of an LDS tile row (activations; codes with MXFP4 ones)
-// Tiled form: at least 8 blocks (a lane fetches 8 scale bytes at once), and rows
-// whose 256 fit 32-bit offsets.
-constexpr int64_t kMinTiledK = 256, kMaxTiledBytes = (int64_t)1 << 24;
+constexpr int64_t kMaxTiledBytes = (int64_t)1 << 24;   // of a row in the tiled form: 256 rows fit 32-bit offsets
 constexpr int kWRow = 32;                       // bytes of codes a row with bf16 activations
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-
-__device__ __forceinline__ int swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 
 // No load and no LDS access of this wave outstanding (expcnt aside), then the
 // workgroup's barrier.
@@ -133,7 +129,7 @@ __device__ bool place_grouped(const MxMatmulArgs& a, Place& p) {
 // straight to LDS (rows 16-byte aligned); otherwise through registers.  BM x BN
 // tile of WM x WN waves; KD units (64 columns, or 256 with MXX) a slab.
 template <bool MXX, bool DIRECT, int BM, int BN, int WM, int WN, int KD, bool GROUPED>
-__global__ void __launch_bounds__(64 * WM * WN, BM * BN == 128 * 256 ? 4 : 2) mx_gemm_kernel(MxMatmulArgs a) {
+__global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a) {
     constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
     constexpr int kUnit = MXX ? 256 : 64, kSlab = KD * kUnit;
     constexpr int kXUnit = BM * kRow, kWUnit = BN * (MXX ? kRow : kWRow);   // bytes of a unit
@@ -196,7 +192,10 @@ __global__ void __launch_bounds__(64 * WM * WN, BM * BN == 128 * 256 ? 4 : 2) mx
     auto w_all = [&](int j) { return wave + j * kWaves; };
     auto w_group = [&](int j) { return w_all(j) % kWGroups; };
     auto w_unit = [&](int j) { return w_all(j) / kWGroups; };
-    auto w_chunk = [&](int j) { return MXX ? (lane & 7) ^ swizzle(w_group(j) * 8 + x_sub) : lane & 1; };
+    // (the halves of W's 32-byte rows change places every eight rows: see swizzle)
+    auto w_chunk = [&](int j) {
+        return MXX ? (lane & 7) ^ swizzle(w_group(j) * 8 + x_sub) : (lane & 1) ^ ((lane >> 4) & 1);
+    };
     // Offsets from the tile's first row fit 32 bits (mx_gemm_takes); the rows of a list have 64.
     typedef typename std::conditional<GROUPED, int64_t, uint32_t>::type XOffset;
     const uint8_t* const xbase = MXX ? a.x_codes + p.m0 * nb * 16 : (const uint8_t*)(a.x + (GROUPED ? 0 : p.m0) * a.ldx);
@@ -267,16 +266,17 @@ __global__ void __launch_bounds__(64 * WM * WN, BM * BN == 128 * 256 ? 4 : 2) mx
         }
         if (!DIRECT) store_x(st);
     };
+    const int64_t last8 = nb > 8 ? nb - 8 : 0;
     uint64_t sc[NT], sc_next[NT];               // bf16 activations: scales of the units at hand
     auto fetch_scales = [&](int64_t q) {        // of units q .. q + 3, as far as there are any: the last eight
-        const int64_t b = 2 * q < nb - 8 ? 2 * q : nb - 8;
+        const int64_t b = 2 * q < last8 ? 2 * q : last8;
         const GlobalBytes sb = scalar_base(wscales + b);
 #pragma unroll
         for (int i = 0; i < NT; ++i)
             sc_next[i] = *(const __attribute__((address_space(1))) u64u*)(sb + lane_offset(ssrc[i]));
     };
     auto take_scales = [&](int64_t q) {
-        const int64_t b = 2 * q < nb - 8 ? 2 * q : nb - 8;
+        const int64_t b = 2 * q < last8 ? 2 * q : last8;
 #pragma unroll
         for (int i = 0; i < NT; ++i) sc[i] = sc_next[i] >> (8 * (int)(2 * q - b));
         if (2 * q + 8 < nb) fetch_scales(q + 4);
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(64 * WM * WN, BM * BN == 128 * 256 ? 4 : 2) mx
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             if (MXX && s % 2 == 0) wf[s >> 1][i] = *(const u32x4*)(wt + TR * i * kRow + at);
-            if (!MXX && s == 0) wf[0][i] = *(const u32x4*)(wt + (TR * i + r) * kWRow + g * 16);
+            if (!MXX && s == 0) wf[0][i] = *(const u32x4*)(wt + (TR * i + r) * kWRow + ((g ^ (r >> 3)) & 1) * 16);
         }
 #pragma unroll
         for (int j = 0; j < HT; ++j)
@@ -388,7 +388,14 @@ __global__ void __launch_bounds__(64 * WM * WN, BM * BN == 128 * 256 ? 4 : 2) mx
         multiply(S3());
     };
 
-    if (!MXX) fetch_scales(0);
+    if (!MXX) {
+        if (nb >= 8) {
+            fetch_scales(0);
+        } else {                                // fewer than eight bytes a row: all that there will be
+#pragma unroll
+            for (int i = 0; i < NT; ++i) sc_next[i] = scales8(wscales + ssrc[i], 0, nb);
+        }
+    }
     if (full > 0) {
         start(stage0, 0);
         finish(stage0);
@@ -536,7 +543,7 @@ hipError_t launch_bf16(const MxMatmulArgs& a, hipStream_t s) {
 }  // namespace
 
 bool mx_gemm_takes(const MxMatmulArgs& a) {
-    return a.K >= kMinTiledK && a.K * 2 < kMaxTiledBytes &&
+    return a.K * 2 < kMaxTiledBytes &&
            (a.x_codes || a.n_experts > 0 || a.M == 1 || a.ldx * 2 < kMaxTiledBytes);
 }
 

@@ -75,7 +75,8 @@ __global__ void __launch_bounds__(64 * W, 2) mx_gemv_kernel(MxMatmulArgs a, int 
     // offsets from the tile's first row (32 bits hold them: kMxMaxK); rows past the tile repeat its last
     const uint8_t* const wbase = a.codes + (expert * a.N + n0) * nb * 16;
     const uint8_t* const sbase = a.scales + (expert * a.N + n0) * nb;
-    auto piece = [&](int l) { return (l & 7) ^ ((l >> 3) & 7); };      // of row l / 8 of eight: see swizzle
+    // of row l / 8 of the i-th eight rows: the piece that lane l brings
+    auto piece = [&](int l, int i) { return (l & 7) ^ swizzle((i & 1) * 8 + (l >> 3)); };
     uint32_t woff[2 * NT];
 #pragma unroll
     for (int i = 0; i < 2 * NT; ++i) {
@@ -84,13 +85,13 @@ __global__ void __launch_bounds__(64 * W, 2) mx_gemv_kernel(MxMatmulArgs a, int 
     }
     const int full = (int)(a.K / kChunk), chunks = (int)((a.K + kChunk - 1) / kChunk);
     const int segs = (chunks + kSegChunks - 1) / kSegChunks;
-    // Row of 128 bytes, 16-byte pieces: piece q of row i sits at q ^ swizzle(i).
-    auto swizzle = [](int i) { return (i & 7) ^ ((i >> 3) & 1); };
+    // Where piece 0 (16 bytes) of token i's 512 bytes sits: the tokens that are read
+    // together, 0-3 and 12-15 a lane group ahead of 4-11, hit different banks (see swizzle).
+    auto token_slot = [](int i) { return (i & 3) | ((i >> 3) & 1) << 2 | (((i >> 3) ^ (i >> 2)) & 1) << 3; };
 
     for (int64_t t0 = begin; t0 < end; t0 += TB) {
         const int count = (int)(end - t0 < TB ? end - t0 : TB);
-        // Two tokens a load: lanes 0..31 and 32..63 bring 512 bytes each; piece q
-        // of token i sits at q ^ i.
+        // Two tokens a load: lanes 0..31 and 32..63 bring 512 bytes each.
         int64_t xoff[TB / 2];
         auto find_x = [&]() {
             // by scalar loads: a vector load would be waited for behind those to LDS
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(64 * W, 2) mx_gemv_kernel(MxMatmulArgs a, int 
                     const uint32_t s = (uint32_t)(lane < 32 ? slot[2 * j] : slot[2 * j + 1]);
                     row = (int64_t)((s < (uint32_t)slots ? s : 0u) / (uint32_t)a.top_k);
                 }
-                xoff[j] = (row * a.ldx + (((lane & 31) ^ i) << 3)) * 2;
+                xoff[j] = (row * a.ldx + (((lane & 31) ^ token_slot(i)) << 3)) * 2;
             }
         };
         const uint8_t* const xcbase = MXX ? a.x_codes + t0 * nb * 16 : nullptr;
@@ -114,7 +115,8 @@ __global__ void __launch_bounds__(64 * W, 2) mx_gemv_kernel(MxMatmulArgs a, int 
         // where the lane's four octets of a token's 128 columns, and its two blocks of a row, sit
         uint32_t xat[4], wat[2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) xat[j] = (uint32_t)((r & (TB - 1)) * 512 + (((4 * g + j) ^ (r & (TB - 1))) << 4));
+        for (int j = 0; j < 4; ++j)
+            xat[j] = (uint32_t)((r & (TB - 1)) * 512 + (((4 * g + j) ^ token_slot(r & (TB - 1))) << 4));
 #pragma unroll
         for (int u = 0; u < 2; ++u) wat[u] = (uint32_t)(r * 128 + (((4 * u + g) ^ swizzle(r)) << 4));
 
@@ -125,7 +127,7 @@ __global__ void __launch_bounds__(64 * W, 2) mx_gemv_kernel(MxMatmulArgs a, int 
             const GlobalBytes cb = scalar_base(wbase + (int64_t)c * 128);
 #pragma unroll
             for (int i = 0; i < 2 * NT; ++i)
-                load_lds16(cb + lane_offset(woff[i] + (uint32_t)((piece(lane) ^ (i & 1)) << 4)), b + i * 1024);
+                load_lds16(cb + lane_offset(woff[i] + (uint32_t)((piece(lane, i)) << 4)), b + i * 1024);
         };
         auto load_x = [&](uint8_t* b, u32x4* xc, uint64_t& xs, int c) {
             if (MXX) {
@@ -164,14 +166,14 @@ __global__ void __launch_bounds__(64 * W, 2) mx_gemv_kernel(MxMatmulArgs a, int 
             } else {
 #pragma unroll
                 for (int j = 0; j < TB / 2; ++j) {
-                    const int q = ((l & 31) ^ (2 * j + (l >> 5))) << 3;
+                    const int q = ((l & 31) ^ token_slot(2 * j + (l >> 5))) << 3;
                     *(u32x4*)(b + kWBytes + j * 1024 + l * 16) =
                         load_x8(a.x + (lane_offset(xoff[j]) >> 1) - q, (int64_t)c * kChunk + q, a.K);
                 }
             }
 #pragma unroll
             for (int i = 0; i < 2 * NT; ++i) {
-                int q = 8 * c + (piece(l) ^ (i & 1));
+                int q = 8 * c + piece(l, i);
                 q = q < nb ? q : nb - 1;
                 load_lds16((GlobalBytes)wbase + lane_offset(woff[i] + (uint32_t)q * 16u), b + i * 1024);
             }

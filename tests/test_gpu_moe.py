@@ -234,6 +234,32 @@ def test_experts_skip_bad_lists(dmm):
     assert (got[3:] == 3).all() and intact(whole)
 
 
+@pytest.mark.parametrize("M,K", [(60, 96), (200, 40), (200, 320)])
+def test_tiled_experts_skip_bad_lists(dmm, M, K):
+    """The same with enough slots for the tiles."""
+    say(f"mx_matmul_experts with bad lists M={M} K={K}")
+    N, E = 140, 3
+    rng = np.random.default_rng(M + K)
+    x = activations(rng, M, K)
+    c, s = packed(rng, E * N, K)
+    w = oracle.mx_unpack(c, s, K).reshape(E, N, K)
+    order = rng.permutation(M).astype(np.int32)
+    bad = rng.random(M) < 0.2
+    order[bad] = rng.choice(np.array([-1, -7, M, M + 1, 2**31 - 1, -2**31], np.int64), bad.sum()).astype(np.int32)
+    offsets = np.array([-3, M // 2, M // 2 + 9, 2 * M], np.int32)
+    whole, y = guarded(M * N, torch.float32)
+    y.fill_(3.0)
+    dmm.mx_matmul_experts(bf16_of(x), dev(c), dev(s), N, y, E, dev(offsets), dev(order), 1)
+    got = host(y).reshape(M, N)
+    for e, at in enumerate((np.arange(M // 2), np.arange(M // 2, M // 2 + 9), np.arange(M // 2 + 9, M))):
+        t = order[at[~bad[at]]]
+        ref, B = oracle.matmul_ref(workloads.bf16_bits(x)[t], w[e])
+        assert_close(got[t], ref, B, K, torch.float32, f"expert {e}")
+    left = np.ones(M, bool)
+    left[order[~bad]] = False
+    assert (got[left] == 3).all() and intact(whole)
+
+
 def test_layer_together(dmm):
     """A whole expert layer: routing, balance loss and gradient, both of the
     experts' products (the second with activations of its own for each slot)

@@ -188,6 +188,9 @@ SHAPES = [
     (300, 1001, 1000, 24, True), (513, 260, 1184, 0, False), (1, 7, 9000, 0, True),
     # enough tiles for the larger ones
     (700, 4300, 330, 0, True), (650, 4404, 1155, 3, False), (1030, 12500, 264, 0, True), (1027, 12403, 577, 1, False),
+    # more than a few tokens of short rows
+    (40, 50, 1, 0, True), (70, 300, 31, 1, False), (130, 260, 63, 0, True), (300, 257, 255, 0, False),
+    (64, 128, 225, 7, True), (650, 4404, 130, 6, False), (1030, 12500, 200, 0, True), (1030, 12500, 64, 0, False),
 ]
 IDS = ["x".join(map(str, s[:3])) for s in SHAPES]
 
@@ -313,6 +316,12 @@ def test_empty_sums(dmm):
     dmm.mx_matmul_mx(torch.empty((3, 0, 16), dtype=torch.uint8, device=DEV),
                      torch.empty((3, 0), dtype=torch.uint8, device=DEV), 3, 0, c, s, 5, y)
     assert not host(y).any()
+    many = torch.full((70, 5), 9.0, device=DEV)
+    dmm.mx_matmul(torch.empty((70, 0), dtype=torch.bfloat16, device=DEV), c, s, 5, many, bias=torch.arange(5.0, device=DEV))
+    assert np.array_equal(host(many), np.tile(np.arange(5, dtype=np.float32), (70, 1)))
+    dmm.mx_matmul_mx(torch.empty((70, 0, 16), dtype=torch.uint8, device=DEV),
+                     torch.empty((70, 0), dtype=torch.uint8, device=DEV), 70, 0, c, s, 5, many)
+    assert not host(many).any()
     dmm.mx_matmul(x[:0], c, s, 5, y[:0])
     dmm.mx_pack(torch.empty((0, 5), device=DEV), torch.empty((0, 1, 16), dtype=torch.uint8, device=DEV),
                 torch.empty((0, 1), dtype=torch.uint8, device=DEV))
