@@ -30,9 +30,15 @@ namespace {
 
 constexpr int kRow = 128;                       // bytes of an LDS tile row (activations; codes with MXFP4 ones)
 constexpr int64_t kMaxTiledBytes = (int64_t)1 << 24;   // of a row in the tiled form: 256 rows fit 32-bit offsets
-constexpr int kWRow = 32;                       // bytes of codes a row with bf16 activations
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// Which slot of W's rows of LANES chunks chunk 0 takes (rows of 128 bytes as the
+// activations'; of rows of 64, four of which fill the banks, likewise).
+template <int LANES>
+__device__ __forceinline__ int w_slot(int row) {
+    return LANES == 8 ? swizzle(row) : ((row >> 2) ^ (row >> 3)) & 3;
+}
 
 // No load and no LDS access of this wave outstanding (expcnt aside), then the
 // workgroup's barrier.
@@ -132,8 +138,9 @@ template <bool MXX, bool DIRECT, int BM, int BN, int WM, int WN, int KD, bool GR
 __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a) {
     constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
     constexpr int kUnit = MXX ? 256 : 64, kSlab = KD * kUnit;
-    constexpr int kXUnit = BM * kRow, kWUnit = BN * (MXX ? kRow : kWRow);   // bytes of a unit
-    constexpr int kXBytes = KD * kXUnit, kWBytes = KD * kWUnit;
+    constexpr int kWRow = MXX ? kRow : KD * 32;         // bytes of W's rows in LDS: a unit, or with bf16 activations a slab
+    constexpr int kXUnit = BM * kRow, kWUnit = BN * kRow;
+    constexpr int kXBytes = KD * kXUnit, kWBytes = BN * (kSlab / 2);
     constexpr int kSRow = 8 * KD, kSBytes = MXX ? (BM + BN) * kSRow : 0;
     constexpr int kStage = kXBytes + kWBytes + kSBytes;
     constexpr int TR = MXX ? 16 : 32;           // rows of a matrix instruction's tile
@@ -142,7 +149,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a
     constexpr int kXLoads = kXBytes / 1024 / kWaves, kWLoads = kWBytes / 1024 / kWaves;
     constexpr bool kOneWave = kWaves <= 4 && 2 * (2 * kStage + (GROUPED ? 256 : 0)) > 160 * 1024;   // a SIMD
     static_assert(kXLoads * 1024 * kWaves == kXBytes && kWLoads * 1024 * kWaves == kWBytes, "whole loads");
-    static_assert(kXUnit % 1024 == 0 && kWUnit % 1024 == 0 && kXLoads % KD == 0, "a load stays in a unit");
+    static_assert(kXUnit % 1024 == 0 && kXLoads % KD == 0, "a load stays in a unit");
+    static_assert(MXX || KD == 2 || KD == 4, "w_slot");
     static_assert(!MXX || BM + BN <= kThreads, "a thread for each row's scales");
     __shared__ __attribute__((aligned(1024))) uint8_t stage0[kStage];
     __shared__ __attribute__((aligned(1024))) uint8_t stage1[kStage];
@@ -184,18 +192,18 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a
     // l % 2 of row l / 2).  Load j of wave w is row group (w kXLoads + j) of all of
     // the slab's units; a wave's row groups repeat from unit to unit.
     const int x_sub = lane >> 3;
-    constexpr int kXGroups = kXUnit / 1024, kWGroups = kWUnit / 1024;
-    auto x_group = [&](int j) { return wave + (j % (kXLoads / KD)) * kWaves; };         // of kXGroups
+    auto x_group = [&](int j) { return wave + (j % (kXLoads / KD)) * kWaves; };
     auto x_unit = [&](int j) { return j / (kXLoads / KD); };
     auto x_chunk = [&](int j) { return (lane & 7) ^ swizzle(x_group(j) * 8 + x_sub); };
-    // W's groups are dealt over the whole slab (a unit may have fewer than there are waves)
+    // W's loads are dealt over the whole slab (a unit may have fewer than there are
+    // waves).  Whole lines of the rows' codes, as far as a slab has them: with bf16
+    // activations a unit is only 32 bytes of a row, and loads of such pieces cost as
+    // much as loads of lines.
+    constexpr int kWLanes = kWRow / 16, kWRows = 64 / kWLanes, kWGroups = BN / kWRows;  // lanes a row, rows a load
     auto w_all = [&](int j) { return wave + j * kWaves; };
-    auto w_group = [&](int j) { return w_all(j) % kWGroups; };
-    auto w_unit = [&](int j) { return w_all(j) / kWGroups; };
-    // (the halves of W's 32-byte rows change places every eight rows: see swizzle)
-    auto w_chunk = [&](int j) {
-        return MXX ? (lane & 7) ^ swizzle(w_group(j) * 8 + x_sub) : (lane & 1) ^ ((lane >> 4) & 1);
-    };
+    auto w_tile_row = [&](int j) { return w_all(j) % kWGroups * kWRows + lane / kWLanes; };
+    auto w_unit = [&](int j) { return MXX ? w_all(j) / kWGroups : 0; };
+    auto w_chunk = [&](int j) { return (lane & (kWLanes - 1)) ^ w_slot<kWLanes>(w_tile_row(j)); };
     // Offsets from the tile's first row fit 32 bits (mx_gemm_takes); the rows of a list have 64.
     typedef typename std::conditional<GROUPED, int64_t, uint32_t>::type XOffset;
     const uint8_t* const xbase = MXX ? a.x_codes + p.m0 * nb * 16 : (const uint8_t*)(a.x + (GROUPED ? 0 : p.m0) * a.ldx);
@@ -208,8 +216,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a
     uint32_t wsrc[kWLoads];
 #pragma unroll
     for (int j = 0; j < kWLoads; ++j) {
-        const int row = MXX ? w_group(j) * 8 + x_sub : w_group(j) * 32 + (lane >> 1);
-        wsrc[j] = lane_offset((uint32_t)w_row(row) * ((uint32_t)nb * 16u) + (uint32_t)(w_chunk(j) * 16 + w_unit(j) * (kUnit / 2)));
+        wsrc[j] = lane_offset((uint32_t)w_row(w_tile_row(j)) * ((uint32_t)nb * 16u) + (uint32_t)(w_chunk(j) * 16 + w_unit(j) * (kUnit / 2)));
     }
     // Scales.  MXX: thread tid stages a slab's bytes of one row of W (the first BN
     // threads) or x.  Otherwise lane (r, g) keeps eight bytes, the scales of four
@@ -292,7 +299,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a
     int sw[NT], sx[MT];
     auto read = [&](const uint8_t* st, int k, int s) {
         const uint8_t* const xt = st + k * kXUnit + wm * (BM / WM) * kRow;
-        const uint8_t* const wt = st + kXBytes + k * kWUnit + wn * (BN / WN) * (MXX ? kRow : kWRow);
+        const uint8_t* const wt = st + kXBytes + (MXX ? k * kWUnit : 0) + wn * (BN / WN) * kWRow;
         const int at = r * kRow + (((MXX ? 4 * (s >> 1) + g : 4 * g + s) ^ swizzle(r)) << 4);
         if (MXX && s == 0) {
             const uint8_t* const ws = st + kXBytes + kWBytes + wn * (BN / WN) * kSRow + 8 * k;
@@ -305,7 +312,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             if (MXX && s % 2 == 0) wf[s >> 1][i] = *(const u32x4*)(wt + TR * i * kRow + at);
-            if (!MXX && s == 0) wf[0][i] = *(const u32x4*)(wt + (TR * i + r) * kWRow + ((g ^ (r >> 3)) & 1) * 16);
+            if (!MXX && s == 0) wf[0][i] = *(const u32x4*)(wt + (TR * i + r) * kWRow + (((2 * k + g) ^ w_slot<kWLanes>(r)) << 4));
         }
 #pragma unroll
         for (int j = 0; j < HT; ++j)
