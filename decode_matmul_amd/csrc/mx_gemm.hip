@@ -247,13 +247,13 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a
 #pragma unroll
         for (int j = 0; j < kXLoads; ++j) *(u32x4*)(st + x_lds(j) + lane * 16) = xr[j];
     };
-    uint64_t sreg[KD];                          // MXX: scales on their way
+    typedef uint32_t Scales __attribute__((ext_vector_type(2 * KD)));
+    typedef Scales ScalesAt __attribute__((aligned(1)));
+    Scales sreg;                                // MXX: scales on their way
     auto start = [&](uint8_t* st, int64_t t) {  // slab t, a whole one
         if (MXX) {
             const GlobalBytes sb = scalar_base((stages_w ? wscales : xscales) + t * kSRow);
-#pragma unroll
-            for (int k = 0; k < KD; ++k)
-                sreg[k] = *(const __attribute__((address_space(1))) u64u*)(sb + lane_offset(ssrc[0]) + 8 * k);
+            sreg = *(const __attribute__((address_space(1))) ScalesAt*)(sb + lane_offset(ssrc[0]));
         }
         const GlobalBytes xb = scalar_base(xbase + t * (KD * kRow));
         const GlobalBytes wb = scalar_base(wbase + t * (kSlab / 2));
@@ -267,10 +267,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a
         for (int j = 0; j < kWLoads; ++j) load_lds16(wb + lane_offset(wsrc[j]), st + w_lds(j));
     };
     auto finish = [&](uint8_t* st) {            // what came to registers
-        if (MXX && tid < BM + BN) {
-#pragma unroll
-            for (int k = 0; k < KD; ++k) *(uint64_t*)(st + kXBytes + kWBytes + tid * kSRow + 8 * k) = sreg[k];
-        }
+        if (MXX && tid < BM + BN) *(Scales*)(st + kXBytes + kWBytes + tid * kSRow) = sreg;
         if (!DIRECT) store_x(st);
     };
     const int64_t last8 = nb > 8 ? nb - 8 : 0;
