@@ -2,24 +2,28 @@
 //
 // Mathematics.  As in mx_gemv.hip, a lane's 16 code bytes are the operand of
 // the 16x16x128 scaled matrix instruction (MXFP4 activations), and four
-// scaled conversions turn eight codes into eight exact bf16 values for the
-// 16x16x32 bf16 instruction (bf16 activations).  Any order of k may be taken
-// that is the same for both operands: with bf16 activations lane group g takes
-// octets 2 g and 2 g + 1 of each 64-wide slab, so its codes are 8 consecutive
-// bytes and one scale.
+// scaled conversions turn eight codes into eight exact bf16 values, here for the
+// 32x32x16 bf16 instruction (bf16 activations).  Any order of k may be taken
+// that is the same for both operands: with bf16 activations lane half g takes
+// block g of each 64-wide unit, octet s in step s, so its codes are 16
+// consecutive bytes and one scale.
 //
 // Mapping.  A workgroup owns BM tokens x BN rows of W, its waves equal parts of
 // that (the largest tile: 256 x 256, 8 waves of 128 x 64, 128 accumulators a
 // lane).  W is the first operand, so a lane ends with four consecutive n of one
 // token.  K is cut into slabs, which take turns in two LDS arrays: distinct
 // ones, so the compiler can tell a load in flight to one from the reads of the
-// other.  Activations' rows are 128 bytes a unit (64 bf16 or 256 codes), W's 128
-// or 32, and go from global memory straight to LDS, a slab ahead; fragments go
-// to registers a step ahead.  Chunk c (16 bytes) of a 128-byte row r sits at slot
-// c ^ swizzle(r), which spreads the 16 rows of a fragment read over all banks.
+// other.  Rows go from global memory straight to LDS in whole lines of 128 bytes
+// (64 bf16 or 256 codes; slabs of 128 columns have 64 bytes of codes), a slab
+// ahead; fragments go to registers a step ahead.  Chunks (16 bytes) change places
+// within their rows so that a fragment read hits all banks (swizzle, w_slot).
 //
-// Bound: the matrix instructions for the largest tile, the slabs' way from L2
-// (and its latency, where a compute unit has one tile) for the smaller ones.
+// Bound.  The largest tile: the matrix instructions and the power they draw
+// (bf16 2048 x 8192 x 8192: 1.3 PFLOP/s at 2.1 GHz; MXFP4 activations: with the
+// loads left out 62 of 75 us remain, and the same instructions from registers
+// alone reach 7.3 PFLOP/s).  Smaller tiles: what a compute unit can have under
+// way, about 40 KB, against the latency of memory: 64 x 64 tiles take 1.1 us a
+// slab of 40 KB whether K is dealt to one group of waves or to two.
 #include <type_traits>
 
 #include "mx.h"
@@ -552,24 +556,26 @@ bool mx_gemm_takes(const MxMatmulArgs& a) {
 }
 
 // The largest tile that still gives every compute unit one (its rate is the
-// highest, 1.2 PFLOP/s with bf16 and 3.5 with MXFP4 activations, but a wave of
-// tiles costs its time whether it fills the chip or not).  us by tile:
+// highest, 1.3 PFLOP/s with bf16 and 3.6 with MXFP4 activations, but a wave of
+// tiles costs its time whether it fills the chip or not).  us by tile, in one run:
 //   bf16    256 x 256 / 128 x 128 / 64 x 64
-//     M = 2048, 8192 x 8192   221 /  242 /  353
-//     M = 1024, 4096 x 4096    90 /   41 /   46
-//     M =  512, 4096 x 4096    89 /   37 /   26
-//     M =   64, 8192 x 8192   158 /   69 /   37
+//     M = 2048, 8192 x 8192   237 /  269 /  366
+//     M = 1024, 4096 x 4096    89 /   43 /   52
+//     M =  512, 4096 x 4096    88 /   37 /   27
+//     M =   64, 8192 x 8192   155 /   66 /   36
 //   MXFP4
-//     M = 2048, 8192 x 8192    79 /  108 /  176
-//     M = 1024, 4096 x 4096    38 /   21 /   26
-//     M =  512, 4096 x 4096    37 /   19 /   15
-// Experts: by the slots an expert has on average, 32 x 128 / 64 x 256 / 128 x 256
+//     M = 2048, 8192 x 8192    83 /  106 /  159
+//     M = 1024, 4096 x 4096    37 /   19 /   24
+//     M =  512, 4096 x 4096    36 /   17 /   13
+// Experts: by the slots an expert has on average, 32 x 128 / 64 x 256
 //     (64 experts of 2048 x 4096)
-//     25   102 / 122 / 132       251   444 / 350 / 350
+//     32   109 / 116     48   127 / 112     256   435 / 331
+// (four waves of 64 x 64 a tile of 64 x 256; eight of 32 x 64 took 348 where they
+// take 326, tiles of 128 x 256 took 333 there and 181 against 134 at 64 slots).
 hipError_t launch_mx_gemm(const MxMatmulArgs& a, hipStream_t s) {
     if (a.n_experts > 0)
-        return a.M * a.top_k < 48 * (int64_t)a.n_experts ? launch_bf16<32, 128, 1, 4, 4, true>(a, s)
-                                                         : launch_bf16<64, 256, 2, 4, 2, true>(a, s);
+        return a.M * a.top_k < 40 * (int64_t)a.n_experts ? launch_bf16<32, 128, 1, 4, 4, true>(a, s)
+                                                         : launch_bf16<64, 256, 1, 4, 2, true>(a, s);
     const int64_t cus = compute_unit_count();
     auto tiles = [&](int64_t side) { return ((a.M + side - 1) / side) * ((a.N + side - 1) / side); };
     if (4 * tiles(256) >= 3 * cus)

@@ -342,11 +342,18 @@ hipError_t launch_bf16(const MxMatmulArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_mx_matmul(const MxMatmulArgs& a, hipStream_t s) {
-    // Passes of 16 tokens are as fast as tiles up to two of them (M = 32, 8192 x
-    // 8192: 22.3 us against 33.5; M = 64: 38.8 against 37.5), and for experts up to
-    // about six slots each (64 experts of 2048 x 4096: 65 us against 72 at 4 slots,
-    // 84 against 76 at 8).
-    const bool many = a.n_experts > 0 ? a.M * a.top_k >= 6 * (int64_t)a.n_experts : a.M > 32;
+    const int64_t tiles = (a.N + 15) / 16, cus = compute_unit_count();
+    // Passes of 16 tokens against the tiled form, whose 64 x 64 tiles leave compute
+    // units idle where N is small (us, tiled from the second figure on):
+    //   bf16   8192 x 8192   M = 32: 22 / 35     4096 x 4096   M = 48: 13.5 / 15.9
+    //                                           4096 x 14336  M = 48: 36 / 54
+    //   MXFP4  8192 x 8192   M = 32: 21 / 19     4096 x 4096   M = 32: 8.8 / 8.4
+    //         14336 x 4096   M = 17: 15 / 12     4096 x 14336  M = 32: 18 / 30
+    // and for experts up to about six slots each (64 experts of 2048 x 4096: 65 us
+    // against 72 at 4 slots, 84 against 76 at 8).
+    const bool wide = tiles >= 2 * cus;
+    const int64_t few = a.x_codes ? (wide ? 16 : 32) : wide ? 32 : 48;
+    const bool many = a.n_experts > 0 ? a.M * a.top_k >= 6 * (int64_t)a.n_experts : a.M > few;
     if (many && mx_gemm_takes(a)) return launch_mx_gemm(a, s);
     if (a.n_experts > 0)
         return launch_bf16<8, 2, 4, true>(a, s);
@@ -357,7 +364,6 @@ hipError_t launch_mx_matmul(const MxMatmulArgs& a, hipStream_t s) {
     //   M = 1:  (1, 8) 10.3 / 10.6 / 5.2   (2, 4)  9.3 / 12.1 / 6.2   (4, 4) 11.3 / 21.5 / 11.0
     //   M = 8:  (1, 8) 18.1 / 14.8 / 5.5   (2, 8) 13.2 / 12.0 / 6.1   (2, 4) 10.6 / 13.0 / 6.7
     //   M = 16: (1, 4) 24.3 / 20.9 / 6.9   (2, 4) 16.2 / 14.9 / 7.5   (4, 4) 12.4 / 17.8 / 9.2
-    const int64_t tiles = (a.N + 15) / 16, cus = compute_unit_count();
     if (a.x_codes)
         return tiles <= 2 * cus ? launch<true, 16, 1, 8, true, false>(a, s) : launch<true, 16, 2, 4, true, false>(a, s);
     if (a.M <= 2) return tiles <= 2 * cus ? launch_bf16<2, 1, 8, false>(a, s) : launch_bf16<2, 2, 4, false>(a, s);
