@@ -74,6 +74,7 @@ __device__ bool place_grouped(const MxMatmulArgs& a, Place& p) {
         const int o = a.offsets[e];
         return o < 0 ? 0 : (o > slots ? slots : o);
     };
+    if (tid == 0) found[2] = -1;
     int total = 0;
     for (int e0 = 0; e0 < a.n_experts; e0 += kThreads) {
         const int e = e0 + tid;
@@ -128,6 +129,7 @@ __device__ bool place_grouped(const MxMatmulArgs& a, Place& p) {
         }
         __syncthreads();
     }
+    if (readfirstlane(found[2]) < 0) return false;  // overlapping lists can have more tiles than an int counts
     p.m0 = readfirstlane(found[0]);
     const int64_t last = readfirstlane(found[1]);
     p.m_end = last < p.m0 + BM ? last : p.m0 + BM;

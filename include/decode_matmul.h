@@ -485,8 +485,9 @@ int mx_pack(const void* W, int32_t w_dtype, int64_t rows, int64_t K, int64_t ldw
 
 /*
  * mx_unpack -- decode an MXFP4 package to W_out [rows, K] of out_dtype, row r
- * at element r * K.  Both TQ_F32 and TQ_BF16 hold every value exactly (4 or 6
- * times 2^127, which neither holds, becomes an infinity).
+ * at element r * K.  Both TQ_F32 and TQ_BF16 hold every value exactly (2, 3, 4
+ * and 6 times 2^127, which neither holds and mx_pack never writes, become
+ * infinities).
  *
  *  d_status  device int32, or NULL for no report; set to 0, then
  *            TQ_DATA_RANGE if a block is NaN (s = 255), TQ_DATA_PADDING if a
@@ -507,11 +508,12 @@ int mx_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t
  *  y       device [M, N] of y_dtype (fp32, or bf16 nearest-even of the fp32
  *          result).
  *
- * Every weight is exact in bf16 and every product in fp32; sums are held in
+ * Every weight mx_unpack holds is exact in bf16 and every product in fp32; sums are held in
  * fp32, in an order fixed by the shape (two calls give the same bits).  A NaN
  * block makes its output column NaN.  What x holds past K, and codes past K,
  * take no part.  M = 0 or N = 0 is a no-op; with K = 0, x and the package may
- * be NULL and y = bias (or 0).  M and N are below 2^31, K is below 2^27.
+ * be NULL and y = bias (or 0).  M and N are below 2^31, K is below 2^27; sizes
+ * that need more than 2^32 - 1 threads (N of 2^29 and more) are TQ_ERR_SHAPE.
  */
 int mx_matmul(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint8_t* codes,
               const uint8_t* scales, int64_t N, const float* bias, void* y, int32_t y_dtype,

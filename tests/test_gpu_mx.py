@@ -346,6 +346,81 @@ def test_activations_at_any_offset(dmm, M):
         assert_close(host(y), ref, B, K, torch.float32, f"offset {off}")
 
 
+@pytest.mark.parametrize("M", [1, 4, 16, 33, 130])
+@pytest.mark.parametrize("K", [512, 1024, 8704, 700])
+def test_scales_at_any_offset(dmm, M, K):
+    """Scale bytes that start anywhere give the same bits as aligned ones."""
+    say(f"scales' offsets M={M} K={K}")
+    N, nb = 70, -(-K // 32)
+    rng = np.random.default_rng(M + K)
+    x = activations(rng, M, K)
+    c, s = packed(rng, N, K)
+    X, C = bf16_of(x), dev(c)
+    xc, xs = packed(rng, M, K)
+    XC = dev(xc)
+    first = {}
+    for off in (0, 1, 8, 15):
+        S, XS = (torch.full((n * nb + off,), 200, dtype=torch.uint8, device=DEV)[off:].view(n, nb) for n in (N, M))
+        S.copy_(dev(s))
+        XS.copy_(dev(xs))
+        y = torch.empty((2, M, N), device=DEV)
+        dmm.mx_matmul(X, C, S, N, y[0])
+        dmm.mx_matmul_mx(XC, XS, M, K, C, S, N, y[1])
+        got = host(y)
+        if off == 0:
+            ref, B = oracle.matmul_ref(workloads.bf16_bits(x), oracle.mx_unpack(c, s, K))
+            assert_close(got[0], ref, B, K, torch.float32, "aligned")
+            first = got
+        assert np.array_equal(got, first), off
+
+
+@pytest.mark.parametrize("M", [2, 60])
+def test_far_rows(dmm, M):
+    """Rows of x a long way apart: offsets past 2^31 bytes, x's rows past
+    what the tiles' 32-bit offsets take."""
+    say(f"far rows M={M}")
+    K, N, ld = 64, 40, 9000001
+    rng = np.random.default_rng(M)
+    x = activations(rng, M, K)
+    c, s = packed(rng, N, K)
+    ref, B = oracle.matmul_ref(workloads.bf16_bits(x), oracle.mx_unpack(c, s, K))
+    for step in (ld, 60000000 if M == 2 else 30000000):
+        buf = torch.full(((M - 1) * step + K,), float("nan"), dtype=torch.bfloat16, device=DEV)
+        xo = buf.as_strided((M, K), (step, 1))
+        xo.copy_(bf16_of(x))
+        y = torch.empty((M, N), device=DEV)
+        dmm.mx_matmul(xo, dev(c), dev(s), N, y)
+        assert_close(host(y), ref, B, K, torch.float32, f"rows {step} apart")
+        xc, xs = (torch.zeros(sh, dtype=torch.uint8, device=DEV) for sh in dmm.mx_shape(M, K))
+        dmm.mx_pack(xo, xc, xs)
+        pc, ps = oracle.mx_pack(x)[:2]
+        assert np.array_equal(xc.cpu().numpy(), pc) and np.array_equal(xs.cpu().numpy(), ps)
+
+
+def test_two_streams_at_once(dmm):
+    """Calls on two streams, each with its own tensors, that may run together."""
+    say("two streams")
+    rng = np.random.default_rng(8)
+    jobs = []
+    for M, N, K in ((5, 4000, 2048), (300, 1000, 1024)):
+        x = activations(rng, M, K)
+        c, s = packed(rng, N, K)
+        jobs.append((bf16_of(x), dev(c), dev(s), N, torch.empty((M, N), device=DEV), torch.cuda.Stream()))
+    alone = []
+    for X, C, S, N, y, _ in jobs:
+        dmm.mx_matmul(X, C, S, N, y)
+        alone.append(host(y))
+        y.zero_()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for X, C, S, N, y, stream in jobs:
+            with torch.cuda.stream(stream):
+                dmm.mx_matmul(X, C, S, N, y)
+    torch.cuda.synchronize()
+    for (_, _, _, _, y, _), a in zip(jobs, alone):
+        assert np.array_equal(host(y), a)
+
+
 def test_large_offsets(dmm):
     """Rows whose codes lie past 2^31 bytes, and outputs past 2^31 elements' bytes."""
     say("large offsets")
