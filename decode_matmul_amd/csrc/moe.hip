@@ -192,12 +192,13 @@ __global__ void __launch_bounds__(kScanThreads) route_scan_kernel(int32_t* cc, i
 
 // ---------------------------------------------------------------- balance
 //
-// With c'_e = E c_e / n the loss is the sum over tokens of s_t / T, s_t = sum_e
-// c'_e p_te, so tokens and T are counted in one pass; w = c' / T, and the gradient
-// of s_t is p_te (w_e - s_t) with that w.  A row's E logits lie with L lanes (a
-// power of two, 64 / L rows a wave at a time), eight consecutive ones each, read
-// once; the maximum and the two sums are exchanged among the L lanes.
-// Bound: the logits' bytes, and the launches for few tokens.
+// The loss is E / (n T) times the sum over tokens of s_t = sum_e c_e p_te, so
+// tokens, T and n are counted in one pass, and the gradient of a token's part is
+// p_te (w_e - sum_j w_j p_tj) with w = E c / (n T).  A row's E logits lie with L
+// lanes (a power of two, 64 / L rows a wave at a time), eight consecutive ones each,
+// read once; the maximum and the two sums are exchanged among the L lanes.
+// Bound: about as many vector instructions as the logits' bytes take time (65536
+// x 128 bf16: a dozen for each logit); the launches for few tokens.
 constexpr int kBalThreads = 256;
 constexpr int kBalWaves = kBalThreads / 64;
 
@@ -223,7 +224,7 @@ __device__ __forceinline__ float over_group(float v, F f) {
 
 template <int L>
 __device__ __forceinline__ float group_max(float v) {
-    return over_group<L>(v, [](float a, float b) { return fmaxf(a, b); });
+    return over_group<L>(v, [](float a, float b) { return __builtin_elementwise_maximum(a, b); });
 }
 
 template <int L>
@@ -237,19 +238,22 @@ __device__ __forceinline__ double wave_sum(double v) {
     return v;
 }
 
-// Eight weights from w[0] on, `have` of them there; the others are 0.
-__device__ __forceinline__ void load_weights(const float* w, int have, float* v) {
+// Eight weights or counts (within 2^-24) from w[0] on, `have` of them there; the others are 0.
+template <class T>
+__device__ __forceinline__ void load_weights(const T* w, int have, float* v) {
+    typedef T Four __attribute__((ext_vector_type(4)));
+    typedef Four FourAt __attribute__((aligned(4)));
     if (have >= 8) {
-        const f32x4 a = *(const f32x4a*)w, b = *(const f32x4a*)(w + 4);
+        const Four a = *(const FourAt*)w, b = *(const FourAt*)(w + 4);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            v[i] = a[i];
-            v[4 + i] = b[i];
+            v[i] = (float)a[i];
+            v[4 + i] = (float)b[i];
         }
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < have ? w[i] : 0.f;
+    for (int i = 0; i < 8; ++i) v[i] = i < have ? (float)w[i] : 0.f;
 }
 
 // Eight logits at p, `have` of them there; the others are -inf.
@@ -281,47 +285,35 @@ __device__ __forceinline__ void load_logits(const void* base, int64_t at, int ha
     }
 }
 
-// A row's softmax, in place of its logits, and sum_e w_e p_e.  Rows of -inf give p = 0.
+// A row's logits to e = exp(z - top), 1 / sum e and sum w p.  False for a row of
+// -inf only, which has no softmax.  The maximum is the one that keeps a NaN, which
+// then takes the whole row; so does an infinity (inf - inf).
 template <int L>
-__device__ __forceinline__ float row_softmax(float* p, const float* w) {
-    float top = -__builtin_inff();
-    bool nan = false;
+__device__ __forceinline__ bool row_softmax(float* e, const float* w, float& inv, float& s) {
+    float top = e[0];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        nan |= p[i] != p[i];
-        top = fmaxf(top, p[i]);
-    }
-    if (nan) top = __builtin_inff();            // inf - inf: every p of the row becomes NaN
+    for (int i = 1; i < 8; ++i) top = __builtin_elementwise_maximum(top, e[i]);
     top = group_max<L>(top);
     float sum = 0.f, ws = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         // off by about (top - z) 2^-24 of itself, the rounding of its argument, and a unit
-        p[i] = __builtin_amdgcn_exp2f((p[i] - top) * 1.44269504088896340736f);
-        sum += p[i];
-        ws += w[i] * p[i];
+        e[i] = __builtin_amdgcn_exp2f((e[i] - top) * 1.44269504088896340736f);
+        sum += e[i];
+        ws = __builtin_fmaf(w[i], e[i], ws);
     }
-    sum = group_sum<L>(sum);
-    ws = group_sum<L>(ws);
-    if (top == -__builtin_inff()) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] = 0.f;
-        return 0.f;
-    }
-    if (top == __builtin_inff()) sum = __builtin_nanf("");
-    const float inv = 1.f / sum;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] *= inv;
-    return ws * inv;
+    inv = __builtin_amdgcn_rcpf(group_sum<L>(sum));     // a unit off
+    s = group_sum<L>(ws) * inv;
+    return top != -__builtin_inff();
 }
 
-// loss and weights from the sum over tokens, their number, and the counts.
+// loss and weights from the sum of s_t over tokens, their number T, and the counts, whose sum is n.
 __device__ __forceinline__ void finish_balance(double sum, int64_t T, double n, int E, const int32_t* counts,
                                                float* loss, float* weights) {
     const bool some = T > 0 && n > 0.0;
     for (int e = (int)threadIdx.x; e < E; e += kBalThreads)
         weights[e] = some ? (float)((double)E * ((double)counts[e] / n) / (double)T) : 0.f;
-    if (threadIdx.x == 0) loss[0] = some ? (float)(sum / (double)T) : 0.f;
+    if (threadIdx.x == 0) loss[0] = some ? (float)(sum / (double)T * ((double)E / n)) : 0.f;
 }
 
 // Tokens of a workgroup of the loss: kTokens for each group of L lanes, all of
@@ -338,7 +330,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_loss_kernel(const void* l
     __shared__ double part[3][kBalWaves];
     const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
     const int e0 = (lane % L) * 8, have = E - e0;
-    float z[kTokens][8];
+    float z[kTokens][8], w[8];
     bool live[kTokens];
     const int64_t t0 = (int64_t)blockIdx.x * loss_rows(L) + (int)threadIdx.x / L;
 #pragma unroll
@@ -348,47 +340,38 @@ __global__ void __launch_bounds__(kBalThreads) balance_loss_kernel(const void* l
         load_logits<BF16>(logits, live[i] ? t * ldl + e0 : 0, live[i] ? have : 0, z[i]);
         if (mask && live[i]) live[i] = mask[t] != 0;
     }
-    __shared__ float wt[kMoeMaxExperts];
-    double n = 0.0;
-    for (int e = (int)threadIdx.x; e < E; e += kBalThreads) {
-        n += (double)counts[e];
-        wt[e] = (float)counts[e];               // within 2^-24, like the other factors of a weight here
-    }
-    n = wave_sum(n);
-    if (lane == 0) part[2][wave] = n;
-    __syncthreads();
-    n = 0.0;
-    for (int i = 0; i < kBalWaves; ++i) n += part[2][i];
-    float w[8];
-    const float scale = n > 0.0 ? (float)((double)E / n) : 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = i < have ? scale * wt[e0 + i] : 0.f;
-    double sum = 0.0, tokens = 0.0;
+    load_weights(counts + e0, have, w);
+    double sum = 0.0;
+    int tokens = 0;
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) {
-        const float s = row_softmax<L>(z[i], w);
-        if (live[i] && lane % L == 0) {
-            sum += (double)s;
-            tokens += 1.0;
-        }
+        float inv, s;
+        if (row_softmax<L>(z[i], w, inv, s) && live[i]) sum += (double)s;
+        tokens += __popcll(__ballot(live[i] && lane % L == 0));
     }
-    sum = wave_sum(sum);
-    tokens = wave_sum(tokens);
+#pragma unroll
+    for (int d = 32; d >= L; d >>= 1) sum += __shfl_xor(sum, d);        // the lanes of a row have the same
     if (lane == 0) {
         part[0][wave] = sum;
-        part[1][wave] = tokens;
+        part[1][wave] = (double)tokens;
+    }
+    const bool only = gridDim.x == 1;
+    if (only) {
+        double n = 0.0;
+        for (int e = (int)threadIdx.x; e < E; e += kBalThreads) n += (double)counts[e];
+        n = wave_sum(n);
+        if (lane == 0) part[2][wave] = n;
     }
     __syncthreads();
-    sum = tokens = 0.0;
-    for (int i = 0; i < kBalWaves; ++i) {
-        sum += part[0][i];
-        tokens += part[1][i];
-    }
-    if (gridDim.x == 1) {
-        finish_balance(sum, (int64_t)tokens, n, E, counts, loss, weights);
+    double v[3] = {0.0, 0.0, 0.0};
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+        for (int i = 0; i < kBalWaves && (k < 2 || only); ++i) v[k] += part[k][i];
+    if (only) {
+        finish_balance(v[0], (int64_t)v[1], v[2], E, counts, loss, weights);
     } else if (threadIdx.x == 0) {
-        partial[2 * (int64_t)blockIdx.x] = sum;
-        partial[2 * (int64_t)blockIdx.x + 1] = tokens;
+        partial[2 * (int64_t)blockIdx.x] = v[0];
+        partial[2 * (int64_t)blockIdx.x + 1] = v[1];
     }
 }
 
@@ -429,9 +412,15 @@ __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const void* l
     load_logits<BF16>(logits, t * ldl + e0, have, p);
     load_weights(weights + e0, have, w);
     const bool live = !mask || mask[t] != 0;
-    const float up = dloss[0], s = row_softmax<L>(p, w);
+    float inv, s;
+    const bool some = row_softmax<L>(p, w, inv, s);
+    const float up = dloss[0] * inv;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = live ? up * p[i] * (w[i] - s) : 0.f;
+    for (int i = 0; i < 8; ++i) p[i] = up * p[i] * (w[i] - s);
+    if (!(some && live)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = 0.f;
+    }
     const int64_t at = t * E + e0;
     if (BF16) {
         uint16_t* const d = (uint16_t*)dlogits + at;
