@@ -38,16 +38,6 @@ __device__ __forceinline__ int expert_of(const int32_t* ids, int64_t slot, int64
     return id >= 0 && id < E ? id : E;
 }
 
-// Lanes of the wave with this lane's id (0 <= id <= E), out of those in `live`.
-__device__ __forceinline__ uint64_t same_id(int id, uint64_t live, int bits) {
-    uint64_t m = live;
-    for (int b = 0; b < bits; ++b) {
-        const uint64_t v = __ballot((id >> b) & 1);
-        m &= ((id >> b) & 1) ? v : ~v;
-    }
-    return m;
-}
-
 // Exclusive sums of v over the workgroup's threads, and the sum of all; `sums`
 // holds kRouteWaves words and is free again after the next barrier.
 __device__ __forceinline__ int exclusive_sum(int v, int* sums, int& all) {
@@ -87,40 +77,54 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const int32_
     int id[kRows], rank[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) id[i] = expert_of(ids, first + 64 * i, slots, E);
+    // expert e's slots in all chunks, and in earlier ones
+    auto gather = [&](int e, int& total, int& earlier) {
+        total = earlier = 0;
+        if (e > E) return;
+        if (MODE == kOnly) {
+#pragma unroll
+            for (int w = 0; w < kRouteWaves; ++w) total += lds[w * (E + 1) + e];
+        } else if (MODE == kSummed) {
+#pragma unroll 8
+            for (int c = 0; c < chunks; ++c) {
+                const int v = cc[c * (E + 1) + e];
+                total += v;
+                if (c < (int)blockIdx.x) earlier += v;
+            }
+        } else {
+            total = cc[(int64_t)chunks * (E + 1) + e];
+            earlier = cc[(int64_t)blockIdx.x * (E + 1) + e];
+        }
+    };
+    int total = 0, earlier = 0;
+    if (MODE != kOnly) gather(tid, total, earlier);         // on its way meanwhile
+    // lanes of the wave with this lane's id, in each row
+    uint64_t same[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) same[i] = __ballot(id[i] >= 0);
+    for (int b = 0; b < bits; ++b)
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const bool one = (id[i] >> b) & 1;
+            const uint64_t v = __ballot(one);
+            same[i] &= one ? v : ~v;
+        }
     for (int i = tid; i < kRouteWaves * (E + 1); i += kRouteThreads) lds[i] = 0;
     __syncthreads();
     // volatile: a row's places are read after the row before wrote them, by other lanes of the wave
     volatile int* const mine = lds + wave * (E + 1);
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-        const uint64_t same = same_id(id[i], __ballot(id[i] >= 0), bits);
-        const int below = __popcll(same & ((1ull << lane) - 1ull));
+        const int below = __popcll(same[i] & ((1ull << lane) - 1ull));
         const int base = id[i] >= 0 ? mine[id[i]] : 0;
         rank[i] = base + below;
-        if (id[i] >= 0 && below == 0) mine[id[i]] = base + __popcll(same);
+        if (id[i] >= 0 && below == 0) mine[id[i]] = base + __popcll(same[i]);
     }
     __syncthreads();
     int carry = 0;                              // slots of the experts below e0
     for (int e0 = 0; e0 <= E; e0 += kRouteThreads) {
-        // expert e's slots in all chunks, and in earlier ones
         const int e = e0 + tid;
-        int total = 0, earlier = 0;
-        if (e <= E) {
-            if (MODE == kOnly) {
-#pragma unroll
-                for (int w = 0; w < kRouteWaves; ++w) total += lds[w * (E + 1) + e];
-            } else if (MODE == kSummed) {
-#pragma unroll 8
-                for (int c = 0; c < chunks; ++c) {
-                    const int v = cc[c * (E + 1) + e];
-                    total += v;
-                    if (c < (int)blockIdx.x) earlier += v;
-                }
-            } else {
-                total = cc[(int64_t)chunks * (E + 1) + e];
-                earlier = cc[(int64_t)blockIdx.x * (E + 1) + e];
-            }
-        }
+        if (MODE == kOnly || e0 > 0) gather(e, total, earlier);
         int all;
         const int offset = carry + exclusive_sum(total, sums, all);
         carry += all;
