@@ -488,7 +488,7 @@ def _call(what, device, *args):
         raise ValueError(f"{what}: tensors are on {device}, not on a GPU")
     fn = getattr(_lib, what)
     stream = torch._C._cuda_getCurrentRawStream(device.index)
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == device.index:
         rc = fn(*args, stream)
     else:
         with torch.cuda.device(device):
