@@ -465,45 +465,77 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a
     // lane (r, g) of tile (i, j): token TR j + r, four n from TR i + 8 q + 4 g for
     // each q (16 x 16 tiles: from 4 g)
     const int64_t n_left = a.N - p.n0;
-    const bool quads = a.N % 4 == 0 && ((uintptr_t)a.y & 15) == 0;
+    auto quad = [&](int i, int j, int q, int col) {
+        f32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        if (a.bias) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (col + e < n_left) v[e] += a.bias[p.expert * a.N + p.n0 + col + e];
+        }
+        return v;
+    };
+    // Row of y of tile row i (of the workgroup's), -1 for none.
+    auto y_row = [&](int i) -> int64_t {
+        if (i >= m_rows) return -1;
+        if (!GROUPED) return p.m0 + i;
+        const int64_t slot = a.order[p.m0 + i];
+        return slot < slots ? slot : -1;
+    };
+    // Rows of y in 16-byte pieces: the wave's TR tokens x NT TR columns of each j
+    // change hands in LDS, so that whole lines are written.
+    auto write_rows = [&](auto type) {
+        typedef decltype(type) T;
+        constexpr int kCols = NT * TR, kPitch = kCols * (int)sizeof(T) + 16, kEach = 16 / (int)sizeof(T);
+        constexpr int kLanes = kCols / kEach, kAtOnce = 64 / kLanes;
+        constexpr int kHalf = kWaves / 2;       // waves a stage
+        static_assert(kHalf * TR * kPitch <= kStage && TR % kAtOnce == 0, "the stages hold the waves' rows");
+        uint8_t* const mine = (wave < kHalf ? stage0 : stage1) + wave % kHalf * (TR * kPitch);
+        const int c = lane % kLanes, col = wn * (BN / WN) + c * kEach;
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int q = 0; q < TR * TR / 256; ++q) {
+                    const int at = TR * i + 8 * q + 4 * g;
+                    const f32x4 v = quad(i, j, q, wn * (BN / WN) + at);
+                    if constexpr (sizeof(T) == 4) *(f32x4*)(mine + r * kPitch + at * 4) = v;
+                    else *(u32x2*)(mine + r * kPitch + at * 2) = (u32x2){bf16_pair(v.x, v.y), bf16_pair(v.z, v.w)};
+                }
+            asm volatile("" ::: "memory");      // a wave's LDS accesses happen in order
+#pragma unroll
+            for (int k = 0; k < TR; k += kAtOnce) {
+                const int row = k + lane / kLanes;
+                const u32x4 d = *(const u32x4*)(mine + row * kPitch + c * 16);
+                const int64_t out = y_row(wm * (BM / WM) + TR * j + row);
+                if (out >= 0 && col < n_left) *(u32x4*)((T*)a.y + out * a.N + p.n0 + col) = d;
+            }
+            asm volatile("" ::: "memory");
+        }
+    };
+    const bool f32 = a.y_dtype == TQ_F32;
+    if (a.N % (f32 ? 4 : 8) == 0 && ((uintptr_t)a.y & 15) == 0) {
+        lds_barrier();                          // every wave is done with the stages
+        if (f32) write_rows(float());
+        else write_rows((uint16_t)0);
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
-        const int64_t m = p.m0 + wm * (BM / WM) + TR * j + r;
-        if (m >= p.m_end) continue;
-        int64_t out = m;
-        if (GROUPED) {
-            out = a.order[m];
-            if (out < 0 || out >= slots) continue;
-        }
+        const int64_t out = y_row(wm * (BM / WM) + TR * j + r);
+        if (out < 0) continue;
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int q = 0; q < TR * TR / 256; ++q) {
                 const int col = wn * (BN / WN) + TR * i + 8 * q + 4 * g;
-                if (col >= n_left) continue;
-                f32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-                if (a.bias) {
+                const f32x4 v = quad(i, j, q, col);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (col + e < n_left) v[e] += a.bias[p.expert * a.N + p.n0 + col + e];
-                }
-                const int64_t at = out * a.N + p.n0 + col;
-                if (quads) {
-                    if (a.y_dtype == TQ_F32) {
-                        *(f32x4*)((float*)a.y + at) = v;
-                    } else {
-                        u32x2 d;
-                        d.x = bf16_pair(v.x, v.y);
-                        d.y = bf16_pair(v.z, v.w);
-                        *(u32x2*)((uint16_t*)a.y + at) = d;
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (col + e >= n_left) continue;
-                        if (a.y_dtype == TQ_F32) ((float*)a.y)[at + e] = v[e];
-                        else ((uint16_t*)a.y)[at + e] = f32_to_bf16_rne(v[e]);
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    if (col + e >= n_left) continue;
+                    const int64_t at = out * a.N + p.n0 + col + e;
+                    if (f32) ((float*)a.y)[at] = v[e];
+                    else ((uint16_t*)a.y)[at] = f32_to_bf16_rne(v[e]);
                 }
             }
     }
