@@ -278,20 +278,29 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a
         if (MXX && !DIRECT && tid < BM + BN) *(Scales*)(st + kXBytes + kWBytes + tid * kSRow) = sreg;
         if (!MXX && !DIRECT) store_x(st);
     };
-    const int64_t last8 = nb > 8 ? nb - 8 : 0;
-    uint64_t sc[NT], sc_next[NT];               // bf16 activations: scales of the units at hand
-    auto fetch_scales = [&](int64_t q) {        // of units q .. q + 3, as far as there are any: the last eight
-        const int64_t b = 2 * q < last8 ? 2 * q : last8;
+    // bf16 activations: scales of the units at hand and of the next, 16 bytes (eight
+    // units) of a row at a time; 8 at a time were a third of a slab's requests.
+    typedef uint64_t Sixteen __attribute__((ext_vector_type(2)));
+    typedef Sixteen SixteenAt __attribute__((aligned(1)));
+    const int64_t last = nb > 16 ? nb - 16 : 0;
+    Sixteen sc[NT], sc_next[NT];
+    auto fetch_scales = [&](int64_t q) {        // of units q .. q + 7, as far as there are any: the last 16
+        const int64_t b = 2 * q < last ? 2 * q : last;
         const GlobalBytes sb = scalar_base(wscales + b);
 #pragma unroll
         for (int i = 0; i < NT; ++i)
-            sc_next[i] = *(const __attribute__((address_space(1))) u64u*)(sb + lane_offset(ssrc[i]));
+            sc_next[i] = *(const __attribute__((address_space(1))) SixteenAt*)(sb + lane_offset(ssrc[i]));
     };
-    auto take_scales = [&](int64_t q) {
-        const int64_t b = 2 * q < last8 ? 2 * q : last8;
+    auto take_scales = [&](int64_t q) {         // q a multiple of 8
+        const int64_t b = 2 * q < last ? 2 * q : last;
+        const int skip = 8 * (int)(2 * q - b);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) sc[i] = sc_next[i] >> (8 * (int)(2 * q - b));
-        if (2 * q + 8 < nb) fetch_scales(q + 4);
+        for (int i = 0; i < NT; ++i) {
+            sc[i] = sc_next[i];
+            if (skip >= 64) sc[i] = (Sixteen){sc[i].y >> (skip - 64), 0};
+            else if (skip > 0) sc[i] = (Sixteen){sc[i].x >> skip | sc[i].y << (64 - skip), sc[i].y >> skip};
+        }
+        if (2 * q + 16 < nb) fetch_scales(q + 8);
     };
 
     // ---- fragments: step s (of four) of a unit from LDS to registers, then
@@ -346,9 +355,9 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
                 if (s == 0) wc[i] = wf[0][i];
-                const uint32_t b = (uint32_t)(sc[i] >> (8 * g)) & 0xffu;
+                const uint32_t b = (uint32_t)(sc[i].x >> (8 * g)) & 0xffu;
                 w[i] = mx_decode8(wc[i][s], e8m0_bits(b));
-                if (s == 3) sc[i] >>= 16;
+                if (s == 3) sc[i] = (Sixteen){sc[i].x >> 16 | sc[i].y << 48, sc[i].y >> 16};
             }
 #pragma unroll
             for (int j = 0; j < MT; ++j)
@@ -380,7 +389,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a
     auto slab = [&](uint8_t* cur, uint8_t* other, int64_t t) {
 #pragma unroll
         for (int k = 0; k < KD; ++k) {
-            if (!MXX && (KD % 4 == 0 ? k % 4 == 0 : (t * KD + k) % 4 == 0)) take_scales(t * KD + k);
+            if (!MXX && (t * KD + k) % 8 == 0) take_scales(t * KD + k);
             read(cur, k, 1);
             multiply(S0());
             read(cur, k, 2);
@@ -401,11 +410,12 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a
     };
 
     if (!MXX) {
-        if (nb >= 8) {
+        if (nb >= 16) {
             fetch_scales(0);
-        } else {                                // fewer than eight bytes a row: all that there will be
+        } else {                                // fewer than 16 bytes a row: all that there will be
 #pragma unroll
-            for (int i = 0; i < NT; ++i) sc_next[i] = scales8(wscales + ssrc[i], 0, nb);
+            for (int i = 0; i < NT; ++i)
+                sc_next[i] = (Sixteen){scales8(wscales + ssrc[i], 0, nb), scales8(wscales + ssrc[i], 8, nb)};
         }
     }
     if (full > 0) {
@@ -452,7 +462,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a
         lds_barrier();
 #pragma unroll 1
         for (int k = 0; k < (int)rest; ++k) {
-            if (!MXX && (full * KD + k) % 4 == 0) take_scales(full * KD + k);
+            if (!MXX && (full * KD + k) % 8 == 0) take_scales(full * KD + k);
             read(stage0, k, 0);
             read(stage0, k, 1);
             multiply(S0());
