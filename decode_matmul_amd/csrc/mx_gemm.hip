@@ -61,7 +61,8 @@ struct Place {
 
 // Tile b of the experts' tiles: experts in turn, an expert's tiles of BM
 // positions in turn, the tiles along N innermost; each XCD gets a contiguous
-// share of the tiles that there are.  False when there are fewer.
+// share of the tiles that there are.  False when there are fewer: then m0 is the
+// workgroup's number among the m_end that have none.
 template <int BM, int BN, int kThreads>
 __device__ bool place_grouped(const MxMatmulArgs& a, Place& p) {
     __shared__ int found[3];
@@ -96,7 +97,12 @@ __device__ bool place_grouped(const MxMatmulArgs& a, Place& p) {
     // XCD b % 8 takes tiles all * (b % 8) / 8 .. all * (b % 8 + 1) / 8 - 1
     const int64_t x = b % 8, lo = all * x / 8, hi = all * (x + 1) / 8;
     const int64_t t = lo + b / 8;
-    if (t >= hi) return false;
+    if (t >= hi) {
+        const int64_t cap = gridDim.x / 8;      // of an XCD
+        p.m0 = cap * x - lo + t - hi;
+        p.m_end = cap * 8 - all;
+        return false;
+    }
     const int want = readfirstlane((int)(t / ntiles));
     p.n0 = (t - (int64_t)want * ntiles) * BN;
     int before = 0;
@@ -129,12 +135,29 @@ __device__ bool place_grouped(const MxMatmulArgs& a, Place& p) {
         }
         __syncthreads();
     }
-    if (readfirstlane(found[2]) < 0) return false;  // overlapping lists can have more tiles than an int counts
+    if (readfirstlane(found[2]) < 0) {          // overlapping lists can have more tiles than an int counts
+        p.m0 = p.m_end = a.M * a.top_k;
+        return false;
+    }
     p.m0 = readfirstlane(found[0]);
     const int64_t last = readfirstlane(found[1]);
     p.m_end = last < p.m0 + BM ? last : p.m0 + BM;
     p.expert = readfirstlane(found[2]);
     return true;
+}
+
+// Rows of slots of no expert: NaN.  A workgroup without a tile takes every step-th
+// from number `first` on; there are at least as many of them as those slots make tiles.
+__device__ void write_nan_rows(const MxMatmulArgs& a, int64_t first, int64_t step, int threads) {
+    const int64_t slots = a.M * a.top_k, begin = a.offsets[a.n_experts];
+    for (int64_t i = (begin < 0 ? 0 : begin) + first; i < slots; i += step) {
+        const int64_t slot = a.order[i];
+        if (slot < 0 || slot >= slots) continue;
+        for (int64_t n = threadIdx.x; n < a.N; n += threads) {
+            if (a.y_dtype == TQ_F32) ((float*)a.y)[slot * a.N + n] = __builtin_nanf("");
+            else ((uint16_t*)a.y)[slot * a.N + n] = 0x7fc0u;
+        }
+    }
 }
 
 // MXX: activations in MXFP4.  DIRECT: whole slabs of bf16 activations (MXX: of
@@ -168,7 +191,10 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a
 
     Place p;
     if (GROUPED) {
-        if (!place_grouped<BM, BN, kThreads>(a, p)) return;
+        if (!place_grouped<BM, BN, kThreads>(a, p)) {
+            write_nan_rows(a, p.m0, p.m_end, kThreads);
+            return;
+        }
     } else {
         // groups of 8 tiles along M share the rows of W; each XCD takes a contiguous range
         const int64_t mt = (a.M + BM - 1) / BM, nt = (a.N + BN - 1) / BN;
@@ -553,21 +579,6 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a
     }
 }
 
-// Rows of slots of no expert: NaN.
-__global__ void __launch_bounds__(256) nan_rows_kernel(MxMatmulArgs a) {
-    const int64_t slots = a.M * a.top_k;
-    int64_t begin = a.offsets[a.n_experts];
-    begin = begin < 0 ? 0 : begin;
-    for (int64_t i = begin + blockIdx.x; i < slots; i += gridDim.x) {
-        const int64_t slot = a.order[i];
-        if (slot < 0 || slot >= slots) continue;
-        for (int64_t n = threadIdx.x; n < a.N; n += 256) {
-            if (a.y_dtype == TQ_F32) ((float*)a.y)[slot * a.N + n] = __builtin_nanf("");
-            else ((uint16_t*)a.y)[slot * a.N + n] = 0x7fc0u;
-        }
-    }
-}
-
 template <bool MXX, bool DIRECT, int BM, int BN, int WM, int WN, int KD, bool GROUPED>
 hipError_t launch(const MxMatmulArgs& a, hipStream_t s) {
     constexpr int kThreads = 64 * WM * WN;
@@ -581,9 +592,6 @@ hipError_t launch(const MxMatmulArgs& a, hipStream_t s) {
     }
     if (!grid_fits(blocks, kThreads)) return hipErrorInvalidConfiguration;
     mx_gemm_kernel<MXX, DIRECT, BM, BN, WM, WN, KD, GROUPED><<<(unsigned)blocks, kThreads, 0, s>>>(a);
-    hipError_t e = hipGetLastError();
-    if (!GROUPED || e != hipSuccess) return e;
-    nan_rows_kernel<<<256, 256, 0, s>>>(a);
     return hipGetLastError();
 }
 

@@ -260,6 +260,29 @@ def test_tiled_experts_skip_bad_lists(dmm, M, K):
     assert (got[left] == 3).all() and intact(whole)
 
 
+@pytest.mark.parametrize("M,E,valid", [(300, 5, 0), (512, 1, 448), (512, 1, 512), (700, 3, 1), (90, 2, 64)])
+def test_padded_batches(dmm, M, E, valid):
+    """Batches whose tail (or all) is padding: its rows are NaN, the others right."""
+    say(f"padded batch M={M} E={E} valid={valid}")
+    N, K = 520, 64
+    rng = np.random.default_rng(M + valid)
+    x = activations(rng, M, K)
+    c, s = packed(rng, E * N, K)
+    w = oracle.mx_unpack(c, s, K).reshape(E, N, K)
+    ids = rng.integers(0, E, (M, 1)).astype(np.int32)
+    ids[valid:] = -1
+    counts, offsets, order = route(dmm, ids, E)
+    whole, y = guarded(M * N, torch.bfloat16)
+    dmm.mx_matmul_experts(bf16_of(x), dev(c), dev(s), N, y, E, offsets, order, 1)
+    got = host(y).reshape(M, N)
+    assert intact(whole) and np.isnan(got[valid:]).all()
+    for e in range(E):
+        t = np.nonzero(ids[:, 0] == e)[0]
+        if len(t):
+            ref, B = oracle.matmul_ref(workloads.bf16_bits(x)[t], w[e])
+            assert_close(got[t], ref, B, K, torch.bfloat16, f"expert {e}")
+
+
 def test_layer_together(dmm):
     """A whole expert layer: routing, balance loss and gradient, both of the
     experts' products (the second with activations of its own for each slot)
