@@ -124,6 +124,7 @@ _H16 = (torch.float16, torch.int16, torch.uint16)
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
+_MASK = (torch.uint8, torch.bool)
 
 
 def packed_shape(rows, K, G):
@@ -478,29 +479,29 @@ def _float_dtype(t, name):
     raise TypeError(f"{name} dtype {t.dtype} must be float32 or bfloat16")
 
 
-def _at(t):
-    return None if t is None else t.data_ptr()
+def _ptr(t, name, dtypes, numel, device):
+    """The address of a contiguous tensor of `numel` elements on the device."""
+    if t is None or t.dtype not in dtypes or t.numel() != numel or not t.is_contiguous() or t.device != device:
+        _need(t, name, dtypes, numel, device)
+    return t.data_ptr()
 
 
-def _call(what, device, *args):
-    """The C entry point `what` on the device's current stream, with the device current."""
+def _maybe(t, name, dtypes, numel, device):
+    return None if t is None else _ptr(t, name, dtypes, numel, device)
+
+
+def _call(what, fn, device, *args):
+    """The C entry point fn on the device's current stream, with the device current."""
+    index = device.index
     if device.type != "cuda":
         raise ValueError(f"{what}: tensors are on {device}, not on a GPU")
-    fn = getattr(_lib, what)
-    stream = torch._C._cuda_getCurrentRawStream(device.index)
-    if torch._C._cuda_getDevice() == device.index:
-        rc = fn(*args, stream)
+    if torch._C._cuda_getDevice() == index:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, stream)
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc != TQ_OK:
         _raise(rc, what)
-
-
-def _package(codes, scales, rows, K, device, prefix=""):
-    nb = -(-K // 32)
-    _need(codes, prefix + "codes", _U8, rows * nb * 16, device)
-    _need(scales, prefix + "scales", _U8, rows * nb, device)
 
 
 def mx_pack(W, codes, scales, status=None):
@@ -512,10 +513,10 @@ def mx_pack(W, codes, scales, status=None):
     wdt = _float_dtype(W, "W")
     rows, K = W.shape
     ldw = _rows(W, "W", (W.dtype,), rows, K, dev)
-    _package(codes, scales, rows, K, dev)
-    if status is not None:
-        _need(status, "status", _I32, 1, dev)
-    _call("mx_pack", dev, _at(W), wdt, rows, K, ldw, _at(codes), _at(scales), _at(status))
+    nb = -(-K // 32)
+    _call("mx_pack", _lib.mx_pack, dev, W.data_ptr(), wdt, rows, K, ldw,
+          _ptr(codes, "codes", _U8, rows * nb * 16, dev), _ptr(scales, "scales", _U8, rows * nb, dev),
+          _maybe(status, "status", _I32, 1, dev))
     return status
 
 
@@ -523,12 +524,11 @@ def mx_unpack(codes, scales, rows, K, W_out, status=None):
     """Decode an MXFP4 package into W_out [rows, K] (float32 or bfloat16, both
     exact).  With status (int32 [1]) data errors are reported there."""
     dev = codes.device
-    _package(codes, scales, rows, K, dev)
+    nb = -(-K // 32)
     odt = _float_dtype(W_out, "W_out")
-    _need(W_out, "W_out", (W_out.dtype,), rows * K, dev)
-    if status is not None:
-        _need(status, "status", _I32, 1, dev)
-    _call("mx_unpack", dev, _at(codes), _at(scales), rows, K, _at(W_out), odt, _at(status))
+    _call("mx_unpack", _lib.mx_unpack, dev, _ptr(codes, "codes", _U8, rows * nb * 16, dev),
+          _ptr(scales, "scales", _U8, rows * nb, dev), rows, K,
+          _ptr(W_out, "W_out", (W_out.dtype,), rows * K, dev), odt, _maybe(status, "status", _I32, 1, dev))
     return status
 
 
@@ -538,25 +538,20 @@ def mx_matmul(x, codes, scales, N, y, bias=None):
     dev = x.device
     M, K = x.shape
     ldx = _rows(x, "x", _BF16, M, K, dev)
-    _package(codes, scales, N, K, dev)
-    if bias is not None:
-        _need(bias, "bias", _F32, N, dev)
-    _need(y, "y", (y.dtype,), M * N, dev)
-    ydt = _ydtype(y)
-    _call("mx_matmul", dev, _at(x), M, K, ldx, _at(codes), _at(scales), N, _at(bias), _at(y), ydt)
+    nb = -(-K // 32)
+    _call("mx_matmul", _lib.mx_matmul, dev, x.data_ptr(), M, K, ldx,
+          _ptr(codes, "codes", _U8, N * nb * 16, dev), _ptr(scales, "scales", _U8, N * nb, dev), N,
+          _maybe(bias, "bias", _F32, N, dev), _ptr(y, "y", (y.dtype,), M * N, dev), _ydtype(y))
 
 
 def mx_matmul_mx(x_codes, x_scales, M, K, codes, scales, N, y, bias=None):
     """mx_matmul with the [M, K] activations as an MXFP4 package too."""
     dev = x_codes.device
-    _package(x_codes, x_scales, M, K, dev, "x_")
-    _package(codes, scales, N, K, dev)
-    if bias is not None:
-        _need(bias, "bias", _F32, N, dev)
-    _need(y, "y", (y.dtype,), M * N, dev)
-    ydt = _ydtype(y)
-    _call("mx_matmul_mx", dev, _at(x_codes), _at(x_scales), M, K, _at(codes), _at(scales), N,
-          _at(bias), _at(y), ydt)
+    nb = -(-K // 32)
+    _call("mx_matmul_mx", _lib.mx_matmul_mx, dev, _ptr(x_codes, "x_codes", _U8, M * nb * 16, dev),
+          _ptr(x_scales, "x_scales", _U8, M * nb, dev), M, K,
+          _ptr(codes, "codes", _U8, N * nb * 16, dev), _ptr(scales, "scales", _U8, N * nb, dev), N,
+          _maybe(bias, "bias", _F32, N, dev), _ptr(y, "y", (y.dtype,), M * N, dev), _ydtype(y))
 
 
 def moe_route_workspace_bytes(M, top_k, n_experts):
@@ -571,8 +566,8 @@ def _workspace(workspace, dev):
     """Pointer and size of an optional uint8 workspace."""
     if workspace is None:
         return None, 0
-    _need(workspace, "workspace", _U8, workspace.numel(), dev)
-    return _at(workspace), workspace.numel()
+    n = workspace.numel()
+    return _ptr(workspace, "workspace", _U8, n, dev), n
 
 
 def moe_route(expert_ids, n_experts, counts, offsets, order, workspace=None):
@@ -581,13 +576,11 @@ def moe_route(expert_ids, n_experts, counts, offsets, order, workspace=None):
     expert; ids outside [0, n_experts) last)."""
     dev = expert_ids.device
     M, top_k = expert_ids.shape
-    _need(expert_ids, "expert_ids", _I32, M * top_k, dev)
-    _need(counts, "counts", _I32, n_experts, dev)
-    _need(offsets, "offsets", _I32, n_experts + 1, dev)
-    _need(order, "order", _I32, M * top_k, dev)
     ws, nbytes = _workspace(workspace, dev)
-    _call("moe_route", dev, _at(expert_ids), M, top_k, n_experts, _at(counts), _at(offsets),
-          _at(order), ws, nbytes)
+    _call("moe_route", _lib.moe_route, dev, _ptr(expert_ids, "expert_ids", _I32, M * top_k, dev), M, top_k,
+          n_experts, _ptr(counts, "counts", _I32, n_experts, dev),
+          _ptr(offsets, "offsets", _I32, n_experts + 1, dev), _ptr(order, "order", _I32, M * top_k, dev),
+          ws, nbytes)
 
 
 def mx_matmul_experts(x, codes, scales, N, y, n_experts, offsets, order, top_k, bias=None):
@@ -596,15 +589,12 @@ def mx_matmul_experts(x, codes, scales, N, y, n_experts, offsets, order, top_k, 
     dev = x.device
     M, K = x.shape
     ldx = _rows(x, "x", _BF16, M, K, dev)
-    _package(codes, scales, n_experts * N, K, dev)
-    if bias is not None:
-        _need(bias, "bias", _F32, n_experts * N, dev)
-    _need(offsets, "offsets", _I32, n_experts + 1, dev)
-    _need(order, "order", _I32, M * top_k, dev)
-    _need(y, "y", (y.dtype,), M * top_k * N, dev)
-    ydt = _ydtype(y)
-    _call("mx_matmul_experts", dev, _at(x), M, K, ldx, _at(codes), _at(scales), N, n_experts,
-          _at(bias), _at(offsets), _at(order), top_k, _at(y), ydt)
+    rows, nb = n_experts * N, -(-K // 32)
+    _call("mx_matmul_experts", _lib.mx_matmul_experts, dev, x.data_ptr(), M, K, ldx,
+          _ptr(codes, "codes", _U8, rows * nb * 16, dev), _ptr(scales, "scales", _U8, rows * nb, dev), N,
+          n_experts, _maybe(bias, "bias", _F32, rows, dev),
+          _ptr(offsets, "offsets", _I32, n_experts + 1, dev), _ptr(order, "order", _I32, M * top_k, dev),
+          top_k, _ptr(y, "y", (y.dtype,), M * top_k * N, dev), _ydtype(y))
 
 
 def moe_balance_workspace_bytes(M, n_experts):
@@ -624,14 +614,10 @@ def moe_balance(logits, counts, loss, weights, token_mask=None, workspace=None):
     ldt = _float_dtype(logits, "logits")
     M, E = logits.shape
     ldl = _rows(logits, "logits", (logits.dtype,), M, E, dev)
-    _need(counts, "counts", _I32, E, dev)
-    _need(loss, "loss", _F32, 1, dev)
-    _need(weights, "weights", _F32, E, dev)
-    if token_mask is not None:
-        _need(token_mask, "token_mask", (torch.uint8, torch.bool), M, dev)
     ws, nbytes = _workspace(workspace, dev)
-    _call("moe_balance", dev, _at(logits), ldt, M, E, ldl, _at(token_mask), _at(counts), _at(loss),
-          _at(weights), ws, nbytes)
+    _call("moe_balance", _lib.moe_balance, dev, logits.data_ptr(), ldt, M, E, ldl,
+          _maybe(token_mask, "token_mask", _MASK, M, dev), _ptr(counts, "counts", _I32, E, dev),
+          _ptr(loss, "loss", _F32, 1, dev), _ptr(weights, "weights", _F32, E, dev), ws, nbytes)
 
 
 def moe_balance_grad(logits, weights, dloss, dlogits, token_mask=None):
@@ -641,13 +627,9 @@ def moe_balance_grad(logits, weights, dloss, dlogits, token_mask=None):
     ldt = _float_dtype(logits, "logits")
     M, E = logits.shape
     ldl = _rows(logits, "logits", (logits.dtype,), M, E, dev)
-    _need(weights, "weights", _F32, E, dev)
-    _need(dloss, "dloss", _F32, 1, dev)
-    _need(dlogits, "dlogits", (logits.dtype,), M * E, dev)
-    if token_mask is not None:
-        _need(token_mask, "token_mask", (torch.uint8, torch.bool), M, dev)
-    _call("moe_balance_grad", dev, _at(logits), ldt, M, E, ldl, _at(token_mask), _at(weights),
-          _at(dloss), _at(dlogits))
+    _call("moe_balance_grad", _lib.moe_balance_grad, dev, logits.data_ptr(), ldt, M, E, ldl,
+          _maybe(token_mask, "token_mask", _MASK, M, dev), _ptr(weights, "weights", _F32, E, dev),
+          _ptr(dloss, "dloss", _F32, 1, dev), _ptr(dlogits, "dlogits", (logits.dtype,), M * E, dev))
 
 
 def raw():
