@@ -162,10 +162,11 @@ __device__ void write_nan_rows(const MxMatmulArgs& a, int64_t first, int64_t ste
 
 // MXX: activations in MXFP4.  DIRECT: whole slabs of bf16 activations (MXX: of
 // scales) go straight to LDS, their rows aligned; otherwise through registers.  BM x BN
-// tile of WM x WN waves; KD units (64 columns, or 256 with MXX) a slab.
-template <bool MXX, bool DIRECT, int BM, int BN, int WM, int WN, int KD, bool GROUPED>
-__global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a) {
-    constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+// tile of WM x WN waves; KD units (64 columns, or 256 with MXX) a slab.  KG
+// groups of WM x WN waves take every KG-th slab each, and the first adds up the sums.
+template <bool MXX, bool DIRECT, int BM, int BN, int WM, int WN, int KD, int KG, bool GROUPED>
+__global__ void __launch_bounds__(64 * WM * WN * KG, 2) mx_gemm_kernel(MxMatmulArgs a) {
+    constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;                 // of a group
     constexpr int kUnit = MXX ? 256 : 64, kSlab = KD * kUnit;
     constexpr int kWRow = MXX ? kRow : KD * 32;         // bytes of W's rows in LDS: a unit, or with bf16 activations a slab
     constexpr int kXUnit = BM * kRow, kWUnit = BN * kRow;
@@ -176,15 +177,19 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a
     constexpr int MT = BM / WM / TR, NT = BN / WN / TR; // tiles of a wave
     constexpr int HT = MXX ? MT / 2 : MT;       // tiles along M of a step
     constexpr int kXLoads = kXBytes / 1024 / kWaves, kWLoads = kWBytes / 1024 / kWaves;
-    constexpr bool kOneWave = kWaves <= 4 && 2 * (2 * kStage + (GROUPED ? 256 : 0)) > 160 * 1024;   // a SIMD
+    constexpr bool kOneWave = kWaves * KG <= 4 && 2 * (2 * KG * kStage + (GROUPED ? 256 : 0)) > 160 * 1024;   // a SIMD
     static_assert(kXLoads * 1024 * kWaves == kXBytes && kWLoads * 1024 * kWaves == kWBytes, "whole loads");
     static_assert(kXUnit % 1024 == 0 && kXLoads % KD == 0, "a load stays in a unit");
     static_assert(MXX || KD == 2 || KD == 4, "w_slot");
     static_assert(!MXX || BM + BN <= kThreads, "a thread for each row's scales");
-    __shared__ __attribute__((aligned(1024))) uint8_t stage0[kStage];
-    __shared__ __attribute__((aligned(1024))) uint8_t stage1[kStage];
+    static_assert(KG == 1 || (!GROUPED && !MXX && KG * KD >= 8), "a group fetches the scales of each of its slabs");
+    __shared__ __attribute__((aligned(1024))) uint8_t stages0[KG * kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t stages1[KG * kStage];
 
-    const int tid = (int)threadIdx.x, lane = tid & 63, wave = readfirstlane(tid >> 6);
+    const int kg = KG == 1 ? 0 : readfirstlane((int)threadIdx.x / kThreads);
+    const int tid = (int)threadIdx.x - kg * kThreads, lane = tid & 63, wave = readfirstlane(tid >> 6);
+    uint8_t* const stage0 = stages0 + kg * kStage;
+    uint8_t* const stage1 = stages1 + kg * kStage;
     const int r = lane % TR, g = lane / TR;
     const int wm = wave / WN, wn = wave % WN;
     const int64_t nb = (a.K + 31) / 32;
@@ -285,12 +290,12 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a
     Scales sreg;                                // MXX: scales on their way
     auto start = [&](uint8_t* st, int64_t t) {  // slab t, a whole one
         if (MXX) {
-            const GlobalBytes from = scalar_base((stages_w ? wscales : xscales) + t * kSRow) + lane_offset(ssrc[0]);
+            const GlobalBytes from = scalar_base((stages_w ? wscales : xscales) + (t * KG + kg) * kSRow) + lane_offset(ssrc[0]);
             if (!DIRECT) sreg = *(const __attribute__((address_space(1))) ScalesAt*)from;
             else if (wave < (BM + BN) / 64) load_lds16(from, st + kXBytes + kWBytes + wave * 1024);
         }
-        const GlobalBytes xb = scalar_base(xbase + t * (KD * kRow));
-        const GlobalBytes wb = scalar_base(wbase + t * (kSlab / 2));
+        const GlobalBytes xb = scalar_base(xbase + (t * KG + kg) * (KD * kRow));
+        const GlobalBytes wb = scalar_base(wbase + (t * KG + kg) * (kSlab / 2));
 #pragma unroll
         for (int j = 0; j < kXLoads; ++j) {
             const GlobalBytes from = xb + lane_offset(xsrc[j % (kXLoads / KD)]) + x_unit(j) * kRow;
@@ -317,7 +322,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a
         for (int i = 0; i < NT; ++i)
             sc_next[i] = *(const __attribute__((address_space(1))) SixteenAt*)(sb + lane_offset(ssrc[i]));
     };
-    auto take_scales = [&](int64_t q) {         // q a multiple of 8
+    auto take_scales = [&](int64_t q) {         // q a multiple of 8 (of KD, where there are groups)
         const int64_t b = 2 * q < last ? 2 * q : last;
         const int skip = 8 * (int)(2 * q - b);
 #pragma unroll
@@ -326,7 +331,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a
             if (skip >= 64) sc[i] = (Sixteen){sc[i].y >> (skip - 64), 0};
             else if (skip > 0) sc[i] = (Sixteen){sc[i].x >> skip | sc[i].y << (64 - skip), sc[i].y >> skip};
         }
-        if (2 * q + 16 < nb) fetch_scales(q + 8);
+        constexpr int kNext = KG == 1 ? 8 : KG * KD;        // units to the next take
+        if (2 * (q + kNext) < nb) fetch_scales(q + kNext);
     };
 
     // ---- fragments: step s (of four) of a unit from LDS to registers, then
@@ -411,11 +417,12 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a
     // slab t + 1 has landed in `other` (what of it came to registers is stored
     // there): while the last step multiplies, slab t + 2 starts into `cur` and the
     // first step of slab t + 1 is read.
-    const int64_t full = a.K / kSlab;
+    // (a group's slab t is slab t KG + kg of the rows)
+    const int64_t full = a.K / kSlab / KG;
     auto slab = [&](uint8_t* cur, uint8_t* other, int64_t t) {
 #pragma unroll
         for (int k = 0; k < KD; ++k) {
-            if (!MXX && (t * KD + k) % 8 == 0) take_scales(t * KD + k);
+            if (!MXX && (KG > 1 ? k == 0 : (t * KD + k) % 8 == 0)) take_scales((t * KG + kg) * KD + k);
             read(cur, k, 1);
             multiply(S0());
             read(cur, k, 2);
@@ -437,7 +444,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a
 
     if (!MXX) {
         if (nb >= 16) {
-            fetch_scales(0);
+            fetch_scales(kg * KD);
         } else {                                // fewer than 16 bytes a row: all that there will be
 #pragma unroll
             for (int i = 0; i < NT; ++i)
@@ -456,14 +463,16 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a
             if (t + 1 < full) slab(stage1, stage0, t + 1);
         }
     }
-    const int64_t rest = (nb * 32 - full * kSlab + kUnit - 1) / kUnit;     // units that are left, the last one maybe cut
-    if (rest > 0) {
+    // units that are left, the last one maybe cut: up to KD for each group
+    const int64_t first = (full * KG + kg) * KD, units = (nb * 32 + kUnit - 1) / kUnit;
+    if (units > full * KG * KD) {
+        const int rest = units > first ? (int)(units - first < KD ? units - first : KD) : 0;
         // The slab that ends past K: activations through registers, zeros past K;
         // W's chunks past its last block repeat it (their products are 0).
         lds_barrier();
 #pragma unroll
         for (int j = 0; j < kXLoads; ++j) {
-            const int64_t u = full * KD + x_unit(j);
+            const int64_t u = first + x_unit(j);
             const uint8_t* const row = xbase + lane_offset(xsrc[j % (kXLoads / KD)]) - x_chunk(j) * 16;
             if (MXX) {
                 xr[j] = (u32x4){0u, 0u, 0u, 0u};
@@ -475,20 +484,20 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a
         store_x(stage0);
 #pragma unroll
         for (int j = 0; j < kWLoads; ++j) {
-            const int64_t c = w_unit(j) * (kUnit / 32) + w_chunk(j), b = full * (kSlab / 32) + c;
+            const int64_t c = w_unit(j) * (kUnit / 32) + w_chunk(j), b = first * (kUnit / 32) + c;
             load_lds16((GlobalBytes)(wbase + lane_offset(wsrc[j]) + ((b < nb ? b : nb - 1) - c) * 16), stage0 + w_lds(j));
         }
         if (MXX && tid < BM + BN) {
 #pragma unroll
             for (int k = 0; k < KD; ++k)
                 *(uint64_t*)(stage0 + kXBytes + kWBytes + tid * kSRow + 8 * k) =
-                    scales8((stages_w ? wscales : xscales) + ssrc[0], (full * KD + k) * 8, nb);
+                    scales8((stages_w ? wscales : xscales) + ssrc[0], (first + k) * 8, nb);
         }
         wait_loads<0>();
         lds_barrier();
 #pragma unroll 1
-        for (int k = 0; k < (int)rest; ++k) {
-            if (!MXX && (full * KD + k) % 8 == 0) take_scales(full * KD + k);
+        for (int k = 0; k < rest; ++k) {
+            if (!MXX && (KG > 1 ? k == 0 : (first + k) % 8 == 0)) take_scales(first + k);
             read(stage0, k, 0);
             read(stage0, k, 1);
             multiply(S0());
@@ -498,6 +507,38 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a
             multiply(S2());
             multiply(S3());
         }
+    }
+
+    if constexpr (KG > 1) {
+        constexpr int Q = TR * TR / 256;        // quads of a lane's sums
+        static_assert((KG - 1) * BM * BN * 4 <= KG * kStage, "the sums fit the stages");
+        lds_barrier();
+        auto sums = [&](int from, int i, int j, int q) -> f32x4& {
+            return ((f32x4*)stages0)[((((from - 1) * kWaves + wave) * NT + i) * MT + j) * (Q * 64) + q * 64 + lane];
+        };
+        if (kg > 0) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int j = 0; j < MT; ++j)
+#pragma unroll
+                    for (int q = 0; q < Q; ++q)
+                        sums(kg, i, j, q) = (f32x4){acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        }
+        lds_barrier();
+        if (kg > 0) return;
+#pragma unroll
+        for (int from = 1; from < KG; ++from)
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int j = 0; j < MT; ++j)
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) {
+                        const f32x4 v = sums(from, i, j, q);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += v[e];
+                    }
     }
 
     // lane (r, g) of tile (i, j): token TR j + r, four n from TR i + 8 q + 4 g for
@@ -525,7 +566,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a
         typedef decltype(type) T;
         constexpr int kCols = NT * TR, kPitch = kCols * (int)sizeof(T) + 16, kEach = 16 / (int)sizeof(T);
         constexpr int kLanes = kCols / kEach, kAtOnce = 64 / kLanes;
-        constexpr int kHalf = kWaves / 2;       // waves a stage
+        constexpr int kHalf = (kWaves + 1) / 2; // waves a stage
         static_assert(kHalf * TR * kPitch <= kStage && TR % kAtOnce == 0, "the stages hold the waves' rows");
         uint8_t* const mine = (wave < kHalf ? stage0 : stage1) + wave % kHalf * (TR * kPitch);
         const int c = lane % kLanes, col = wn * (BN / WN) + c * kEach;
@@ -579,9 +620,9 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(MxMatmulArgs a
     }
 }
 
-template <bool MXX, bool DIRECT, int BM, int BN, int WM, int WN, int KD, bool GROUPED>
+template <bool MXX, bool DIRECT, int BM, int BN, int WM, int WN, int KD, int KG, bool GROUPED>
 hipError_t launch(const MxMatmulArgs& a, hipStream_t s) {
-    constexpr int kThreads = 64 * WM * WN;
+    constexpr int kThreads = 64 * WM * WN * KG;
     const int64_t nt = (a.N + BN - 1) / BN;
     int64_t blocks = (a.M + BM - 1) / BM * nt;
     if (GROUPED) {
@@ -591,15 +632,15 @@ hipError_t launch(const MxMatmulArgs& a, hipStream_t s) {
         blocks = (tiles / 8 + 1) * 8;
     }
     if (!grid_fits(blocks, kThreads)) return hipErrorInvalidConfiguration;
-    mx_gemm_kernel<MXX, DIRECT, BM, BN, WM, WN, KD, GROUPED><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+    mx_gemm_kernel<MXX, DIRECT, BM, BN, WM, WN, KD, KG, GROUPED><<<(unsigned)blocks, kThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 
-template <int BM, int BN, int WM, int WN, int KD, bool GROUPED>
+template <int BM, int BN, int WM, int WN, int KD, int KG, bool GROUPED>
 hipError_t launch_bf16(const MxMatmulArgs& a, hipStream_t s) {
     const bool direct = ((uintptr_t)a.x & 15) == 0 && (a.ldx % 8 == 0 || a.M == 1);
-    return direct ? launch<false, true, BM, BN, WM, WN, KD, GROUPED>(a, s)
-                  : launch<false, false, BM, BN, WM, WN, KD, GROUPED>(a, s);
+    return direct ? launch<false, true, BM, BN, WM, WN, KD, KG, GROUPED>(a, s)
+                  : launch<false, false, BM, BN, WM, WN, KD, KG, GROUPED>(a, s);
 }
 
 }  // namespace
@@ -621,6 +662,15 @@ bool mx_gemm_takes(const MxMatmulArgs& a) {
 //     M = 2048, 8192 x 8192    83 /  106 /  159
 //     M = 1024, 4096 x 4096    37 /   19 /   24
 //     M =  512, 4096 x 4096    36 /   17 /   13
+// Few tiles leave compute units idle and each other one with more to fetch than it
+// can have under way: up to two tiles of 32 x 32 a unit take those, dealt over K to
+// four groups of one wave (a slab of 256 columns each where a unit has one tile, of
+// 128 where two share its LDS).  us, bf16, 32 x 32 / 64 x 64:
+//     M = 32, 8192 x 8192   16 / 33     M =  64, 4096 x 4096    8.0 / 15.7
+//     M = 64, 8192 x 8192   27 / 33     M = 128, 4096 x 4096   10.7 / 15.7
+//     M = 64, 4096 x 14336  24 / 55     M = 256, 4096 x 4096   19.8 / 16.1
+// (two groups of 64 x 64 gain nothing, 37.6 at M = 64, 8192 x 8192: the bytes a unit
+// fetches stay the same.)
 // Experts: by the slots an expert has on average, 32 x 128 / 64 x 256
 //     (64 experts of 2048 x 4096)
 //     32   109 / 116     48   127 / 112     256   435 / 331
@@ -628,19 +678,21 @@ bool mx_gemm_takes(const MxMatmulArgs& a) {
 // take 326, tiles of 128 x 256 took 333 there and 181 against 134 at 64 slots).
 hipError_t launch_mx_gemm(const MxMatmulArgs& a, hipStream_t s) {
     if (a.n_experts > 0)
-        return a.M * a.top_k < 40 * (int64_t)a.n_experts ? launch_bf16<32, 128, 1, 4, 4, true>(a, s)
-                                                         : launch_bf16<64, 256, 1, 4, 2, true>(a, s);
+        return a.M * a.top_k < 40 * (int64_t)a.n_experts ? launch_bf16<32, 128, 1, 4, 4, 1, true>(a, s)
+                                                         : launch_bf16<64, 256, 1, 4, 2, 1, true>(a, s);
     const int64_t cus = compute_unit_count();
     auto tiles = [&](int64_t side) { return ((a.M + side - 1) / side) * ((a.N + side - 1) / side); };
+    if (!a.x_codes && tiles(32) <= cus) return launch_bf16<32, 32, 1, 1, 4, 4, false>(a, s);
+    if (!a.x_codes && tiles(32) <= 2 * cus) return launch_bf16<32, 32, 1, 1, 2, 4, false>(a, s);
     if (4 * tiles(256) >= 3 * cus)
-        return a.x_codes ? launch<true, false, 256, 256, 2, 4, 1, false>(a, s) : launch_bf16<256, 256, 2, 4, 2, false>(a, s);
+        return a.x_codes ? launch<true, false, 256, 256, 2, 4, 1, 1, false>(a, s) : launch_bf16<256, 256, 2, 4, 2, 1, false>(a, s);
     if (4 * tiles(128) >= 3 * cus)
-        return a.x_codes ? launch<true, false, 128, 128, 2, 2, 1, false>(a, s) : launch_bf16<128, 128, 2, 2, 2, false>(a, s);
-    if (!a.x_codes) return launch_bf16<64, 64, 2, 2, 4, false>(a, s);
+        return a.x_codes ? launch<true, false, 128, 128, 2, 2, 1, 1, false>(a, s) : launch_bf16<128, 128, 2, 2, 2, 1, false>(a, s);
+    if (!a.x_codes) return launch_bf16<64, 64, 2, 2, 4, 1, false>(a, s);
     // Aligned scales straight to LDS: 11.3 us against 12.1 at M = 512, 4096 x 4096.
     // The larger tiles' slabs have 8 bytes a row, two lanes of 4, which gained nothing.
     const bool aligned = a.K % 512 == 0 && (((uintptr_t)a.scales | (uintptr_t)a.x_scales) & 15) == 0;
-    return aligned ? launch<true, true, 64, 64, 2, 2, 2, false>(a, s) : launch<true, false, 64, 64, 2, 2, 2, false>(a, s);
+    return aligned ? launch<true, true, 64, 64, 2, 2, 2, 1, false>(a, s) : launch<true, false, 64, 64, 2, 2, 2, 1, false>(a, s);
 }
 
 }  // namespace dmm

@@ -343,16 +343,13 @@ hipError_t launch_bf16(const MxMatmulArgs& a, hipStream_t s) {
 
 hipError_t launch_mx_matmul(const MxMatmulArgs& a, hipStream_t s) {
     const int64_t tiles = (a.N + 15) / 16, cus = compute_unit_count();
-    // Passes of 16 tokens against the tiled form, whose 64 x 64 tiles leave compute
-    // units idle where N is small (us, tiled from the second figure on):
-    //   bf16   8192 x 8192   M = 32: 22 / 35     4096 x 4096   M = 48: 13.5 / 15.9
-    //                                           4096 x 14336  M = 48: 36 / 54
-    //   MXFP4  8192 x 8192   M = 32: 21 / 19     4096 x 4096   M = 32: 8.8 / 8.4
-    //         14336 x 4096   M = 17: 15 / 12     4096 x 14336  M = 32: 18 / 30
+    // One pass of 16 tokens against the tiled form (us, tiled from the second figure on):
+    //   bf16   M = 16   8192 x 8192  14.5 / 14.7   4096 x 4096  6.7 / 7.6   14336 x 4096  12.3 / 14.2
+    //          M = 32   8192 x 8192  22.1 / 16.1   4096 x 4096  10.2 / 7.7  14336 x 4096  19.2 / 15.8
+    //   MXFP4  M = 32   8192 x 8192  21 / 19       4096 x 4096  8.8 / 8.4   4096 x 14336  18 / 30
     // and for experts up to about six slots each (64 experts of 2048 x 4096: 65 us
     // against 72 at 4 slots, 84 against 76 at 8).
-    const bool wide = tiles >= 2 * cus;
-    const int64_t few = a.x_codes ? (wide ? 16 : 32) : wide ? 32 : 48;
+    const int64_t few = a.x_codes && tiles < 2 * cus ? 32 : 16;
     const bool many = a.n_experts > 0 ? a.M * a.top_k >= 6 * (int64_t)a.n_experts : a.M > few;
     if (many && mx_gemm_takes(a)) return launch_mx_gemm(a, s);
     if (a.n_experts > 0)

@@ -191,6 +191,9 @@ SHAPES = [
     # more than a few tokens of short rows
     (40, 50, 1, 0, True), (70, 300, 31, 1, False), (130, 260, 63, 0, True), (300, 257, 255, 0, False),
     (64, 128, 225, 7, True), (650, 4404, 130, 6, False), (1030, 12500, 200, 0, True), (1030, 12500, 64, 0, False),
+    # small tiles dealt over K to groups of waves, several rounds of them and what is left
+    (20, 4000, 6000, 0, True), (129, 2100, 2600, 3, False), (40, 7000, 1500, 8, True), (64, 512, 8192, 0, False),
+    (300, 1000, 2048, 1, True),
 ]
 IDS = ["x".join(map(str, s[:3])) for s in SHAPES]
 
