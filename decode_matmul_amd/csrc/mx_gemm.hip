@@ -298,6 +298,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) mx_gemm_kernel(MxMatmulA
         const GlobalBytes wb = scalar_base(wbase + (t * KG + kg) * (kSlab / 2));
 #pragma unroll
         for (int j = 0; j < kXLoads; ++j) {
+            if (BM == 32 && x_group(j) * 8 >= m_rows) continue;     // rows no token reads: few tokens fetch less
             const GlobalBytes from = xb + lane_offset(xsrc[j % (kXLoads / KD)]) + x_unit(j) * kRow;
             if (MXX || DIRECT) load_lds16(from, st + x_lds(j));
             else xr[j] = *(const __attribute__((address_space(1))) u32x4h*)from;
