@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) mx_gemm_kernel(MxMatmulA
     static_assert(kXUnit % 1024 == 0 && kXLoads % KD == 0, "a load stays in a unit");
     static_assert(MXX || KD == 2 || KD == 4, "w_slot");
     static_assert(!MXX || BM + BN <= kThreads, "a thread for each row's scales");
-    static_assert(KG == 1 || (!GROUPED && !MXX && KG * KD >= 8), "a group fetches the scales of each of its slabs");
+    static_assert(KG == 1 || (!GROUPED && (MXX || KG * KD >= 8)), "a group fetches the scales of each of its slabs");
     __shared__ __attribute__((aligned(1024))) uint8_t stages0[KG * kStage];
     __shared__ __attribute__((aligned(1024))) uint8_t stages1[KG * kStage];
 
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) mx_gemm_kernel(MxMatmulA
     const uint8_t* const xscales = MXX ? a.x_scales + p.m0 * nb : nullptr;
     static_assert(!MXX || !DIRECT || kSRow == 16, "a lane brings a row's scales");
     uint32_t ssrc[NT];
-    const bool stages_w = wave < BN / 64;
+    const bool stages_w = BN % 64 == 0 ? wave < BN / 64 : tid < BN;
     if (MXX) {
         ssrc[0] = lane_offset((uint32_t)(stages_w ? w_row(tid) : (int)x_row((tid - BN) & (BM - 1))) * (uint32_t)nb);
     } else {
@@ -290,7 +290,8 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) mx_gemm_kernel(MxMatmulA
     Scales sreg;                                // MXX: scales on their way
     auto start = [&](uint8_t* st, int64_t t) {  // slab t, a whole one
         if (MXX) {
-            const GlobalBytes from = scalar_base((stages_w ? wscales : xscales) + (t * KG + kg) * kSRow) + lane_offset(ssrc[0]);
+            const uint8_t* const rows = (stages_w ? wscales : xscales) + (t * KG + kg) * kSRow;
+            const GlobalBytes from = (BN % 64 == 0 ? scalar_base(rows) : (GlobalBytes)rows) + lane_offset(ssrc[0]);
             if (!DIRECT) sreg = *(const __attribute__((address_space(1))) ScalesAt*)from;
             else if (wave < (BM + BN) / 64) load_lds16(from, st + kXBytes + kWBytes + wave * 1024);
         }
@@ -670,6 +671,9 @@ bool mx_gemm_takes(const MxMatmulArgs& a) {
 //     M = 32, 8192 x 8192   16 / 33     M =  64, 4096 x 4096    8.0 / 15.7
 //     M = 64, 8192 x 8192   27 / 33     M = 128, 4096 x 4096   10.7 / 15.7
 //     M = 64, 4096 x 14336  24 / 55     M = 256, 4096 x 4096   19.8 / 16.1
+// MXFP4 (slabs of 256 columns), 32 x 32 / 64 x 64:
+//     M = 32, 8192 x 8192   12.6 / 17.9   M =  64, 4096 x 4096  6.3 / 8.0
+//     M = 64, 8192 x 8192   15.7 / 18.4   M = 256, 4096 x 4096  13.0 / 8.4
 // (two groups of 64 x 64 gain nothing, 37.6 at M = 64, 8192 x 8192: the bytes a unit
 // fetches stay the same.)
 // Experts: by the slots an expert has on average, 32 x 128 / 64 x 256
@@ -683,8 +687,10 @@ hipError_t launch_mx_gemm(const MxMatmulArgs& a, hipStream_t s) {
                                                          : launch_bf16<64, 256, 1, 4, 2, 1, true>(a, s);
     const int64_t cus = compute_unit_count();
     auto tiles = [&](int64_t side) { return ((a.M + side - 1) / side) * ((a.N + side - 1) / side); };
-    if (!a.x_codes && tiles(32) <= cus) return launch_bf16<32, 32, 1, 1, 4, 4, false>(a, s);
-    if (!a.x_codes && tiles(32) <= 2 * cus) return launch_bf16<32, 32, 1, 1, 2, 4, false>(a, s);
+    if (tiles(32) <= 2 * cus) {
+        if (a.x_codes) return launch<true, false, 32, 32, 1, 1, 1, 4, false>(a, s);
+        return tiles(32) <= cus ? launch_bf16<32, 32, 1, 1, 4, 4, false>(a, s) : launch_bf16<32, 32, 1, 1, 2, 4, false>(a, s);
+    }
     if (4 * tiles(256) >= 3 * cus)
         return a.x_codes ? launch<true, false, 256, 256, 2, 4, 1, 1, false>(a, s) : launch_bf16<256, 256, 2, 4, 2, 1, false>(a, s);
     if (4 * tiles(128) >= 3 * cus)

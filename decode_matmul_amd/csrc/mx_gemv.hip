@@ -346,10 +346,15 @@ hipError_t launch_mx_matmul(const MxMatmulArgs& a, hipStream_t s) {
     // One pass of 16 tokens against the tiled form (us, tiled from the second figure on):
     //   bf16   M = 16   8192 x 8192  14.5 / 14.7   4096 x 4096  6.7 / 7.6   14336 x 4096  12.3 / 14.2
     //          M = 32   8192 x 8192  22.1 / 16.1   4096 x 4096  10.2 / 7.7  14336 x 4096  19.2 / 15.8
-    //   MXFP4  M = 32   8192 x 8192  21 / 19       4096 x 4096  8.8 / 8.4   4096 x 14336  18 / 30
+    // MXFP4 activations, whose tiles fetch little, pass earlier where the 32 x 32 tiles
+    // of one row of them fill the chip (64 x 64 tiles, past two a unit, do not pay):
+    //   M = 1      8192 x 8192  11.3 / 11.5   14336 x 4096  9.4 / 8.6    28672 x 8192  26 / 36
+    //   M = 16     8192 x 8192  14.3 / 12.6   14336 x 4096  11.2 / 10.1  28672 x 8192  30 / 39
+    //              4096 x 4096  6.2 / 5.9      4096 x 14336 12.9 / 17.4
     // and for experts up to about six slots each (64 experts of 2048 x 4096: 65 us
     // against 72 at 4 slots, 84 against 76 at 8).
-    const int64_t few = a.x_codes && tiles < 2 * cus ? 32 : 16;
+    const int64_t halves = (a.N + 31) / 32;
+    const int64_t few = !a.x_codes || 2 * halves <= cus || halves > 2 * cus ? 16 : halves <= cus ? 8 : 0;
     const bool many = a.n_experts > 0 ? a.M * a.top_k >= 6 * (int64_t)a.n_experts : a.M > few;
     if (many && mx_gemm_takes(a)) return launch_mx_gemm(a, s);
     if (a.n_experts > 0)
