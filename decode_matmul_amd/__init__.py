@@ -479,7 +479,7 @@ def _float_dtype(t, name):
     raise TypeError(f"{name} dtype {t.dtype} must be float32 or bfloat16")
 
 
-def _ptr(t, name, dtypes, numel, device):
+def _checked(t, name, dtypes, numel, device):
     """The address of a contiguous tensor of `numel` elements on the device."""
     if t is None or t.dtype not in dtypes or t.numel() != numel or not t.is_contiguous() or t.device != device:
         _need(t, name, dtypes, numel, device)
@@ -487,7 +487,7 @@ def _ptr(t, name, dtypes, numel, device):
 
 
 def _maybe(t, name, dtypes, numel, device):
-    return None if t is None else _ptr(t, name, dtypes, numel, device)
+    return None if t is None else _checked(t, name, dtypes, numel, device)
 
 
 def _call(what, fn, device, *args):
@@ -515,7 +515,7 @@ def mx_pack(W, codes, scales, status=None):
     ldw = _rows(W, "W", (W.dtype,), rows, K, dev)
     nb = -(-K // 32)
     _call("mx_pack", _lib.mx_pack, dev, W.data_ptr(), wdt, rows, K, ldw,
-          _ptr(codes, "codes", _U8, rows * nb * 16, dev), _ptr(scales, "scales", _U8, rows * nb, dev),
+          _checked(codes, "codes", _U8, rows * nb * 16, dev), _checked(scales, "scales", _U8, rows * nb, dev),
           _maybe(status, "status", _I32, 1, dev))
     return status
 
@@ -526,9 +526,9 @@ def mx_unpack(codes, scales, rows, K, W_out, status=None):
     dev = codes.device
     nb = -(-K // 32)
     odt = _float_dtype(W_out, "W_out")
-    _call("mx_unpack", _lib.mx_unpack, dev, _ptr(codes, "codes", _U8, rows * nb * 16, dev),
-          _ptr(scales, "scales", _U8, rows * nb, dev), rows, K,
-          _ptr(W_out, "W_out", (W_out.dtype,), rows * K, dev), odt, _maybe(status, "status", _I32, 1, dev))
+    _call("mx_unpack", _lib.mx_unpack, dev, _checked(codes, "codes", _U8, rows * nb * 16, dev),
+          _checked(scales, "scales", _U8, rows * nb, dev), rows, K,
+          _checked(W_out, "W_out", (W_out.dtype,), rows * K, dev), odt, _maybe(status, "status", _I32, 1, dev))
     return status
 
 
@@ -540,18 +540,18 @@ def mx_matmul(x, codes, scales, N, y, bias=None):
     ldx = _rows(x, "x", _BF16, M, K, dev)
     nb = -(-K // 32)
     _call("mx_matmul", _lib.mx_matmul, dev, x.data_ptr(), M, K, ldx,
-          _ptr(codes, "codes", _U8, N * nb * 16, dev), _ptr(scales, "scales", _U8, N * nb, dev), N,
-          _maybe(bias, "bias", _F32, N, dev), _ptr(y, "y", (y.dtype,), M * N, dev), _ydtype(y))
+          _checked(codes, "codes", _U8, N * nb * 16, dev), _checked(scales, "scales", _U8, N * nb, dev), N,
+          _maybe(bias, "bias", _F32, N, dev), _checked(y, "y", (y.dtype,), M * N, dev), _ydtype(y))
 
 
 def mx_matmul_mx(x_codes, x_scales, M, K, codes, scales, N, y, bias=None):
     """mx_matmul with the [M, K] activations as an MXFP4 package too."""
     dev = x_codes.device
     nb = -(-K // 32)
-    _call("mx_matmul_mx", _lib.mx_matmul_mx, dev, _ptr(x_codes, "x_codes", _U8, M * nb * 16, dev),
-          _ptr(x_scales, "x_scales", _U8, M * nb, dev), M, K,
-          _ptr(codes, "codes", _U8, N * nb * 16, dev), _ptr(scales, "scales", _U8, N * nb, dev), N,
-          _maybe(bias, "bias", _F32, N, dev), _ptr(y, "y", (y.dtype,), M * N, dev), _ydtype(y))
+    _call("mx_matmul_mx", _lib.mx_matmul_mx, dev, _checked(x_codes, "x_codes", _U8, M * nb * 16, dev),
+          _checked(x_scales, "x_scales", _U8, M * nb, dev), M, K,
+          _checked(codes, "codes", _U8, N * nb * 16, dev), _checked(scales, "scales", _U8, N * nb, dev), N,
+          _maybe(bias, "bias", _F32, N, dev), _checked(y, "y", (y.dtype,), M * N, dev), _ydtype(y))
 
 
 def moe_route_workspace_bytes(M, top_k, n_experts):
@@ -567,7 +567,7 @@ def _workspace(workspace, dev):
     if workspace is None:
         return None, 0
     n = workspace.numel()
-    return _ptr(workspace, "workspace", _U8, n, dev), n
+    return _checked(workspace, "workspace", _U8, n, dev), n
 
 
 def moe_route(expert_ids, n_experts, counts, offsets, order, workspace=None):
@@ -577,9 +577,9 @@ def moe_route(expert_ids, n_experts, counts, offsets, order, workspace=None):
     dev = expert_ids.device
     M, top_k = expert_ids.shape
     ws, nbytes = _workspace(workspace, dev)
-    _call("moe_route", _lib.moe_route, dev, _ptr(expert_ids, "expert_ids", _I32, M * top_k, dev), M, top_k,
-          n_experts, _ptr(counts, "counts", _I32, n_experts, dev),
-          _ptr(offsets, "offsets", _I32, n_experts + 1, dev), _ptr(order, "order", _I32, M * top_k, dev),
+    _call("moe_route", _lib.moe_route, dev, _checked(expert_ids, "expert_ids", _I32, M * top_k, dev), M, top_k,
+          n_experts, _checked(counts, "counts", _I32, n_experts, dev),
+          _checked(offsets, "offsets", _I32, n_experts + 1, dev), _checked(order, "order", _I32, M * top_k, dev),
           ws, nbytes)
 
 
@@ -591,10 +591,10 @@ def mx_matmul_experts(x, codes, scales, N, y, n_experts, offsets, order, top_k, 
     ldx = _rows(x, "x", _BF16, M, K, dev)
     rows, nb = n_experts * N, -(-K // 32)
     _call("mx_matmul_experts", _lib.mx_matmul_experts, dev, x.data_ptr(), M, K, ldx,
-          _ptr(codes, "codes", _U8, rows * nb * 16, dev), _ptr(scales, "scales", _U8, rows * nb, dev), N,
+          _checked(codes, "codes", _U8, rows * nb * 16, dev), _checked(scales, "scales", _U8, rows * nb, dev), N,
           n_experts, _maybe(bias, "bias", _F32, rows, dev),
-          _ptr(offsets, "offsets", _I32, n_experts + 1, dev), _ptr(order, "order", _I32, M * top_k, dev),
-          top_k, _ptr(y, "y", (y.dtype,), M * top_k * N, dev), _ydtype(y))
+          _checked(offsets, "offsets", _I32, n_experts + 1, dev), _checked(order, "order", _I32, M * top_k, dev),
+          top_k, _checked(y, "y", (y.dtype,), M * top_k * N, dev), _ydtype(y))
 
 
 def moe_balance_workspace_bytes(M, n_experts):
@@ -616,8 +616,8 @@ def moe_balance(logits, counts, loss, weights, token_mask=None, workspace=None):
     ldl = _rows(logits, "logits", (logits.dtype,), M, E, dev)
     ws, nbytes = _workspace(workspace, dev)
     _call("moe_balance", _lib.moe_balance, dev, logits.data_ptr(), ldt, M, E, ldl,
-          _maybe(token_mask, "token_mask", _MASK, M, dev), _ptr(counts, "counts", _I32, E, dev),
-          _ptr(loss, "loss", _F32, 1, dev), _ptr(weights, "weights", _F32, E, dev), ws, nbytes)
+          _maybe(token_mask, "token_mask", _MASK, M, dev), _checked(counts, "counts", _I32, E, dev),
+          _checked(loss, "loss", _F32, 1, dev), _checked(weights, "weights", _F32, E, dev), ws, nbytes)
 
 
 def moe_balance_grad(logits, weights, dloss, dlogits, token_mask=None):
@@ -628,8 +628,8 @@ def moe_balance_grad(logits, weights, dloss, dlogits, token_mask=None):
     M, E = logits.shape
     ldl = _rows(logits, "logits", (logits.dtype,), M, E, dev)
     _call("moe_balance_grad", _lib.moe_balance_grad, dev, logits.data_ptr(), ldt, M, E, ldl,
-          _maybe(token_mask, "token_mask", _MASK, M, dev), _ptr(weights, "weights", _F32, E, dev),
-          _ptr(dloss, "dloss", _F32, 1, dev), _ptr(dlogits, "dlogits", (logits.dtype,), M * E, dev))
+          _maybe(token_mask, "token_mask", _MASK, M, dev), _checked(weights, "weights", _F32, E, dev),
+          _checked(dloss, "dloss", _F32, 1, dev), _checked(dlogits, "dlogits", (logits.dtype,), M * E, dev))
 
 
 def raw():
