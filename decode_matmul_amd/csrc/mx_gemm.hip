@@ -22,8 +22,8 @@
 // (bf16 2048 x 8192 x 8192: 1.3 PFLOP/s at 2.1 GHz; MXFP4 activations: with the
 // loads left out 62 of 75 us remain, and the same instructions from registers
 // alone reach 7.3 PFLOP/s).  Smaller tiles: what a compute unit can have under
-// way, about 40 KB, against the latency of memory: 64 x 64 tiles take 1.1 us a
-// slab of 40 KB whether K is dealt to one group of waves or to two.
+// way, about 40 KB, against the latency of memory, and the requests for it (one for
+// 8 bytes costs as much as one for a line).
 #include <type_traits>
 
 #include "mx.h"
