@@ -225,9 +225,9 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) mx_gemm_kernel(MxMatmulA
     auto w_row = [&](int i) { return i < n_rows ? i : n_rows - 1; };
 
     // Loads to LDS fill 1024 bytes at a time: eight rows of 128 bytes, lane l the
-    // chunk whose slot is l % 8 of row l / 8 (or 32 of W's 32-byte rows, lane l half
-    // l % 2 of row l / 2).  Load j of wave w is row group (w kXLoads + j) of all of
-    // the slab's units; a wave's row groups repeat from unit to unit.
+    // chunk whose slot is l % 8 of row l / 8 (W's rows of 64 bytes likewise, four lanes
+    // each).  Load j of wave w is row group w + (j % (kXLoads / KD)) kWaves of a unit;
+    // a wave's row groups repeat from unit to unit.
     const int x_sub = lane >> 3;
     auto x_group = [&](int j) { return wave + (j % (kXLoads / KD)) * kWaves; };
     auto x_unit = [&](int j) { return j / (kXLoads / KD); };
@@ -256,8 +256,8 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) mx_gemm_kernel(MxMatmulA
         wsrc[j] = lane_offset((uint32_t)w_row(w_tile_row(j)) * ((uint32_t)nb * 16u) + (uint32_t)(w_chunk(j) * 16 + w_unit(j) * (kUnit / 2)));
     }
     // Scales.  MXX: thread tid stages a slab's bytes of one row of W (the first BN
-    // threads) or x, or (DIRECT) 16 bytes a row go straight to LDS.  Otherwise lane (r, g) keeps eight bytes, the
-    // scales of four units, of each of its rows of W.
+    // threads) or x, or (DIRECT) 16 bytes a row go straight to LDS.  Otherwise lane
+    // (r, g) keeps 16 bytes, the scales of eight units, of each of its rows of W.
     const uint8_t* const wscales = a.scales + (p.expert * a.N + p.n0) * nb;
     const uint8_t* const xscales = MXX ? a.x_scales + p.m0 * nb : nullptr;
     static_assert(!MXX || !DIRECT || kSRow == 16, "a lane brings a row's scales");
