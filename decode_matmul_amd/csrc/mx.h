@@ -67,6 +67,17 @@ __device__ __forceinline__ u32x4 load_x8(const uint16_t* row, int64_t k, int64_t
     return v;
 }
 
+// The codes of a cut block, of which the first `kept` count.  The others meet
+// activations that are 0, but with the largest scales they stand for infinities.
+__device__ __forceinline__ u32x4 cut_codes(u32x4 c, int kept) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int n = kept - 8 * i;
+        c[i] &= n >= 8 ? 0xffffffffu : n > 0 ? (1u << (4 * n)) - 1u : 0u;
+    }
+    return c;
+}
+
 // A uniform pointer the compiler keeps in scalar registers as it is, so that a
 // lane's address stays base + 32-bit offset (folded into per-lane pointers,
 // the slabs' addresses take more registers than there are).

@@ -502,6 +502,10 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) mx_gemm_kernel(MxMatmulA
             if (!MXX && (KG > 1 ? k == 0 : (first + k) % 8 == 0)) take_scales(first + k);
             read(stage0, k, 0);
             read(stage0, k, 1);
+            if (!MXX && a.K % 32 != 0 && k + 1 == units - first && 2 * (int)(first + k) + g == (int)nb - 1) {
+#pragma unroll
+                for (int i = 0; i < NT; ++i) wf[0][i] = cut_codes(wf[0][i], (int)(a.K % 32));
+            }
             multiply(S0());
             read(stage0, k, 2);
             multiply(S1());

@@ -21,6 +21,8 @@
 //  * bf16 activations of a chunk, straight to a buffer of the wave's own.
 // 16-byte pieces are permuted within their rows so that the 16 rows of a
 // fragment read hit all banks.
+#include <type_traits>
+
 #include "mx.h"
 
 namespace dmm {
@@ -181,7 +183,7 @@ __global__ void __launch_bounds__(64 * W, 2) mx_gemv_kernel(MxMatmulArgs a, int 
         f32x4 acc[NT];
 #pragma unroll
         for (int i = 0; i < NT; ++i) acc[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
-        auto multiply = [&](const uint8_t* b, const u32x4* xc, uint64_t xs, int c) {
+        auto multiply = [&](const uint8_t* b, const u32x4* xc, uint64_t xs, int c, auto tail) {
             uint64_t sc[NT];
 #pragma unroll
             for (int i = 0; i < NT; ++i)
@@ -191,6 +193,11 @@ __global__ void __launch_bounds__(64 * W, 2) mx_gemv_kernel(MxMatmulArgs a, int 
                 u32x4 w[NT];
 #pragma unroll
                 for (int i = 0; i < NT; ++i) w[i] = *(const u32x4*)(b + i * 2048 + wat[u]);
+                if constexpr (!MXX && decltype(tail)::value) {
+                    const int left = (int)lane_offset((uint32_t)a.K) - 32 * (8 * c + 4 * u + g);
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) w[i] = cut_codes(w[i], left);
+                }
                 if (MXX) {
                     const int s = (int)((uint32_t)(xs >> (32 * u)) >> (8 * g));
 #pragma unroll
@@ -279,19 +286,19 @@ __global__ void __launch_bounds__(64 * W, 2) mx_gemv_kernel(MxMatmulArgs a, int 
                 if (c == wave && c + W < full) wait_loads<kXLoads>();
                 else if (c + W < full) wait_loads<kLoads>();
                 else wait_loads<0>();
-                multiply(b0, xc0, xs0, c);
+                multiply(b0, xc0, xs0, c, std::false_type());
                 if (c + 2 * W < full) load(b0, xc0, xs0, c + 2 * W);
                 if (c + W >= c_end) break;
                 if (c + 2 * W < full) wait_loads<kLoads>();
                 else wait_loads<0>();
-                multiply(b1, xc1, xs1, c + W);
+                multiply(b1, xc1, xs1, c + W, std::false_type());
                 if (c + 3 * W < full) load(b1, xc1, xs1, c + 3 * W);
             }
         }
         if (full < chunks && full % W == wave) {
             load_tail(b0, xc0, xs0, full);
             wait_loads<0>();
-            multiply(b0, xc0, xs0, full);
+            multiply(b0, xc0, xs0, full, std::true_type());
         }
         lds_barrier();
         f32x4* const red = (f32x4*)&buf0[0][0];                     // [W][NT][64]: the buffers are free now
