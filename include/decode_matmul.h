@@ -485,9 +485,9 @@ int mx_pack(const void* W, int32_t w_dtype, int64_t rows, int64_t K, int64_t ldw
 
 /*
  * mx_unpack -- decode an MXFP4 package to W_out [rows, K] of out_dtype, row r
- * at element r * K.  Both TQ_F32 and TQ_BF16 hold every value exactly (2, 3, 4
- * and 6 times 2^127, which neither holds and mx_pack never writes, become
- * infinities).
+ * at element r * K.  Both TQ_F32 and TQ_BF16 hold every value below 2^128
+ * exactly; the others (2, 3, 4 and 6 times 2^127, 4 and 6 times 2^126), which
+ * mx_pack never writes, become infinities.
  *
  *  d_status  device int32, or NULL for no report; set to 0, then
  *            TQ_DATA_RANGE if a block is NaN (s = 255), TQ_DATA_PADDING if a
