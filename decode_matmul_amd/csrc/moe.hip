@@ -418,9 +418,18 @@ __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const void* l
     const bool live = !mask || mask[t] != 0;
     float inv, s;
     const bool some = row_softmax<L>(p, w, inv, s);
+    // w_e - s, of a token that has chosen its expert, is far below the rounding of s:
+    // what s is off by comes back as the mean of the differences and is taken off again
+    float off = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        w[i] -= s;
+        off = __builtin_fmaf(w[i], p[i], off);
+    }
+    off = group_sum<L>(off) * inv;
     const float up = dloss[0] * inv;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = up * p[i] * (w[i] - s);
+    for (int i = 0; i < 8; ++i) p[i] = up * p[i] * (w[i] - off);
     if (!(some && live)) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) p[i] = 0.f;

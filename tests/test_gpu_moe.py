@@ -353,3 +353,35 @@ def test_layer_together(dmm):
         xq = oracle.mx_unpack(*oracle.mx_pack(x)[:2], K)
         w3 = oracle.mx_unpack(c3, s3, K)
         assert_close(eager[7], xq @ w3.T, np.abs(xq) @ np.abs(w3).T, K, torch.float32, "shared")
+
+
+@pytest.mark.parametrize("E", [2, 3, 64, 100, 512])
+@pytest.mark.parametrize("gap", [0, 4, 8, 12, 14, 16, 18, 20, 24])
+def test_gradient_of_confident_tokens(dmm, E, gap):
+    """A token whose top logit leads by `gap`: w_e - s is then small against w and
+    s themselves.  With the terms centred, d_j = w_j - s for the computed s = s* + h,
+    |h| <= rel s*, and the result p_e (d_e - sum_j p_j d_j), h drops out but for
+    its product with the error of p: off by at most 2 rel p_e (D_e + sum_j p_j D_j
+    + 2 rel s*), D_j = |w_j - s*|, with rel = (d + 32) 2^-23 of a probability."""
+    say(f"moe_balance_grad of confident tokens E={E} gap={gap}")
+    rng = np.random.default_rng(E + gap)
+    M = 96
+    z = bf16_values(rng.standard_normal((M, E)).astype(np.float32))
+    top = rng.integers(0, E, M)
+    z[np.arange(M), top] = z.max(axis=1) + gap
+    z = bf16_values(z)
+    w = (rng.integers(0, 60, E) / 97.0).astype(np.float32)
+    p = np.exp(z.astype(np.float64) - z.max(axis=1, keepdims=True))
+    p /= p.sum(axis=1, keepdims=True)
+    s = (p * w).sum(axis=1, keepdims=True)
+    D = np.abs(w - s)
+    # w - s itself cancels in 64 bits too late to matter: 2^-53 against 1e-9
+    ref = p * (w - s)
+    rel = ((z.max(axis=1) - z.min(axis=1) + 32) * 2.0 ** -23)[:, None]
+    tol = 2 * rel * p * (D + (p * D).sum(axis=1, keepdims=True) + 2 * rel * s)
+    for dtype, step in ((torch.float32, 2.0 ** -24), (torch.bfloat16, 2.0 ** -8)):
+        Z = dev(z) if dtype == torch.float32 else bf16_of(z)
+        g = torch.empty((M, E), dtype=dtype, device=DEV)
+        dmm.moe_balance_grad(Z, dev(w), torch.ones(1, device=DEV), g)
+        off = np.abs(host(g).astype(np.float64) - ref)
+        assert (off <= tol + step * np.abs(ref)).all(), (off / (tol + step * np.abs(ref))).max()
