@@ -12,7 +12,6 @@ typedef float f32x4a __attribute__((ext_vector_type(4), aligned(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint64_t u64u __attribute__((aligned(1)));
-typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(1)));
 
 // An E8M0 byte as the fp32 whose exponent field it is: what the scaled
 // conversions take (0 stands for 2^-127 and 255 for NaN there).

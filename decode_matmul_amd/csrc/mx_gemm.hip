@@ -44,15 +44,6 @@ __device__ __forceinline__ int w_slot(int row) {
     return LANES == 8 ? swizzle(row) : ((row >> 2) ^ (row >> 3)) & 3;
 }
 
-// No load and no LDS access of this wave outstanding (expcnt aside), then the
-// workgroup's barrier.
-__device__ __forceinline__ void wait_and_meet() {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x70);
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
-
 // The workgroup's tile: its tokens are positions [m0, m_end) of the batch or
 // of the order list, its rows of W start at n0.
 struct Place {
