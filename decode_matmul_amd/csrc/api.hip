@@ -451,8 +451,8 @@ int moe_balance(const void* logits, int32_t l_dtype, int64_t M, int32_t n_expert
         !aligned(weights, 4) || !aligned(workspace, 8))
         return TQ_ERR_ALIGN;
     if (need > 0 && workspace_bytes < need) return TQ_ERR_SHAPE;
-    return grid_status(dmm::launch_moe_balance(logits, l_dtype, M, n_experts, ldl, token_mask, counts, loss,
-                                               weights, workspace, (hipStream_t)stream));
+    return hip_status(dmm::launch_moe_balance(logits, l_dtype, M, n_experts, ldl, token_mask, counts, loss,
+                                              weights, workspace, (hipStream_t)stream));
 }
 
 int moe_balance_grad(const void* logits, int32_t l_dtype, int64_t M, int32_t n_experts, int64_t ldl,

@@ -308,7 +308,7 @@ constexpr int kMoeMaxExperts = 512;
 int64_t moe_route_ws_bytes(int64_t slots, int E);
 hipError_t launch_moe_route(const int32_t* ids, int64_t slots, int E, int32_t* counts, int32_t* offsets,
                             int32_t* order, void* workspace, hipStream_t s);
-int64_t moe_balance_ws_bytes(int64_t M, int E);
+int64_t moe_balance_ws_bytes(int64_t M, int E);     // -1: more threads than a launch can have
 hipError_t launch_moe_balance(const void* logits, int l_dtype, int64_t M, int E, int64_t ldl, const uint8_t* mask,
                               const int32_t* counts, float* loss, float* weights, void* workspace, hipStream_t s);
 hipError_t launch_moe_balance_grad(const void* logits, int l_dtype, int64_t M, int E, int64_t ldl,

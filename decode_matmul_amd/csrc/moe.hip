@@ -479,7 +479,6 @@ template <bool BF16, int L>
 hipError_t balance(const void* logits, int64_t M, int E, int64_t ldl, const uint8_t* mask, const int32_t* counts,
                    float* loss, float* weights, double* partial, hipStream_t s) {
     const int64_t blocks = loss_blocks(M, E);
-    if (!grid_fits(blocks, kBalThreads)) return hipErrorInvalidConfiguration;
     balance_loss_kernel<BF16, L><<<(unsigned)blocks, kBalThreads, 0, s>>>(logits, M, E, ldl, mask, counts, loss,
                                                                          weights, partial);
     hipError_t e = hipGetLastError();
@@ -546,7 +545,10 @@ hipError_t launch_moe_route(const int32_t* ids, int64_t slots, int E, int32_t* c
     return hipGetLastError();
 }
 
-int64_t moe_balance_ws_bytes(int64_t M, int E) { return loss_blocks(M, E) == 1 ? 0 : loss_blocks(M, E) * 16; }
+int64_t moe_balance_ws_bytes(int64_t M, int E) {
+    const int64_t blocks = loss_blocks(M, E);
+    return !grid_fits(blocks, kBalThreads) ? -1 : blocks == 1 ? 0 : blocks * 16;
+}
 
 hipError_t launch_moe_balance(const void* logits, int l_dtype, int64_t M, int E, int64_t ldl, const uint8_t* mask,
                               const int32_t* counts, float* loss, float* weights, void* workspace, hipStream_t s) {

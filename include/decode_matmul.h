@@ -609,6 +609,8 @@ int mx_matmul_experts(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, cons
  *              Overwritten; calls that share it must not overlap.
  *
  * Softmax statistics are fp32, the sum over tokens is float64 in a fixed order.
+ * With L = n_experts / 8 rounded up to a power of two, M L is at most 2^34 -
+ * 1024 (TQ_ERR_SHAPE).
  */
 int moe_balance(const void* logits, int32_t l_dtype, int64_t M, int32_t n_experts, int64_t ldl,
                 const uint8_t* token_mask, const int32_t* counts, float* loss, float* weights,
@@ -627,6 +629,8 @@ int64_t moe_balance_workspace_bytes(int64_t M, int32_t n_experts);
  *  dloss    device fp32 [1].
  *  dlogits  device [M, n_experts] of l_dtype, row t at element t * n_experts;
  *           rows of masked tokens, and of -inf only, are 0.
+ *
+ * With L as above, M L is at most 2^32 - 256 (TQ_ERR_SHAPE).
  */
 int moe_balance_grad(const void* logits, int32_t l_dtype, int64_t M, int32_t n_experts, int64_t ldl,
                      const uint8_t* token_mask, const float* weights, const float* dloss,

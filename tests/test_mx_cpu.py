@@ -220,3 +220,18 @@ def test_binding_refuses_wrong_tensors():
         dmm.moe_balance_grad(torch.zeros(2, 4), torch.zeros(4), torch.zeros(1), torch.zeros(2, 3, dtype=f32))
     with pytest.raises(ValueError):
         dmm.moe_balance_workspace_bytes(1, 0)
+
+
+def test_moe_balance_largest_batches():
+    """2^24 - 1 workgroups are the most: of 1024 / L tokens for the loss, 256 / L for
+    the gradient, L = 64 lanes a token of 512 experts, 8 of 64."""
+    for E, L in ((512, 64), (257, 64), (64, 8)):
+        most = ((1 << 24) - 1) * 1024 // L
+        if most < BIG:
+            assert lib.moe_balance_workspace_bytes(most, E) == 16 * ((1 << 24) - 1)
+            assert lib.moe_balance_workspace_bytes(most + 1, E) == -1
+            with pytest.raises(ValueError):
+                dmm.moe_balance_workspace_bytes(most + 1, E)
+            assert lib.moe_balance(FAKE, 0, most + 1, E, E, None, FAKE, FAKE, FAKE, FAKE, 1 << 40, None) == SHAPE
+        assert lib.moe_balance_grad(FAKE, 0, ((1 << 24) - 1) * 256 // L + 1, E, E, None, FAKE, FAKE, FAKE, None) == SHAPE
+    assert lib.moe_balance_workspace_bytes(BIG - 1, 8) > 0
