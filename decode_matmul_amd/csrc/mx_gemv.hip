@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(64 * W, 2) mx_gemv_kernel(MxMatmulArgs a, int 
 template <bool MXX, int TB, int NT, int W, bool DIRECT, bool GROUPED>
 hipError_t launch(const MxMatmulArgs& a, hipStream_t s) {
     constexpr int rows = 16 * NT;
-    const int64_t blocks = (a.N + rows - 1) / rows * (GROUPED ? a.n_experts + 1 : 1);
+    const int64_t blocks = (a.N + rows - 1) / rows * (GROUPED ? (int64_t)a.n_experts + 1 : 1);
     if (!grid_fits(blocks, 64 * W)) return hipErrorInvalidConfiguration;
     const int scale_lines = a.K % 512 == 0 && ((uintptr_t)a.scales & 15) == 0;
     mx_gemv_kernel<MXX, TB, NT, W, DIRECT, GROUPED><<<(unsigned)blocks, 64 * W, 0, s>>>(a, scale_lines);

@@ -235,3 +235,10 @@ def test_moe_balance_largest_batches():
             assert lib.moe_balance(FAKE, 0, most + 1, E, E, None, FAKE, FAKE, FAKE, FAKE, 1 << 40, None) == SHAPE
         assert lib.moe_balance_grad(FAKE, 0, ((1 << 24) - 1) * 256 // L + 1, E, E, None, FAKE, FAKE, FAKE, None) == SHAPE
     assert lib.moe_balance_workspace_bytes(BIG - 1, 8) > 0
+
+
+def test_most_experts():
+    """One workgroup for every 32 rows of W and expert, and for the slots of none."""
+    for E in (BIG - 1, 1 << 24):
+        for N in (1, 33, 65):
+            assert lib.mx_matmul_experts(FAKE, 4, 64, 64, FAKE, FAKE, N, E, None, FAKE, FAKE, 2, FAKE, 0, None) == SHAPE
