@@ -90,3 +90,11 @@ def test_smallest_scales(dmm, M, N):
         xc, xs, _ = oracle.mx_pack(x)
         dmm.mx_matmul_mx(dev(xc), dev(xs), M, K, dev(c), dev(s), N, y)
         assert np.array_equal(host(y), ref), f"MXFP4, k = {k}"
+
+
+def test_call_on_the_current_stream(dmm):
+    say("stream handles")
+    side = torch.cuda.Stream()
+    for stream in (torch.cuda.default_stream(), side):
+        with torch.cuda.stream(stream):
+            assert dmm._raw_stream(0) == torch.cuda.current_stream(0).cuda_stream == stream.cuda_stream

@@ -2,6 +2,9 @@
 hand, and what the entry points and their binding refuse before any launch."""
 
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -242,3 +245,21 @@ def test_most_experts():
     for E in (BIG - 1, 1 << 24):
         for N in (1, 33, 65):
             assert lib.mx_matmul_experts(FAKE, 4, 64, 64, FAKE, FAKE, N, E, None, FAKE, FAKE, 2, FAKE, 0, None) == SHAPE
+
+
+def test_binding_needs_no_private_function_of_torch():
+    """Without them a call takes the current device and stream from the public functions."""
+    program = """
+import types, torch
+for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import decode_matmul_amd as dmm
+torch.cuda.current_device = lambda: 3
+torch.cuda.current_stream = lambda device: types.SimpleNamespace(cuda_stream=70 + device)
+seen = []
+dmm._call("test", lambda *a: seen.append(a) or 0, torch.device("cuda", 3), 1, 2)
+assert seen == [(1, 2, 73)], seen
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", program], cwd=root, check=True)
