@@ -490,9 +490,10 @@ def _maybe(t, name, dtypes, numel, device):
     return None if t is None else _checked(t, name, dtypes, numel, device)
 
 
-# The handle of a device's current stream.  torch.cuda.current_stream makes a Stream
-# object on the way (1.1 us against 0.1); the shorter way is not a public one, and a
-# torch without it is served by the public function.
+# The current device, and the handle of its current stream.  torch.cuda.current_stream
+# makes a Stream object on the way (1.1 us against 0.1); the shorter ways are not public
+# ones, and a torch without them is served by the public functions.
+_current_device = getattr(torch._C, "_cuda_getDevice", lambda: torch.cuda.current_device())
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -502,7 +503,7 @@ def _call(what, fn, device, *args):
     index = device.index
     if device.type != "cuda":
         raise ValueError(f"{what}: tensors are on {device}, not on a GPU")
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         rc = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
