@@ -66,15 +66,12 @@ __device__ __forceinline__ u32x4 load_x8(const uint16_t* row, int64_t k, int64_t
     return v;
 }
 
-// The codes of a cut block, of which the first `kept` count.  The others meet
+// The codes of a cut block, of which the first `kept` (0 .. 32) count.  The others meet
 // activations that are 0, but with the largest scales they stand for infinities.
 __device__ __forceinline__ u32x4 cut_codes(u32x4 c, int kept) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int n = kept - 8 * i;
-        c[i] &= n >= 8 ? 0xffffffffu : n > 0 ? (1u << (4 * n)) - 1u : 0u;
-    }
-    return c;
+    const uint64_t lo = kept < 16 ? (1ull << (4 * kept)) - 1ull : ~0ull;
+    const uint64_t hi = kept > 16 ? ~0ull >> (128 - 4 * kept) : 0ull;
+    return c & (u32x4){(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
 
 // A uniform pointer the compiler keeps in scalar registers as it is, so that a

@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(64 * W, 2) mx_gemv_kernel(MxMatmulArgs a, int 
                 if constexpr (!MXX && decltype(tail)::value) {
                     const int left = (int)lane_offset((uint32_t)a.K) - 32 * (8 * c + 4 * u + g);
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) w[i] = cut_codes(w[i], left);
+                    for (int i = 0; i < NT; ++i) w[i] = cut_codes(w[i], left < 0 ? 0 : left < 32 ? left : 32);
                 }
                 if (MXX) {
                     const int s = (int)((uint32_t)(xs >> (32 * u)) >> (8 * g));
