@@ -649,33 +649,34 @@ bool mx_gemm_takes(const MxMatmulArgs& a) {
 
 // The largest tile that still gives every compute unit one (its rate is the
 // highest, 1.3 PFLOP/s with bf16 and 3.6 with MXFP4 activations, but a wave of
-// tiles costs its time whether it fills the chip or not).  us by tile, in one run:
+// tiles costs its time whether it fills the chip or not).  us by tile, in one run (graph
+// replays, as at launch_mx_matmul):
 //   bf16    256 x 256 / 128 x 128 / 64 x 64
-//     M = 2048, 8192 x 8192   237 /  269 /  366
-//     M = 1024, 4096 x 4096    89 /   43 /   52
-//     M =  512, 4096 x 4096    88 /   37 /   27
-//     M =   64, 8192 x 8192   155 /   66 /   36
+//     M = 2048, 8192 x 8192   205 /  239 /  334
+//     M = 1024, 4096 x 4096    82 /   41 /   47
+//     M =  512, 4096 x 4096    81 /   36 /   25
+//     M =   64, 8192 x 8192   153 /   67 /   34
 //   MXFP4
-//     M = 2048, 8192 x 8192    83 /  106 /  159
-//     M = 1024, 4096 x 4096    37 /   19 /   24
-//     M =  512, 4096 x 4096    36 /   17 /   13
+//     M = 2048, 8192 x 8192    73 /   97 /  154
+//     M = 1024, 4096 x 4096    32 /   18 /   23
+//     M =  512, 4096 x 4096    31 /   16 /   13
 // Few tiles leave compute units idle and each other one with more to fetch than it
 // can have under way: up to two tiles of 32 x 32 a unit take those, dealt over K to
 // four groups of one wave (a slab of 256 columns each where a unit has one tile, of
 // 128 where two share its LDS).  us, bf16, 32 x 32 / 64 x 64:
-//     M = 32, 8192 x 8192   16 / 33     M =  64, 4096 x 4096    8.0 / 15.7
-//     M = 64, 8192 x 8192   27 / 33     M = 128, 4096 x 4096   10.7 / 15.7
-//     M = 64, 4096 x 14336  24 / 55     M = 256, 4096 x 4096   19.8 / 16.1
+//     M = 32, 8192 x 8192   17 / 33     M =  64, 4096 x 4096    8.9 / 15.7
+//     M = 64, 8192 x 8192   27 / 33     M = 128, 4096 x 4096   11.7 / 15.8
+//     M = 64, 4096 x 14336  24 / 55     M = 256, 4096 x 4096   21.1 / 16.3
 // MXFP4 (slabs of 256 columns), 32 x 32 / 64 x 64:
-//     M = 32, 8192 x 8192   12.6 / 17.9   M =  64, 4096 x 4096  6.3 / 8.0
-//     M = 64, 8192 x 8192   15.7 / 18.4   M = 256, 4096 x 4096  13.0 / 8.4
+//     M = 32, 8192 x 8192   12.5 / 18.4   M =  64, 4096 x 4096  6.3 / 8.4
+//     M = 64, 8192 x 8192   15.9 / 19.6   M = 256, 4096 x 4096  12.8 / 8.6
 // (two groups of 64 x 64 gain nothing, 37.6 at M = 64, 8192 x 8192: the bytes a unit
 // fetches stay the same.)
 // Experts: by the slots an expert has on average, 32 x 128 / 64 x 256
 //     (64 experts of 2048 x 4096)
-//     32   109 / 116     48   127 / 112     256   435 / 331
+//     32   96 / 102     48   116 / 105     256   390 / 289
 // (four waves of 64 x 64 a tile of 64 x 256; eight of 32 x 64 took 348 where they
-// take 326, tiles of 128 x 256 took 333 there and 181 against 134 at 64 slots).
+// took 326, tiles of 128 x 256 took 333 there and 181 against 134 at 64 slots).
 hipError_t launch_mx_gemm(const MxMatmulArgs& a, hipStream_t s) {
     if (a.n_experts > 0)
         return a.M * a.top_k < 40 * (int64_t)a.n_experts ? launch_bf16<32, 128, 1, 4, 4, 1, true>(a, s)

@@ -350,16 +350,23 @@ hipError_t launch_bf16(const MxMatmulArgs& a, hipStream_t s) {
 
 hipError_t launch_mx_matmul(const MxMatmulArgs& a, hipStream_t s) {
     const int64_t tiles = (a.N + 15) / 16, cus = compute_unit_count();
-    // One pass of 16 tokens against the tiled form (us, tiled from the second figure on):
-    //   bf16   M = 16   8192 x 8192  14.5 / 14.7   4096 x 4096  6.7 / 7.6   14336 x 4096  12.3 / 14.2
-    //          M = 32   8192 x 8192  22.1 / 16.1   4096 x 4096  10.2 / 7.7  14336 x 4096  19.2 / 15.8
+    // Times here and in mx_gemm.hip are us a call in a replayed graph, each call with
+    // other weights (600 MB of them, or 24 sets, in turn).
+    // One pass of 16 tokens against the tiled form (tiled from the second figure on):
+    //   bf16   M = 16   8192 x 8192  14.6 / 14.6   4096 x 4096  6.6 / 7.9   14336 x 4096  12.3 / 13.9
+    //          M = 32   8192 x 8192  22.1 / 16.8   4096 x 4096  10.1 / 8.6  14336 x 4096  19.1 / 16.6
     // MXFP4 activations, whose tiles fetch little, pass earlier where the 32 x 32 tiles
-    // of one row of them fill the chip (64 x 64 tiles, past two a unit, do not pay):
-    //   M = 1      8192 x 8192  11.3 / 11.5   14336 x 4096  9.4 / 8.6    28672 x 8192  26 / 36
-    //   M = 16     8192 x 8192  14.3 / 12.6   14336 x 4096  11.2 / 10.1  28672 x 8192  30 / 39
-    //              4096 x 4096  6.2 / 5.9      4096 x 14336 12.9 / 17.4
-    // and for experts up to about six slots each (64 experts of 2048 x 4096: 65 us
-    // against 72 at 4 slots, 84 against 76 at 8).
+    // of one row of them fill the chip (past two a unit, 64 x 64 tiles are no faster for
+    // one token):
+    //   M = 1      8192 x 8192  11.3 / 11.6   14336 x 4096  9.4 / 8.7    28672 x 8192  26.5 / 26.8
+    //   M = 16     8192 x 8192  14.0 / 12.1   14336 x 4096  10.4 / 9.5   28672 x 8192  30.0 / 28.0
+    //              4096 x 4096  6.1 / 5.9      4096 x 14336 11.7 / 17.4
+    // and for experts from six slots each on (64 experts of 2048 x 4096: 61 / 57 us at 4
+    // slots, just past where they cross, 82 / 62 at 6, 95 / 64 at 8).  That is by the
+    // average, for fairly even lists: how long each is only the GPU knows.  300 slots
+    // that all go to one expert take 153 us here, 384 in tiles 20; and the 320 slots of
+    // no expert beside 56 that have one take 50 of 87, as the last workgroups write their
+    // rows one after another.
     const int64_t halves = (a.N + 31) / 32;
     const int64_t few = !a.x_codes || 2 * halves <= cus || halves > 2 * cus ? 16 : halves <= cus ? 8 : 0;
     const bool many = a.n_experts > 0 ? a.M * a.top_k >= 6 * (int64_t)a.n_experts : a.M > few;
@@ -370,9 +377,9 @@ hipError_t launch_mx_matmul(const MxMatmulArgs& a, hipStream_t s) {
     // (K is what there is to spread), more share a workgroup, so that its
     // activations are read once for them.  us at 14336 x 4096 (3.5 tiles a unit) /
     // 8192 x 8192 (2) / 4096 x 4096 (1), by (tiles, waves) of a workgroup:
-    //   M = 1:  (1, 8) 10.3 / 10.6 / 5.2   (2, 4)  9.3 / 12.1 / 6.2   (4, 4) 11.3 / 21.5 / 11.0
-    //   M = 8:  (1, 8) 18.1 / 14.8 / 5.5   (2, 8) 13.2 / 12.0 / 6.1   (2, 4) 10.6 / 13.0 / 6.7
-    //   M = 16: (1, 4) 24.3 / 20.9 / 6.9   (2, 4) 16.2 / 14.9 / 7.5   (4, 4) 12.4 / 17.8 / 9.2
+    //   M = 1:  (1, 8) 10.4 / 11.1 / 5.2   (2, 4)  9.3 / 12.7 / 6.3   (4, 4) 11.2 / 14.9 / 8.0
+    //   M = 8:  (1, 8) 17.6 / 15.2 / 5.6   (2, 8) 13.6 / 12.6 / 6.2   (2, 4) 10.9 / 13.2 / 6.8
+    //   M = 16: (1, 4) 21.7 / 19.5 / 6.6   (2, 4) 15.8 / 14.6 / 7.3   (4, 4) 12.3 / 17.6 / 8.9
     if (a.x_codes)
         return tiles <= 2 * cus ? launch<true, 16, 1, 8, true, false>(a, s) : launch<true, 16, 2, 4, true, false>(a, s);
     if (a.M <= 2) return tiles <= 2 * cus ? launch_bf16<2, 1, 8, false>(a, s) : launch_bf16<2, 2, 4, false>(a, s);

@@ -508,8 +508,9 @@ int mx_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t
  *  y       device [M, N] of y_dtype (fp32, or bf16 nearest-even of the fp32
  *          result).
  *
- * Every weight mx_unpack holds is exact in bf16 and every product in fp32; sums are held in
- * fp32, in an order fixed by the shape (two calls give the same bits).  A NaN
+ * Every weight mx_unpack holds is exact in bf16, and every product in fp32
+ * that fp32 can hold; sums are held in fp32, in an order fixed by the shape (two
+ * calls give the same bits).  A NaN
  * block makes its output column NaN.  What x holds past K, and codes past K,
  * take no part.  M = 0 or N = 0 is a no-op; with K = 0, x and the package may
  * be NULL and y = bias (or 0).  M and N are below 2^31, K is below 2^27; sizes
@@ -521,12 +522,13 @@ int mx_matmul(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint8_
 
 /*
  * mx_matmul_mx -- mx_matmul with the activations in MXFP4 too (mx_pack of x):
- * both operands go undecoded into the scaled matrix instructions, at four
- * times the bf16 rate.
+ * both operands go undecoded into the scaled matrix instructions, whose peak
+ * is four times that of the bf16 ones (2048 tokens, 8192 x 8192, x packed on the
+ * way: 83 us where mx_matmul takes 207).
  *
  *  x_codes, x_scales  device MXFP4 package of the [M, K] activations.
  *
- * Products are exact and sums are held in fp32.  In a ragged last block the
+ * Products that fp32 can hold are exact, sums are held in fp32.  In a ragged last block the
  * codes past K of at least one operand have to be 0, as mx_pack writes them.
  * Every other argument and error is that of mx_matmul.
  */
@@ -608,7 +610,9 @@ int mx_matmul_experts(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, cons
  *              bytes, 8-byte aligned; NULL where that is 0 (few tokens).
  *              Overwritten; calls that share it must not overlap.
  *
- * Softmax statistics are fp32, the sum over tokens is float64 in a fixed order.
+ * Softmax statistics are fp32, with the hardware's exp2 and reciprocal: with d
+ * the spread of a row's finite logits, a probability is within r = (d + 32) 2^-23 of
+ * itself.  The sum over tokens is float64 in a fixed order.
  * With L = n_experts / 8 rounded up to a power of two, M L is at most 2^34 -
  * 1024 (TQ_ERR_SHAPE).
  */
@@ -630,6 +634,8 @@ int64_t moe_balance_workspace_bytes(int64_t M, int32_t n_experts);
  *  dlogits  device [M, n_experts] of l_dtype, row t at element t * n_experts;
  *           rows of masked tokens, and of -inf only, are 0.
  *
+ * With s = sum_j w_j p_tj and r as above, it is off by at most |*dloss| times
+ * 2 r p_te (|w_e - s| + sum_j p_tj |w_j - s| + 2 r s) and half a step of its type.
  * With L as above, M L is at most 2^32 - 256 (TQ_ERR_SHAPE).
  */
 int moe_balance_grad(const void* logits, int32_t l_dtype, int64_t M, int32_t n_experts, int64_t ldl,
