@@ -478,7 +478,7 @@ int rb_matmul7(const uint16_t* x, int64_t M, int64_t K, const uint8_t* codes7, i
  * ties to the even code, magnitudes above 6 taken to 6, the sign kept.  The
  * scaling is exact, so there is one rounding.  A block with a value that is
  * not finite gets s = 255 and codes 0: it decodes to NaN, and so do the
- * products it takes part in.
+ * products it takes part in.  rows * nb is below 2^30 - 64 (TQ_ERR_SHAPE).
  */
 int mx_pack(const void* W, int32_t w_dtype, int64_t rows, int64_t K, int64_t ldw, uint8_t* codes,
             uint8_t* scales, int32_t* d_status, void* stream);
@@ -492,6 +492,8 @@ int mx_pack(const void* W, int32_t w_dtype, int64_t rows, int64_t K, int64_t ldw
  *  d_status  device int32, or NULL for no report; set to 0, then
  *            TQ_DATA_RANGE if a block is NaN (s = 255), TQ_DATA_PADDING if a
  *            code past K is not 0.
+ *
+ * rows * nb is below 2^29 - 32 (TQ_ERR_SHAPE).
  */
 int mx_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, void* W_out,
               int32_t out_dtype, int32_t* d_status, void* stream);
@@ -579,7 +581,9 @@ int64_t moe_route_workspace_bytes(int64_t M, int32_t top_k, int32_t n_experts);
  * [M * top_k, K]: pass M * top_k for M and 1 for top_k with the same lists.
  * Entries of the lists outside their range are skipped (nothing is read or
  * written out of bounds; rows that are then listed nowhere stay as they
- * were).  The accuracy is that of mx_matmul.
+ * were).  The accuracy is that of mx_matmul, and so are the errors of other
+ * arguments and of sizes that need more than 2^32 - 1 threads ((n_experts + 1) *
+ * ceil(N / 32) of 2^24 and more among them).
  */
 int mx_matmul_experts(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint8_t* codes,
                       const uint8_t* scales, int64_t N, int32_t n_experts, const float* bias,
@@ -612,7 +616,7 @@ int mx_matmul_experts(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, cons
  *
  * Softmax statistics are fp32, with the hardware's exp2 and reciprocal: with d
  * the spread of a row's finite logits, a probability is within r = (d + 32) 2^-23 of
- * itself.  The sum over tokens is float64 in a fixed order.
+ * itself (below 2^-126 it may be 0).  The sum over tokens is float64 in a fixed order.
  * With L = n_experts / 8 rounded up to a power of two, M L is at most 2^34 -
  * 1024 (TQ_ERR_SHAPE).
  */

@@ -263,3 +263,9 @@ assert seen == [(1, 2, 73)], seen
 """
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     subprocess.run([sys.executable, "-c", program], cwd=root, check=True)
+
+
+def test_largest_packages():
+    for K, nb in ((32, 1), (33, 2)):
+        assert lib.mx_pack(FAKE, 1, ((1 << 30) - 64) // nb, K, K, FAKE, FAKE, None, None) == SHAPE
+        assert lib.mx_unpack(FAKE, FAKE, ((1 << 29) - 32) // nb, K, FAKE, 1, None, None) == SHAPE
