@@ -32,7 +32,9 @@ EXPORTS = ("tq_pack", "tq_unpack", "tq_matmul", "tq_matmul_hot", "rb_table", "rb
            "rb_matmul7", "rb_matmul_ws", "rb_prefill_workspace_bytes", "tq_matmul_ws",
            "tq_prefill_workspace_bytes", "rb_matmul_noalloc", "mx_pack", "mx_unpack", "mx_matmul",
            "mx_matmul_mx", "mx_matmul_experts", "moe_route", "moe_route_workspace_bytes",
-           "moe_balance", "moe_balance_workspace_bytes", "moe_balance_grad", "tq_status_string")
+           "moe_balance", "moe_balance_workspace_bytes", "moe_balance_grad", "f8_pack", "f8_unpack",
+           "f8_norm_pack", "f8_matmul", "f8_matmul_experts", "moe_gate", "moe_gate_grad", "moe_combine",
+           "moe_combine_grad", "tq_status_string")
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(
@@ -79,6 +81,18 @@ _lib.moe_route_workspace_bytes.argtypes = [_i64, _i32, _i32]
 _lib.moe_balance.argtypes = [_p, _i32, _i64, _i32, _i64, _p, _p, _p, _p, _p, _i64, _p]
 _lib.moe_balance_workspace_bytes.argtypes = [_i64, _i32]
 _lib.moe_balance_grad.argtypes = [_p, _i32, _i64, _i32, _i64, _p, _p, _p, _p, _p]
+_f64 = ctypes.c_double
+_lib.f8_pack.argtypes = [_p, _i32, _i64, _i64, _i64, _i32, _p, _p, _p, _p]
+_lib.f8_unpack.argtypes = [_p, _p, _i64, _i64, _i32, _p, _i32, _p, _p]
+_lib.f8_norm_pack.argtypes = [_p, _i32, _i64, _i64, _i64, _p, _i64, _p, _i32, _f64, _p, _i64, _p, _i64, _p, _p, _p,
+                              _p]
+_lib.f8_matmul.argtypes = [_p, _p, _i64, _i64, _p, _p, _i64, _p, _p, _i32, _p]
+_lib.f8_matmul_experts.argtypes = [_p, _p, _i64, _i64, _p, _p, _i64, _i32, _p, _p, _p, _i32, _p, _i32, _p]
+_lib.moe_gate.argtypes = [_p, _i32, _i64, _i32, _i64, _p, _p, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.c_float, _p,
+                          _p, _p]
+_lib.moe_gate_grad.argtypes = [_p, _i32, _i64, _i32, _i64, _p, _p, _i32, _i32, _i32, ctypes.c_float, _p, _p]
+_lib.moe_combine.argtypes = [_p, _i32, _i64, _i32, _i64, _p, _p, _i32, _p, _p, _i32, _p]
+_lib.moe_combine_grad.argtypes = [_p, _i32, _i64, _i32, _i64, _p, _p, _i32, _p, _i32, _p, _p, _p]
 _lib.tq_status_string.argtypes = [_i32]
 _lib.tq_status_string.restype = ctypes.c_char_p
 for _name in EXPORTS[:-1]:
@@ -125,6 +139,7 @@ _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
 _MASK = (torch.uint8, torch.bool)
+_F8 = (torch.float8_e4m3fn, torch.uint8)
 
 
 def packed_shape(rows, K, G):
@@ -486,6 +501,11 @@ def _checked(t, name, dtypes, numel, device):
     return t.data_ptr()
 
 
+def _rows_or_none(t, name, dtypes, rows, cols, device):
+    """Address and row distance of an optional matrix."""
+    return (None, 0) if t is None else (t.data_ptr(), _rows(t, name, dtypes, rows, cols, device))
+
+
 def _maybe(t, name, dtypes, numel, device):
     return None if t is None else _checked(t, name, dtypes, numel, device)
 
@@ -638,6 +658,155 @@ def moe_balance_grad(logits, weights, dloss, dlogits, token_mask=None):
     _call("moe_balance_grad", _lib.moe_balance_grad, dev, logits.data_ptr(), ldt, M, E, ldl,
           _maybe(token_mask, "token_mask", _MASK, M, dev), _checked(weights, "weights", _F32, E, dev),
           _checked(dloss, "dloss", _F32, 1, dev), _checked(dlogits, "dlogits", (logits.dtype,), M * E, dev))
+
+
+def f8_shape(rows, K, block_rows=1):
+    """(codes shape, scales shape) of the e4m3 package of a [rows, K] matrix."""
+    nb = -(-K // 128)
+    return (rows, nb, 128), (-(-rows // block_rows), nb)
+
+
+def f8_pack(W, codes, scales, block_rows=1, status=None):
+    """Quantize W [rows, K] (float32 or bfloat16, rows may lie apart) to e4m3 in
+    caller-allocated codes (float8_e4m3fn or uint8) and scales (float32;
+    f8_shape): a scale for 128 columns of block_rows rows, 1 for activations and
+    128 for weights.  With status (int32 [1]) data errors are reported there; a
+    block with a non-finite value becomes NaN either way."""
+    dev = W.device
+    wdt = _float_dtype(W, "W")
+    rows, K = W.shape
+    ldw = _rows(W, "W", (W.dtype,), rows, K, dev)
+    nb = -(-K // 128)
+    _call("f8_pack", _lib.f8_pack, dev, W.data_ptr(), wdt, rows, K, ldw, block_rows,
+          _checked(codes, "codes", _F8, rows * nb * 128, dev),
+          _checked(scales, "scales", _F32, -(-rows // max(block_rows, 1)) * nb, dev),
+          _maybe(status, "status", _I32, 1, dev))
+    return status
+
+
+def f8_unpack(codes, scales, rows, K, W_out, block_rows=1, status=None):
+    """Decode an e4m3 package into W_out [rows, K] (float32 or bfloat16).  With
+    status (int32 [1]) data errors are reported there."""
+    dev = codes.device
+    nb = -(-K // 128)
+    odt = _float_dtype(W_out, "W_out")
+    _call("f8_unpack", _lib.f8_unpack, dev, _checked(codes, "codes", _F8, rows * nb * 128, dev),
+          _checked(scales, "scales", _F32, -(-rows // max(block_rows, 1)) * nb, dev), rows, K, block_rows,
+          _checked(W_out, "W_out", (W_out.dtype,), rows * K, dev), odt, _maybe(status, "status", _I32, 1, dev))
+    return status
+
+
+def f8_norm_pack(x, weight, codes, scales, eps, residual=None, h_out=None, y_out=None, status=None):
+    """h = x (+ residual), y = rms norm of h times weight, and y's e4m3 package
+    (block_rows 1).  x [M, K] float32 or bfloat16, residual, h_out (the sum; may
+    be x or residual) and y_out (y) like it, rows may lie apart; weight [K]
+    float32 or bfloat16."""
+    dev = x.device
+    xdt = _float_dtype(x, "x")
+    M, K = x.shape
+    nb = -(-K // 128)
+    like = (x.dtype,)
+    _call("f8_norm_pack", _lib.f8_norm_pack, dev, x.data_ptr(), xdt, M, K, _rows(x, "x", like, M, K, dev),
+          *_rows_or_none(residual, "residual", like, M, K, dev),
+          _checked(weight, "weight", (weight.dtype,), K, dev), _float_dtype(weight, "weight"), float(eps),
+          *_rows_or_none(h_out, "h_out", like, M, K, dev), *_rows_or_none(y_out, "y_out", like, M, K, dev),
+          _checked(codes, "codes", _F8, M * nb * 128, dev), _checked(scales, "scales", _F32, M * nb, dev),
+          _maybe(status, "status", _I32, 1, dev))
+    return status
+
+
+def f8_matmul(x_codes, x_scales, M, K, codes, scales, N, y, bias=None):
+    """y = x_hat W_hat^T (+ bias) for e4m3 packages of the [M, K] activations
+    (block_rows 1) and the [N, K] weights (block_rows 128)."""
+    dev = x_codes.device
+    nb = -(-K // 128)
+    _call("f8_matmul", _lib.f8_matmul, dev, _checked(x_codes, "x_codes", _F8, M * nb * 128, dev),
+          _checked(x_scales, "x_scales", _F32, M * nb, dev), M, K,
+          _checked(codes, "codes", _F8, N * nb * 128, dev),
+          _checked(scales, "scales", _F32, -(-N // 128) * nb, dev), N, _maybe(bias, "bias", _F32, N, dev),
+          _checked(y, "y", (y.dtype,), M * N, dev), _ydtype(y))
+
+
+def f8_matmul_experts(x_codes, x_scales, M, K, codes, scales, N, y, n_experts, offsets, order, top_k, bias=None):
+    """Grouped f8_matmul: y[t, j] = x_hat[t] W_hat_e^T (+ bias[e]) for the expert
+    e of slot (t, j), with offsets and order from moe_route."""
+    dev = x_codes.device
+    nb = -(-K // 128)
+    _call("f8_matmul_experts", _lib.f8_matmul_experts, dev,
+          _checked(x_codes, "x_codes", _F8, M * nb * 128, dev), _checked(x_scales, "x_scales", _F32, M * nb, dev),
+          M, K, _checked(codes, "codes", _F8, n_experts * N * nb * 128, dev),
+          _checked(scales, "scales", _F32, n_experts * -(-N // 128) * nb, dev), N, n_experts,
+          _maybe(bias, "bias", _F32, n_experts * N, dev),
+          _checked(offsets, "offsets", _I32, n_experts + 1, dev), _checked(order, "order", _I32, M * top_k, dev),
+          top_k, _checked(y, "y", (y.dtype,), M * top_k * N, dev), _ydtype(y))
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _score(score):
+    if score not in _SCORES:
+        raise ValueError(f"score {score!r} must be one of {tuple(_SCORES)}")
+    return _SCORES[score]
+
+
+def moe_gate(logits, expert_ids, weights, score="softmax", bias=None, n_groups=1, top_groups=1, group_top=1,
+             renorm=True, scale=1.0, token_mask=None):
+    """Choose experts by the logits [M, n_experts] (float32 or bfloat16, rows may
+    lie apart): expert_ids int32 [M, top_k] and weights float32 [M, top_k].
+    score "softmax" or "sigmoid"; bias (float32 [n_experts]) shifts the choice
+    only; of n_groups groups the top_groups with the largest sums of group_top
+    scores take part; renorm divides the weights by their sum, scale multiplies
+    them.  token_mask uint8 or bool [M]: tokens of 0 go nowhere (ids -1)."""
+    dev = logits.device
+    ldt = _float_dtype(logits, "logits")
+    M, E = logits.shape
+    top_k = expert_ids.shape[-1]
+    ldl = _rows(logits, "logits", (logits.dtype,), M, E, dev)
+    _call("moe_gate", _lib.moe_gate, dev, logits.data_ptr(), ldt, M, E, ldl,
+          _maybe(token_mask, "token_mask", _MASK, M, dev), _maybe(bias, "bias", _F32, E, dev), _score(score),
+          n_groups, top_groups, group_top, top_k, bool(renorm), scale,
+          _checked(expert_ids, "expert_ids", _I32, M * top_k, dev),
+          _checked(weights, "weights", _F32, M * top_k, dev))
+
+
+def moe_gate_grad(logits, expert_ids, dweights, dlogits, score="softmax", renorm=True, scale=1.0):
+    """Gradient of moe_gate's weights, given dweights float32 [M, top_k], with
+    respect to the logits, into dlogits (the logits' shape and dtype)."""
+    dev = logits.device
+    ldt = _float_dtype(logits, "logits")
+    M, E = logits.shape
+    top_k = expert_ids.shape[-1]
+    ldl = _rows(logits, "logits", (logits.dtype,), M, E, dev)
+    _call("moe_gate_grad", _lib.moe_gate_grad, dev, logits.data_ptr(), ldt, M, E, ldl,
+          _checked(expert_ids, "expert_ids", _I32, M * top_k, dev),
+          _checked(dweights, "dweights", _F32, M * top_k, dev), _score(score), top_k, bool(renorm), scale,
+          _checked(dlogits, "dlogits", (logits.dtype,), M * E, dev))
+
+
+def moe_combine(y, expert_ids, weights, n_experts, out, add=None):
+    """out[t] = sum_j weights[t, j] y[t, j] (+ add[t]) over the slots whose id is
+    an expert; y [M, top_k, N] and out [M, N] float32 or bfloat16, add like out
+    (may be out itself)."""
+    dev = y.device
+    M, top_k, N = y.shape
+    _call("moe_combine", _lib.moe_combine, dev, _checked(y, "y", (y.dtype,), M * top_k * N, dev),
+          _float_dtype(y, "y"), M, top_k, N, _checked(expert_ids, "expert_ids", _I32, M * top_k, dev),
+          _checked(weights, "weights", _F32, M * top_k, dev), n_experts,
+          _maybe(add, "add", (out.dtype,), M * N, dev), _checked(out, "out", (out.dtype,), M * N, dev),
+          _float_dtype(out, "out"))
+
+
+def moe_combine_grad(y, expert_ids, weights, n_experts, dout, dy, dweights):
+    """Gradients of moe_combine given dout [M, N]: dy (y's shape and dtype, may be
+    y itself) and dweights float32 [M, top_k]."""
+    dev = y.device
+    M, top_k, N = y.shape
+    _call("moe_combine_grad", _lib.moe_combine_grad, dev, _checked(y, "y", (y.dtype,), M * top_k * N, dev),
+          _float_dtype(y, "y"), M, top_k, N, _checked(expert_ids, "expert_ids", _I32, M * top_k, dev),
+          _checked(weights, "weights", _F32, M * top_k, dev), n_experts,
+          _checked(dout, "dout", (dout.dtype,), M * N, dev), _float_dtype(dout, "dout"),
+          _checked(dy, "dy", (y.dtype,), M * top_k * N, dev), _checked(dweights, "dweights", _F32, M * top_k, dev))
 
 
 def raw():

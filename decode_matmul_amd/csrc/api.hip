@@ -470,4 +470,153 @@ int moe_balance_grad(const void* logits, int32_t l_dtype, int64_t M, int32_t n_e
                                                     dloss, dlogits, (hipStream_t)stream));
 }
 
+// --------------------------------------------------- e4m3 blocks of 128
+
+int f8_pack(const void* W, int32_t w_dtype, int64_t rows, int64_t K, int64_t ldw, int32_t block_rows,
+            uint8_t* codes, float* scales, int32_t* d_status, void* stream) {
+    if (block_rows != 1 && block_rows != 128) return TQ_ERR_UNSUPPORTED;
+    if (rows < 0 || K < 0 || rows >= kMaxDim || K >= dmm::kMxMaxK || !rows_ok(rows, K, ldw)) return TQ_ERR_SHAPE;
+    if (!is_dtype(w_dtype)) return TQ_ERR_DTYPE;
+    if (rows > 0 && K > 0 && (!W || !codes || !scales)) return TQ_ERR_NULL;
+    if (!aligned(W, bytes_of(w_dtype)) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(d_status, 4))
+        return TQ_ERR_ALIGN;
+    if (!dmm::grid_fits(rows * ((K + 127) / 128) / 16 + 1, 256)) return TQ_ERR_SHAPE;
+    hipStream_t s = (hipStream_t)stream;
+    if (d_status && dmm::launch_status_clear(d_status, s) != hipSuccess) return TQ_ERR_HIP;
+    return grid_status(dmm::launch_f8_pack(W, w_dtype, rows, K, ldw, block_rows, codes, scales, d_status, s));
+}
+
+int f8_unpack(const uint8_t* codes, const float* scales, int64_t rows, int64_t K, int32_t block_rows,
+              void* W_out, int32_t out_dtype, int32_t* d_status, void* stream) {
+    if (block_rows != 1 && block_rows != 128) return TQ_ERR_UNSUPPORTED;
+    if (rows < 0 || K < 0 || rows >= kMaxDim || K >= dmm::kMxMaxK) return TQ_ERR_SHAPE;
+    if (!is_dtype(out_dtype)) return TQ_ERR_DTYPE;
+    if (rows > 0 && K > 0 && (!W_out || !codes || !scales)) return TQ_ERR_NULL;
+    if (!aligned(W_out, bytes_of(out_dtype)) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(d_status, 4))
+        return TQ_ERR_ALIGN;
+    if (!dmm::grid_fits(rows * ((K + 127) / 128) / 16 + 1, 256)) return TQ_ERR_SHAPE;
+    hipStream_t s = (hipStream_t)stream;
+    if (d_status && dmm::launch_status_clear(d_status, s) != hipSuccess) return TQ_ERR_HIP;
+    return grid_status(dmm::launch_f8_unpack(codes, scales, rows, K, block_rows, W_out, out_dtype, d_status, s));
+}
+
+int f8_norm_pack(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx, const void* residual,
+                 int64_t ldr, const void* weight, int32_t w_dtype, double eps, void* h_out, int64_t ldh,
+                 void* y_out, int64_t ldy, uint8_t* codes, float* scales, int32_t* d_status, void* stream) {
+    if (M < 0 || K < 0 || M >= kMaxDim || K >= dmm::kMxMaxK || !rows_ok(M, K, ldx) || !(eps >= 0.0) ||
+        (residual && !rows_ok(M, K, ldr)) || (h_out && !rows_ok(M, K, ldh)) || (y_out && !rows_ok(M, K, ldy)))
+        return TQ_ERR_SHAPE;
+    if (!is_dtype(x_dtype) || !is_dtype(w_dtype)) return TQ_ERR_DTYPE;
+    if (M > 0 && K > 0 && (!x || !weight || !codes || !scales)) return TQ_ERR_NULL;
+    const uintptr_t xb = bytes_of(x_dtype);
+    if (!aligned(x, xb) || !aligned(residual, xb) || !aligned(h_out, xb) || !aligned(y_out, xb) ||
+        !aligned(weight, bytes_of(w_dtype)) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(d_status, 4))
+        return TQ_ERR_ALIGN;
+    if (!dmm::grid_fits(M, 512)) return TQ_ERR_SHAPE;
+    hipStream_t s = (hipStream_t)stream;
+    if (d_status && dmm::launch_status_clear(d_status, s) != hipSuccess) return TQ_ERR_HIP;
+    const dmm::F8NormArgs a = {x,   x_dtype, M,   K,     ldx, residual, ldr,    weight, w_dtype,
+                               eps, h_out,   ldh, y_out, ldy, codes,    scales, d_status};
+    return grid_status(dmm::launch_f8_norm_pack(a, s));
+}
+
+static int f8_matmul_common(const dmm::F8MatmulArgs& a, void* stream) {
+    if (a.M < 0 || a.K < 0 || a.N < 0 || a.M >= kMaxDim || a.K >= dmm::kF8MaxK || a.N >= kMaxDim) return TQ_ERR_SHAPE;
+    if (!is_dtype(a.y_dtype)) return TQ_ERR_DTYPE;
+    if (a.M == 0 || a.N == 0) return TQ_OK;
+    if (!a.y || (a.K > 0 && (!a.x_codes || !a.x_scales || !a.codes || !a.scales))) return TQ_ERR_NULL;
+    if (!aligned(a.x_codes, 16) || !aligned(a.codes, 16) || !aligned(a.x_scales, 4) || !aligned(a.scales, 4) ||
+        !aligned(a.bias, 4) || !aligned(a.y, bytes_of(a.y_dtype)))
+        return TQ_ERR_ALIGN;
+    return grid_status(dmm::launch_f8_matmul(a, (hipStream_t)stream));
+}
+
+int f8_matmul(const uint8_t* x_codes, const float* x_scales, int64_t M, int64_t K, const uint8_t* codes,
+              const float* scales, int64_t N, const float* bias, void* y, int32_t y_dtype, void* stream) {
+    const dmm::F8MatmulArgs a = {x_codes, x_scales, M, K,       N,       codes, scales,
+                                 bias,    0,        nullptr, nullptr, 1,     y,      y_dtype};
+    return f8_matmul_common(a, stream);
+}
+
+int f8_matmul_experts(const uint8_t* x_codes, const float* x_scales, int64_t M, int64_t K, const uint8_t* codes,
+                      const float* scales, int64_t N, int32_t n_experts, const float* bias, const int32_t* offsets,
+                      const int32_t* order, int32_t top_k, void* y, int32_t y_dtype, void* stream) {
+    if (n_experts < 1 || top_k < 1) return TQ_ERR_SHAPE;
+    if (M >= 0 && M < kMaxDim && M * top_k >= kMaxDim) return TQ_ERR_SHAPE;
+    if (M > 0 && N > 0 && (!offsets || !order)) return TQ_ERR_NULL;
+    if (!aligned(offsets, 4) || !aligned(order, 4)) return TQ_ERR_ALIGN;
+    const dmm::F8MatmulArgs a = {x_codes, x_scales,  M,       K,     N,     codes, scales,
+                                 bias,    n_experts, offsets, order, top_k, y,     y_dtype};
+    return f8_matmul_common(a, stream);
+}
+
+// ------------------------------------------- the experts' choice and combination
+
+int moe_gate(const void* logits, int32_t l_dtype, int64_t M, int32_t n_experts, int64_t ldl,
+             const uint8_t* token_mask, const float* bias, int32_t score, int32_t n_groups, int32_t top_groups,
+             int32_t group_top, int32_t top_k, int32_t renorm, float scale, int32_t* expert_ids, float* weights,
+             void* stream) {
+    if (n_experts > dmm::kMoeMaxExperts || top_k > dmm::kGateMaxTopK || n_groups > 64) return TQ_ERR_UNSUPPORTED;
+    if ((score != DMM_SOFTMAX && score != DMM_SIGMOID) || (group_top != 1 && group_top != 2)) return TQ_ERR_UNSUPPORTED;
+    if (M < 0 || M >= kMaxDim || n_experts < 1 || !rows_ok(M, n_experts, ldl) || n_groups < 1 ||
+        n_experts % n_groups != 0 || top_groups < 1 || top_groups > n_groups || top_k < 1 ||
+        top_k > top_groups * (n_experts / n_groups))
+        return TQ_ERR_SHAPE;
+    if (!is_dtype(l_dtype)) return TQ_ERR_DTYPE;
+    if (M == 0) return TQ_OK;
+    if (!logits || !expert_ids || !weights) return TQ_ERR_NULL;
+    if (!aligned(logits, bytes_of(l_dtype)) || !aligned(bias, 4) || !aligned(expert_ids, 4) || !aligned(weights, 4))
+        return TQ_ERR_ALIGN;
+    const dmm::GateArgs a = {logits,     l_dtype,   M,     n_experts,   ldl,   token_mask, bias,   score, n_groups,
+                             top_groups, group_top, top_k, renorm != 0, scale, expert_ids, weights};
+    return grid_status(dmm::launch_moe_gate(a, (hipStream_t)stream));
+}
+
+int moe_gate_grad(const void* logits, int32_t l_dtype, int64_t M, int32_t n_experts, int64_t ldl,
+                  const int32_t* expert_ids, const float* dweights, int32_t score, int32_t top_k, int32_t renorm,
+                  float scale, void* dlogits, void* stream) {
+    if (n_experts > dmm::kMoeMaxExperts || top_k > dmm::kGateMaxTopK) return TQ_ERR_UNSUPPORTED;
+    if (score != DMM_SOFTMAX && score != DMM_SIGMOID) return TQ_ERR_UNSUPPORTED;
+    if (M < 0 || M >= kMaxDim || n_experts < 1 || !rows_ok(M, n_experts, ldl) || top_k < 1) return TQ_ERR_SHAPE;
+    if (!is_dtype(l_dtype)) return TQ_ERR_DTYPE;
+    if (M == 0) return TQ_OK;
+    if (!logits || !expert_ids || !dweights || !dlogits) return TQ_ERR_NULL;
+    if (!aligned(logits, bytes_of(l_dtype)) || !aligned(expert_ids, 4) || !aligned(dweights, 4) ||
+        !aligned(dlogits, bytes_of(l_dtype)))
+        return TQ_ERR_ALIGN;
+    const dmm::GateGradArgs a = {logits, l_dtype, M,     n_experts,   ldl,   expert_ids, dweights,
+                                 top_k,  score,   renorm != 0, scale, dlogits};
+    return grid_status(dmm::launch_moe_gate_grad(a, (hipStream_t)stream));
+}
+
+int moe_combine(const void* y, int32_t y_dtype, int64_t M, int32_t top_k, int64_t N, const int32_t* expert_ids,
+                const float* weights, int32_t n_experts, const void* add, void* out, int32_t out_dtype,
+                void* stream) {
+    if (M < 0 || N < 0 || M >= kMaxDim || N >= kMaxDim || top_k < 1 || M * top_k >= kMaxDim || n_experts < 1)
+        return TQ_ERR_SHAPE;
+    if (!is_dtype(y_dtype) || !is_dtype(out_dtype)) return TQ_ERR_DTYPE;
+    if (M == 0 || N == 0) return TQ_OK;
+    if (!y || !expert_ids || !weights || !out) return TQ_ERR_NULL;
+    if (!aligned(y, bytes_of(y_dtype)) || !aligned(add, bytes_of(out_dtype)) || !aligned(out, bytes_of(out_dtype)) ||
+        !aligned(expert_ids, 4) || !aligned(weights, 4))
+        return TQ_ERR_ALIGN;
+    const dmm::CombineArgs a = {y, y_dtype, M, top_k, N, expert_ids, weights, n_experts, add, out, out_dtype};
+    return grid_status(dmm::launch_moe_combine(a, (hipStream_t)stream));
+}
+
+int moe_combine_grad(const void* y, int32_t y_dtype, int64_t M, int32_t top_k, int64_t N, const int32_t* expert_ids,
+                     const float* weights, int32_t n_experts, const void* dout, int32_t dout_dtype, void* dy,
+                     float* dweights, void* stream) {
+    if (M < 0 || N < 0 || M >= kMaxDim || N >= kMaxDim || top_k < 1 || M * top_k >= kMaxDim || n_experts < 1)
+        return TQ_ERR_SHAPE;
+    if (!is_dtype(y_dtype) || !is_dtype(dout_dtype)) return TQ_ERR_DTYPE;
+    if (M == 0) return TQ_OK;
+    if (!expert_ids || !weights || !dweights || (N > 0 && (!y || !dout || !dy))) return TQ_ERR_NULL;
+    if (!aligned(y, bytes_of(y_dtype)) || !aligned(dy, bytes_of(y_dtype)) || !aligned(dout, bytes_of(dout_dtype)) ||
+        !aligned(expert_ids, 4) || !aligned(weights, 4) || !aligned(dweights, 4))
+        return TQ_ERR_ALIGN;
+    const dmm::CombineGradArgs a = {y, y_dtype, M, top_k, N, expert_ids, weights, n_experts, dout, dout_dtype, dy, dweights};
+    return grid_status(dmm::launch_moe_combine_grad(a, (hipStream_t)stream));
+}
+
 }  // extern "C"

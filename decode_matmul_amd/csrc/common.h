@@ -315,4 +315,110 @@ hipError_t launch_moe_balance_grad(const void* logits, int l_dtype, int64_t M, i
                                    const uint8_t* mask, const float* weights, const float* dloss, void* dlogits,
                                    hipStream_t s);
 
+// ------------------------------------------------------------ e4m3 blocks, the experts' choice and combination
+
+hipError_t launch_f8_pack(const void* W, int w_dtype, int64_t rows, int64_t K, int64_t ldw, int block_rows,
+                          uint8_t* codes, float* scales, int32_t* status, hipStream_t s);
+hipError_t launch_f8_unpack(const uint8_t* codes, const float* scales, int64_t rows, int64_t K, int block_rows,
+                            void* out, int out_dtype, int32_t* status, hipStream_t s);
+
+struct F8NormArgs {
+    const void* x;            // [M, K], rows ldx apart
+    int x_dtype;              // also of residual, h and y
+    int64_t M, K, ldx;
+    const void* residual;     // NULL, or [M, K], rows ldr apart
+    int64_t ldr;
+    const void* weight;       // [K]
+    int w_dtype;
+    double eps;
+    void* h;                  // NULL, or x + residual, rows ldh apart
+    int64_t ldh;
+    void* y;                  // NULL, or the normed rows, ldy apart
+    int64_t ldy;
+    uint8_t* codes;
+    float* scales;
+    int32_t* status;
+};
+hipError_t launch_f8_norm_pack(const F8NormArgs& a, hipStream_t s);
+
+// Most columns of a product: 256 rows of a tile lie within 32-bit offsets of its first.
+constexpr int64_t kF8MaxK = (int64_t)1 << 23;
+struct F8MatmulArgs {
+    const uint8_t* x_codes;   // [M][nb][128]
+    const float* x_scales;    // [M][nb]
+    int64_t M, K, N;
+    const uint8_t* codes;     // [N][nb][128], or n_experts of them back to back
+    const float* scales;      // [ceil(N / 128)][nb] each
+    const float* bias;        // NULL, [N] or [n_experts][N]
+    int n_experts;            // 0: dense
+    const int32_t* offsets;   // grouped: [n_experts + 1] into order
+    const int32_t* order;     // grouped: [M * top_k] slots
+    int top_k;                // 1 when dense
+    void* y;                  // [M, N] or [M, top_k, N]
+    int y_dtype;
+};
+hipError_t launch_f8_matmul(const F8MatmulArgs& a, hipStream_t s);
+
+// Most choices of a token.
+constexpr int kGateMaxTopK = 32;
+struct GateArgs {
+    const void* logits;
+    int l_dtype;
+    int64_t M;
+    int E;
+    int64_t ldl;
+    const uint8_t* mask;
+    const float* bias;
+    int score, n_groups, top_groups, group_top, top_k;
+    bool renorm;
+    float scale;
+    int32_t* ids;
+    float* weights;
+};
+hipError_t launch_moe_gate(const GateArgs& a, hipStream_t s);
+struct GateGradArgs {
+    const void* logits;
+    int l_dtype;
+    int64_t M;
+    int E;
+    int64_t ldl;
+    const int32_t* ids;
+    const float* dweights;
+    int top_k, score;
+    bool renorm;
+    float scale;
+    void* dlogits;
+};
+hipError_t launch_moe_gate_grad(const GateGradArgs& a, hipStream_t s);
+
+struct CombineArgs {
+    const void* y;            // [M, top_k, N]
+    int y_dtype;
+    int64_t M;
+    int top_k;
+    int64_t N;
+    const int32_t* ids;
+    const float* weights;
+    int n_experts;
+    const void* add;          // NULL or [M, N] of o_dtype
+    void* out;                // [M, N]
+    int o_dtype;
+};
+hipError_t launch_moe_combine(const CombineArgs& a, hipStream_t s);
+struct CombineGradArgs {
+    const void* y;
+    int y_dtype;              // also of dy
+    int64_t M;
+    int top_k;
+    int64_t N;
+    const int32_t* ids;
+    const float* weights;
+    int n_experts;
+    const void* dout;
+    int o_dtype;
+    void* dy;
+    float* dweights;
+};
+hipError_t launch_moe_combine_grad(const CombineGradArgs& a, hipStream_t s);
+
 }  // namespace dmm

@@ -2,7 +2,7 @@
 // slots of each expert) and moe_balance / moe_balance_grad.
 #include <type_traits>
 
-#include "mx.h"
+#include "lanes.h"
 
 namespace dmm {
 
@@ -207,42 +207,6 @@ __global__ void __launch_bounds__(kScanThreads) route_scan_kernel(int32_t* cc, i
 constexpr int kBalThreads = 256;
 constexpr int kBalWaves = kBalThreads / 64;
 
-// A value of another lane of 16, by the data-parallel moves: 0xb1 and 0x4e are
-// lanes ^ 1 and ^ 2; 0x141 and 0x140 mirror 8 and 16 lanes, which brings the other
-// half's value once all lanes of a half have the same.
-template <int CTRL>
-__device__ __forceinline__ float moved(float v) {
-    return __builtin_bit_cast(
-        float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
-}
-
-template <int L, class F>
-__device__ __forceinline__ float over_group(float v, F f) {
-    if (L >= 2) v = f(v, moved<0xb1>(v));
-    if (L >= 4) v = f(v, moved<0x4e>(v));
-    if (L >= 8) v = f(v, moved<0x141>(v));
-    if (L >= 16) v = f(v, moved<0x140>(v));
-    if (L >= 32) v = f(v, __shfl_xor(v, 16));
-    if (L >= 64) v = f(v, __shfl_xor(v, 32));
-    return v;
-}
-
-template <int L>
-__device__ __forceinline__ float group_max(float v) {
-    return over_group<L>(v, [](float a, float b) { return __builtin_elementwise_maximum(a, b); });
-}
-
-template <int L>
-__device__ __forceinline__ float group_sum(float v) {
-    return over_group<L>(v, [](float a, float b) { return a + b; });
-}
-
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
-    return v;
-}
-
 // Eight weights or counts (within 2^-24) from w[0] on, `have` of them there; the others are 0.
 template <class T>
 __device__ __forceinline__ void load_weights(const T* w, int have, float* v) {
@@ -259,35 +223,6 @@ __device__ __forceinline__ void load_weights(const T* w, int have, float* v) {
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = i < have ? (float)w[i] : 0.f;
-}
-
-// Eight logits at p, `have` of them there; the others are -inf.
-template <bool BF16>
-__device__ __forceinline__ void load_logits(const void* base, int64_t at, int have, float* z) {
-    if (have >= 8) {
-        if (BF16) {
-            const u32x4 d = *(const u32x4h*)((const uint16_t*)base + at);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                z[2 * i] = __builtin_bit_cast(float, d[i] << 16);
-                z[2 * i + 1] = __builtin_bit_cast(float, d[i] & 0xffff0000u);
-            }
-        } else {
-            const f32x4 a = *(const f32x4a*)((const float*)base + at), b = *(const f32x4a*)((const float*)base + at + 4);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                z[i] = a[i];
-                z[4 + i] = b[i];
-            }
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        z[i] = -__builtin_inff();
-        if (i < have)
-            z[i] = BF16 ? bf16_bits_to_f32(((const uint16_t*)base)[at + i]) : ((const float*)base)[at + i];
-    }
 }
 
 // A row's logits to e = exp(z - top), 1 / sum e and sum w p.  False for a row of
@@ -342,7 +277,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_loss_kernel(const void* l
     for (int i = 0; i < kTokens; ++i) {
         const int64_t t = t0 + i * (kBalThreads / L);
         live[i] = t < M;
-        load_logits<BF16>(logits, live[i] ? t * ldl + e0 : 0, live[i] ? have : 0, z[i]);
+        load_row8<BF16>(logits, live[i] ? t * ldl + e0 : 0, live[i] ? have : 0, z[i], -__builtin_inff());
         if (mask && live[i]) live[i] = mask[t] != 0;
     }
     load_weights(counts + e0, have, w);
@@ -414,7 +349,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const void* l
     const int e0 = (lane % L) * 8, have = E - e0;
     if (t >= M) return;
     float w[8], p[8];
-    load_logits<BF16>(logits, t * ldl + e0, have, p);
+    load_row8<BF16>(logits, t * ldl + e0, have, p, -__builtin_inff());
     load_weights(weights + e0, have, w);
     const bool live = !mask || mask[t] != 0;
     float inv, s;
@@ -435,40 +370,11 @@ __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const void* l
 #pragma unroll
         for (int i = 0; i < 8; ++i) p[i] = 0.f;
     }
-    const int64_t at = t * E + e0;
-    if (BF16) {
-        uint16_t* const d = (uint16_t*)dlogits + at;
-        if (have >= 8) {
-            u32x4 v;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = bf16_pair(p[2 * i], p[2 * i + 1]);
-            *(u32x4h*)d = v;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < have) d[i] = f32_to_bf16_rne(p[i]);
-        }
-    } else {
-        float* const d = (float*)dlogits + at;
-        if (have >= 8) {
-            *(f32x4a*)d = (f32x4){p[0], p[1], p[2], p[3]};
-            *(f32x4a*)(d + 4) = (f32x4){p[4], p[5], p[6], p[7]};
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < have) d[i] = p[i];
-        }
-    }
+    store_row8<BF16>(dlogits, t * E + e0, have, p);
 }
 
 int64_t route_chunks(int64_t slots) { return (slots + kChunk - 1) / kChunk; }
 
-// Lanes of a row of E logits, eight each.
-int row_lanes(int E) {
-    int L = 1;
-    while (8 * L < E) L *= 2;
-    return L;
-}
 static_assert(kMoeMaxExperts <= 64 * 8, "a row fits a wave");
 
 int64_t loss_blocks(int64_t M, int E) {

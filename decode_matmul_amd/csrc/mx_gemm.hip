@@ -26,7 +26,7 @@
 // 8 bytes costs as much as one for a line).
 #include <type_traits>
 
-#include "mx.h"
+#include "experts.h"
 
 namespace dmm {
 
@@ -42,113 +42,6 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 template <int LANES>
 __device__ __forceinline__ int w_slot(int row) {
     return LANES == 8 ? swizzle(row) : ((row >> 2) ^ (row >> 3)) & 3;
-}
-
-// The workgroup's tile: its tokens are positions [m0, m_end) of the batch or
-// of the order list, its rows of W start at n0.
-struct Place {
-    int64_t m0, m_end, n0, expert;
-};
-
-// Tile b of the experts' tiles: experts in turn, an expert's tiles of BM
-// positions in turn, the tiles along N innermost; each XCD gets a contiguous
-// share of the tiles that there are.  False when there are fewer: then m0 is the
-// workgroup's number among the m_end that have none.
-template <int BM, int BN, int kThreads>
-__device__ bool place_grouped(const MxMatmulArgs& a, Place& p) {
-    __shared__ int found[3];
-    __shared__ int sums[kThreads / 64];
-    const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int slots = (int)(a.M * a.top_k);
-    const int ntiles = (int)((a.N + BN - 1) / BN);
-    // bounds of the list of expert e, kept in range whatever the offsets hold
-    auto bound = [&](int e) {
-        const int o = a.offsets[e];
-        return o < 0 ? 0 : (o > slots ? slots : o);
-    };
-    if (tid == 0) found[2] = -1;
-    int total = 0;
-    for (int e0 = 0; e0 < a.n_experts; e0 += kThreads) {
-        const int e = e0 + tid;
-        int t = 0;
-        if (e < a.n_experts) {
-            const int c = bound(e + 1) - bound(e);
-            t = c > 0 ? (c + BM - 1) / BM : 0;
-        }
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) t += __shfl_xor(t, d);
-        if (lane == 0) sums[wave] = t;
-        __syncthreads();
-        for (int w = 0; w < kThreads / 64; ++w) total += sums[w];
-        __syncthreads();
-    }
-    total = readfirstlane(total);
-    const int64_t all = (int64_t)total * ntiles;
-    const int64_t b = blockIdx.x;
-    // XCD b % 8 takes tiles all * (b % 8) / 8 .. all * (b % 8 + 1) / 8 - 1
-    const int64_t x = b % 8, lo = all * x / 8, hi = all * (x + 1) / 8;
-    const int64_t t = lo + b / 8;
-    if (t >= hi) {
-        const int64_t cap = gridDim.x / 8;      // of an XCD
-        p.m0 = cap * x - lo + t - hi;
-        p.m_end = cap * 8 - all;
-        return false;
-    }
-    const int want = readfirstlane((int)(t / ntiles));
-    p.n0 = (t - (int64_t)want * ntiles) * BN;
-    int before = 0;
-    for (int e0 = 0; e0 < a.n_experts; e0 += kThreads) {
-        const int e = e0 + tid;
-        int n = 0, first = 0, last = 0;
-        if (e < a.n_experts) {
-            first = bound(e);
-            last = bound(e + 1);
-            n = last > first ? (last - first + BM - 1) / BM : 0;
-        }
-        int inc = n;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(inc, d);
-            if (lane >= d) inc += o;
-        }
-        if (lane == 63) sums[wave] = inc;
-        __syncthreads();
-        int base = before;
-        for (int w = 0; w < kThreads / 64; ++w) {
-            if (w < wave) base += sums[w];
-            before += sums[w];
-        }
-        const int mine = base + inc - n;
-        if (want >= mine && want < mine + n) {
-            found[0] = first + (want - mine) * BM;
-            found[1] = last;
-            found[2] = e;
-        }
-        __syncthreads();
-    }
-    if (readfirstlane(found[2]) < 0) {          // overlapping lists can have more tiles than an int counts
-        p.m0 = p.m_end = a.M * a.top_k;
-        return false;
-    }
-    p.m0 = readfirstlane(found[0]);
-    const int64_t last = readfirstlane(found[1]);
-    p.m_end = last < p.m0 + BM ? last : p.m0 + BM;
-    p.expert = readfirstlane(found[2]);
-    return true;
-}
-
-// Rows of slots of no expert: NaN.  A workgroup without a tile takes every step-th
-// from number `first` on; there are at least as many of them as those slots make tiles.
-__device__ void write_nan_rows(const MxMatmulArgs& a, int64_t first, int64_t step, int threads) {
-    const int64_t slots = a.M * a.top_k, begin = a.offsets[a.n_experts];
-    for (int64_t i = (begin < 0 ? 0 : begin) + first; i < slots; i += step) {
-        const int64_t slot = a.order[i];
-        if (slot < 0 || slot >= slots) continue;
-        for (int64_t n = threadIdx.x; n < a.N; n += threads) {
-            if (a.y_dtype == TQ_F32) ((float*)a.y)[slot * a.N + n] = __builtin_nanf("");
-            else ((uint16_t*)a.y)[slot * a.N + n] = 0x7fc0u;
-        }
-    }
 }
 
 // MXX: activations in MXFP4.  DIRECT: whole slabs of bf16 activations (MXX: of
@@ -192,15 +85,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) mx_gemm_kernel(MxMatmulA
             return;
         }
     } else {
-        // groups of 8 tiles along M share the rows of W; each XCD takes a contiguous range
-        const int64_t mt = (a.M + BM - 1) / BM, nt = (a.N + BN - 1) / BN;
-        const int64_t t = xcd_block(blockIdx.x, mt * nt);
-        const int64_t grp = t / (8 * nt), m8 = grp * 8, gm = mt - m8 < 8 ? mt - m8 : 8;
-        const int64_t in = t - grp * 8 * nt;
-        p.m0 = (m8 + in % gm) * BM;
-        p.n0 = in / gm * BN;
-        p.m_end = p.m0 + BM < a.M ? p.m0 + BM : a.M;
-        p.expert = 0;
+        p = place_dense<BM, BN>(a);
     }
     const int64_t slots = a.M * a.top_k;
 
@@ -622,12 +507,7 @@ hipError_t launch(const MxMatmulArgs& a, hipStream_t s) {
     constexpr int kThreads = 64 * WM * WN * KG;
     const int64_t nt = (a.N + BN - 1) / BN;
     int64_t blocks = (a.M + BM - 1) / BM * nt;
-    if (GROUPED) {
-        // whole shares of the 8 XCDs: the largest share has a tile more than an eighth
-        const int64_t slots = a.M * a.top_k;
-        const int64_t tiles = (slots / BM + (a.n_experts < slots ? a.n_experts : slots)) * nt;
-        blocks = (tiles / 8 + 1) * 8;
-    }
+    if (GROUPED) blocks = grouped_blocks<BM>(a, nt);
     if (!grid_fits(blocks, kThreads)) return hipErrorInvalidConfiguration;
     mx_gemm_kernel<MXX, DIRECT, BM, BN, WM, WN, KD, KG, GROUPED><<<(unsigned)blocks, kThreads, 0, s>>>(a);
     return hipGetLastError();

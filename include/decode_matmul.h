@@ -2,7 +2,7 @@
  * decode_matmul.h -- C ABI of the packed ternary-code matmul library for
  * AMD MI355X (gfx950).
  *
- * Three weight formats, all decoded inside the matmul kernels (no bf16 copy of
+ * Four weight formats, all decoded inside the matmul kernels (no bf16 copy of
  * the weight matrix is ever written):
  *
  *  1. Mean-abs ternary ("Does your weight format deserve a kernel?",
@@ -23,8 +23,13 @@
  *     specification): 32 consecutive weights of a row share a power of two, and
  *     each is one of 16 e2m1 values.  Its entry points are the mx_* ones.
  *
- * The moe_* entry points are the router's side of the grouped experts: counts
- * and lists of the slots routed to each expert, and the balance loss.
+ *  4. e4m3 blocks: one byte a value, an fp32 scale for each 128 columns of a row
+ *     (activations) or of 128 rows (weights).  Its entry points are the f8_* ones.
+ *
+ * The moe_* entry points are the router's side of the grouped experts: which experts
+ * a token goes to and with what weights (and their gradient), counts and lists of the
+ * slots routed to each expert, the balance loss and its gradient, and the weighted
+ * sum of the experts' rows and its gradient.
  *
  * Conventions for every entry point:
  *  - Pointers named d_* or documented "device" are device pointers owned by
@@ -83,6 +88,9 @@ enum tq_data_flag {
 
 /* Element types of outputs. */
 enum tq_dtype { TQ_F32 = 0, TQ_BF16 = 1 };
+
+/* Scores of moe_gate. */
+enum dmm_score { DMM_SOFTMAX = 0, DMM_SIGMOID = 1 };
 
 /*
  * tq_pack -- quantize and pack W (pack-unpack-run, "Three values and a
@@ -645,6 +653,226 @@ int64_t moe_balance_workspace_bytes(int64_t M, int32_t n_experts);
 int moe_balance_grad(const void* logits, int32_t l_dtype, int64_t M, int32_t n_experts, int64_t ldl,
                      const uint8_t* token_mask, const float* weights, const float* dloss,
                      void* dlogits, void* stream);
+
+/*
+ * e4m3 packages.  A value is a scale times an e4m3 code (4 exponent and 3 mantissa
+ * bits, largest 448, no infinities, 0x7f and 0xff NaN).  With nb = ceil(K / 128), a
+ * [rows, K] matrix is planar:
+ *     codes  uint8 [rows][nb][128]               16-byte aligned
+ *     scales fp32  [ceil(rows / block_rows)][nb]
+ * block_rows is 1 (activations: a scale for 128 columns of a row) or 128 (weights: for
+ * 128 x 128).  Where K is a multiple of 128 the codes are those of a plain row-major
+ * e4m3 matrix.  Codes past K are 0 as f8_pack writes them; the products do not read
+ * them as values.  Products take any fp32 scales; f8_pack writes powers of two.
+ */
+
+/*
+ * f8_pack -- quantize W to e4m3.
+ *
+ *  W         device [rows, K] of w_dtype (TQ_F32 or TQ_BF16), row r at element
+ *            r * ldw; aligned to its element.
+ *  ldw       elements between rows, >= K (rows > 1 need it; TQ_ERR_SHAPE).
+ *  block_rows  1 or 128 (TQ_ERR_UNSUPPORTED).
+ *  codes, scales  device outputs (layout above).
+ *  d_status  device int32, or NULL for no report; set to 0, then
+ *            TQ_DATA_RANGE if a value is not finite.
+ *
+ * Per block, with a = max |W_j|: the scale is the least power of two s with a / s <=
+ * 448, at least 2^-126, and each code is the e4m3 value nearest to W_j / s, ties to
+ * the even code, the sign kept.  The scaling is exact, so there is one rounding.  A
+ * block with a value that is not finite gets a NaN scale and codes 0: it decodes to
+ * NaN, and so do the products it takes part in.  K is below 2^23, rows * nb below
+ * 2^28 - 16 (TQ_ERR_SHAPE).
+ */
+int f8_pack(const void* W, int32_t w_dtype, int64_t rows, int64_t K, int64_t ldw, int32_t block_rows,
+            uint8_t* codes, float* scales, int32_t* d_status, void* stream);
+
+/*
+ * f8_unpack -- decode an e4m3 package to W_out [rows, K] of out_dtype, row r at
+ * element r * K: the fp32 product of code and scale (exact where the scale is a power
+ * of two and the result is above 2^-126), rounded to nearest-even for TQ_BF16.
+ *
+ *  d_status  device int32, or NULL for no report; set to 0, then
+ *            TQ_DATA_RANGE if a value is not finite, TQ_DATA_PADDING if a code past
+ *            K is not 0.
+ *
+ * Sizes as in f8_pack.
+ */
+int f8_unpack(const uint8_t* codes, const float* scales, int64_t rows, int64_t K, int32_t block_rows,
+              void* W_out, int32_t out_dtype, int32_t* d_status, void* stream);
+
+/*
+ * f8_norm_pack -- residual addition, root-mean-square norm and packing in one pass:
+ *
+ *     h = x + residual                       rounded to x_dtype
+ *     f = (sum_k h_k^2 / K + eps)^-1/2       float64, then rounded to fp32
+ *     y = (h f) weight                       each product rounded to fp32
+ *
+ * and the e4m3 package of y with block_rows = 1 (f8_pack's rule).
+ *
+ *  x         device [M, K] of x_dtype (TQ_F32 or TQ_BF16), row t at element t * ldx.
+ *  residual  device [M, K] of x_dtype, rows ldr apart, or NULL (h = x).
+ *  weight    device [K] of w_dtype.
+ *  eps       >= 0 (TQ_ERR_SHAPE).
+ *  h_out     device [M, K] of x_dtype, rows ldh apart, or NULL; may be x or
+ *            residual itself (the same address and distance), no other overlap.
+ *  y_out     device [M, K] of x_dtype, rows ldy apart, or NULL: y rounded once.
+ *  codes, scales  device outputs, [M][nb][128] and [M][nb].
+ *  d_status  device int32, or NULL for no report; set to 0, then
+ *            TQ_DATA_RANGE if a y is not finite.
+ *
+ * Matrices are aligned to their element.  M = 0 or K = 0 is a no-op.  K is below 2^23,
+ * M below 2^23 (TQ_ERR_SHAPE).
+ */
+int f8_norm_pack(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx, const void* residual,
+                 int64_t ldr, const void* weight, int32_t w_dtype, double eps, void* h_out, int64_t ldh,
+                 void* y_out, int64_t ldy, uint8_t* codes, float* scales, int32_t* d_status, void* stream);
+
+/*
+ * f8_matmul -- e4m3 activations times an e4m3 weight matrix:
+ *
+ *     y[m, n] = sum_b sx[m, b] sw[n / 128, b] sum_{k in b} cx[m, k] cw[n, k]  (+ bias[n])
+ *
+ *  x_codes, x_scales  device package of the [M, K] activations, block_rows = 1.
+ *  codes, scales      device package of the [N, K] weights, block_rows = 128.
+ *  bias    device fp32 [N] or NULL.
+ *  y       device [M, N] of y_dtype (fp32, or bf16 nearest-even of the fp32 result).
+ *
+ * Products of codes are exact; a block's sum, the product of its two scales and the
+ * sum over blocks are fp32, in an order fixed by the shape (two calls give the same
+ * bits).  The product of two scales has to be one that fp32 holds (2^-126 to 2^128);
+ * one that overflows makes its sums infinite or NaN.  A NaN scale or code makes what
+ * it takes part in NaN.  M = 0 or N = 0 is a no-op; with K = 0 the packages may be
+ * NULL and y = bias (or 0).  M and N are below 2^31, K is below 2^23; sizes that need
+ * more than 2^32 - 1 threads are TQ_ERR_SHAPE.
+ */
+int f8_matmul(const uint8_t* x_codes, const float* x_scales, int64_t M, int64_t K, const uint8_t* codes,
+              const float* scales, int64_t N, const float* bias, void* y, int32_t y_dtype, void* stream);
+
+/*
+ * f8_matmul_experts -- grouped f8_matmul over the lists of moe_route:
+ *
+ *     y[t, j, n] = f8_matmul of x[t] and the weights of e = expert_ids[t, j]
+ *
+ *  x_codes, x_scales  package of M tokens.
+ *  codes, scales  n_experts packages of [N, K] back to back ([n_experts][N][nb][128]
+ *          and [n_experts][ceil(N / 128)][nb]).
+ *  bias    device fp32 [n_experts][N] or NULL.
+ *  offsets, order  from moe_route with the same M, top_k and n_experts.
+ *  y       device [M, top_k, N] of y_dtype; the rows of slots of no expert are NaN.
+ *
+ * Where every slot has its own activations (an expert's second product), pass M *
+ * top_k for M and 1 for top_k with the same lists.  Entries of the lists outside their
+ * range are skipped (nothing is read or written out of bounds; rows that are then
+ * listed nowhere stay as they were).  M * top_k is below 2^31.  Every other argument and
+ * error is that of f8_matmul.
+ */
+int f8_matmul_experts(const uint8_t* x_codes, const float* x_scales, int64_t M, int64_t K, const uint8_t* codes,
+                      const float* scales, int64_t N, int32_t n_experts, const float* bias, const int32_t* offsets,
+                      const int32_t* order, int32_t top_k, void* y, int32_t y_dtype, void* stream);
+
+/*
+ * moe_gate -- the experts a token goes to and their weights.
+ *
+ * With p = softmax or sigmoid of token t's logits z: experts are chosen by c = p + bias,
+ * or without a bias by z itself (the same order as p's).  An expert whose logit or bias
+ * is -inf is not there.  With n_groups > 1 the experts form groups of n_experts /
+ * n_groups consecutive ones; a group's score is the sum of its group_top largest c
+ * (without a bias and with group_top 2: of p; -inf for experts that are not there), and
+ * only the top_groups groups of the highest scores take part.  The top_k largest c of
+ * those are chosen, in falling order.  Equal values go by index, lowest first; NaN is
+ * above everything.  c and scores are compared as float64 holds them.
+ *
+ *     weights[t, j] = scale * p_j   (renorm: / sum of p over the chosen ones)
+ *
+ *  logits      device [M, n_experts] of l_dtype (TQ_F32 or TQ_BF16), row t at
+ *              element t * ldl (ldl >= n_experts), aligned to its element.
+ *  n_experts   1 .. 512 (TQ_ERR_UNSUPPORTED above).
+ *  token_mask  device uint8 [M] or NULL: tokens whose byte is 0 go nowhere,
+ *              whatever their logits hold.
+ *  bias        device fp32 [n_experts] or NULL; it takes no part in the weights.
+ *  score       DMM_SOFTMAX or DMM_SIGMOID (TQ_ERR_UNSUPPORTED otherwise).
+ *  n_groups    divides n_experts, at most 64 (TQ_ERR_UNSUPPORTED above); 1 for none.
+ *  top_groups  1 .. n_groups.
+ *  group_top   1 or 2 (TQ_ERR_UNSUPPORTED otherwise); a group of one expert has one.
+ *  top_k       1 .. 32 (TQ_ERR_UNSUPPORTED above), at most the experts of top_groups
+ *              groups.
+ *  expert_ids  device int32 [M, top_k]: -1 for masked tokens, and behind the last
+ *              choice where fewer experts are there.
+ *  weights     device fp32 [M, top_k]: 0 where expert_ids is -1.
+ *
+ * Weights are fp32, each within (d + 32) 2^-23 of itself, d the spread of the token's
+ * finite logits (sigmoid: their largest magnitude); +inf and NaN logits of a softmax
+ * make its weights NaN where they are chosen (without renorm: all).  Sizes that need more than 2^32 - 1
+ * threads are TQ_ERR_SHAPE (M of 2^26 and more).
+ */
+int moe_gate(const void* logits, int32_t l_dtype, int64_t M, int32_t n_experts, int64_t ldl,
+             const uint8_t* token_mask, const float* bias, int32_t score, int32_t n_groups, int32_t top_groups,
+             int32_t group_top, int32_t top_k, int32_t renorm, float scale, int32_t* expert_ids, float* weights,
+             void* stream);
+
+/*
+ * moe_gate_grad -- the gradient of moe_gate's weights with respect to the logits,
+ * the choice being constant.  With p_j, w_j the scores and weights of token t's slots:
+ *
+ *     renorm, softmax   dlogits[t, e_j] += w_j (dw_j - mean)
+ *     renorm, sigmoid   dlogits[t, e_j] += w_j (dw_j - mean) (1 - p_j)
+ *     sigmoid           dlogits[t, e_j] += w_j dw_j (1 - p_j)
+ *     softmax           dlogits[t, e]    = p_e (g_e - sum_i p_i g_i),  g_{e_j} += scale dw_j
+ *
+ * where mean = sum_i w_i dw_i / sum_i w_i, and 0 elsewhere.
+ *
+ *  expert_ids  device int32 [M, top_k] from moe_gate (any ids; those outside [0,
+ *              n_experts) take no part, one that comes twice counts twice).
+ *  dweights    device fp32 [M, top_k]; not read where there is no expert.
+ *  dlogits     device [M, n_experts] of l_dtype, row t at element t * n_experts; rows
+ *              without an expert are 0.
+ *
+ * Other arguments as in moe_gate.  Statistics are fp32; the mean is taken off twice, so
+ * that the gradient of a weight that is nearly all is not lost in its rounding.
+ */
+int moe_gate_grad(const void* logits, int32_t l_dtype, int64_t M, int32_t n_experts, int64_t ldl,
+                  const int32_t* expert_ids, const float* dweights, int32_t score, int32_t top_k, int32_t renorm,
+                  float scale, void* dlogits, void* stream);
+
+/*
+ * moe_combine -- the experts' rows of a token into one:
+ *
+ *     out[t, n] = sum_j weights[t, j] y[t, j, n]  (+ add[t, n])
+ *
+ *  y           device [M, top_k, N] of y_dtype, e.g. of mx_matmul_experts.
+ *  expert_ids  device int32 [M, top_k]; slots whose id is outside [0, n_experts) take
+ *              no part, whatever y and weights hold there.
+ *  weights     device fp32 [M, top_k], e.g. of moe_gate.
+ *  add         device [M, N] of out_dtype or NULL (a shared expert, the residual);
+ *              may be out itself.
+ *  out         device [M, N] of out_dtype.
+ *
+ * Sums are fp32, add first and then the slots in order, each product fused into its
+ * addition; a bf16 out is rounded once.  M * top_k is below 2^31; sizes that need more than 2^32 - 1 threads are
+ * TQ_ERR_SHAPE.
+ */
+int moe_combine(const void* y, int32_t y_dtype, int64_t M, int32_t top_k, int64_t N, const int32_t* expert_ids,
+                const float* weights, int32_t n_experts, const void* add, void* out, int32_t out_dtype,
+                void* stream);
+
+/*
+ * moe_combine_grad -- the gradients of moe_combine (add's is dout itself):
+ *
+ *     dy[t, j, n] = weights[t, j] dout[t, n]     dweights[t, j] = sum_n dout[t, n] y[t, j, n]
+ *
+ *  y, expert_ids, weights, n_experts  as in moe_combine.
+ *  dout      device [M, N] of dout_dtype (TQ_F32 or TQ_BF16).
+ *  dy        device [M, top_k, N] of y_dtype; may be y itself.  Rows of slots without
+ *            an expert are 0.
+ *  dweights  device fp32 [M, top_k]; 0 for slots without an expert.  Sums are fp32 in
+ *            a fixed order.
+ *
+ * Sizes as in moe_combine (M * top_k below 2^24).
+ */
+int moe_combine_grad(const void* y, int32_t y_dtype, int64_t M, int32_t top_k, int64_t N, const int32_t* expert_ids,
+                     const float* weights, int32_t n_experts, const void* dout, int32_t dout_dtype, void* dy,
+                     float* dweights, void* stream);
 
 /* Human-readable name of a tq_status value. */
 const char* tq_status_string(int status);

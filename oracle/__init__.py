@@ -21,12 +21,15 @@ pages it follows:
   two-plane sum W ~ d1*T1 + d2*T2 ("The method") and the expert matmul.
 * The OCP Microscaling Formats specification: MXFP4 blocks.  The experts'
   routing lists and the router's balance loss are in the same module.
+* The e4m3 format of the OCP 8-bit floating-point specification, in blocks of 128
+  columns; the norm that packs, the router's choice and the combination of the
+  experts' rows are in the same module.
 
 Floating point is fp64 unless the pages fix a precision (fp16 group scales,
 bf16 activations and reconstructions, fp32 code-book entries).
 
 Parity status: every function is pinned by ``tests/test_oracle_pins.py`` or
-``tests/test_mx_cpu.py`` against worked examples, closed forms, exact rational arithmetic or brute
+``tests/test_mx_cpu.py`` or ``tests/test_f8_cpu.py`` against worked examples, closed forms, exact rational arithmetic or brute
 force.  No function is "parity unpinned".
 """
 
@@ -66,6 +69,19 @@ from .mx import (
     moe_balance,
     moe_balance_grad,
 )
+from .f8 import (
+    E4M3,
+    f8_encode,
+    f8_pack,
+    f8_unpack,
+    f8_matmul,
+    f8_norm,
+    gate_scores,
+    moe_gate,
+    moe_gate_grad,
+    moe_combine,
+    moe_combine_grad,
+)
 from .matmul import (
     REL_BOUND,
     matmul_ref,
@@ -82,6 +98,8 @@ __all__ = [
     "code_words", "rb_block_scales", "rb_encode", "rb_table", "rb_weights",
     "rb_truncate", "pack7", "unpack7", "rb_weights7",
     "E2M1", "mx_pack", "mx_unpack", "moe_route", "moe_balance", "moe_balance_grad",
+    "E4M3", "f8_encode", "f8_pack", "f8_unpack", "f8_matmul", "f8_norm", "gate_scores", "moe_gate", "moe_gate_grad", "moe_combine",
+    "moe_combine_grad",
     "REL_BOUND", "matmul_ref", "ternary_weights", "grouped_ref", "hot_prefix_weights",
     "check_bound",
 ]

@@ -1,0 +1,368 @@
+"""e4m3 packages, the norm that packs and the products on the GPU against the float64 oracle.
+
+Packing, decoding and the norm's package match bit for bit (the norm's factor is rounded
+from float64, whose own rounding reaches an fp32 border once in 2^29).  For products: the
+products of codes are exact in fp32 and a block's sum is off by at most 128 additions, the
+product of its two scales by one rounding, its product with the sum and the addition by one
+each, and a few more join sums and the bias; an addition (of a matrix instruction that
+truncates as well) is off by at most 2^-23 of the largest partial sum, itself at most
+B = sum |x w| + |bias|:
+    |y - y_ref| <= (K + 3 nb + 16) 2^-23 B   (+ 2^-8 |y| for the rounding to bf16).
+Where every product is a whole multiple of one unit and sums stay below 2^24 of it, no
+addition rounds and the results are equal.
+"""
+
+import numpy as np
+import pytest
+
+import oracle
+from test_gpu_mx import DEV, bf16_of, bf16_values, dev, guarded, host, intact, say
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module")
+def dmm():
+    import decode_matmul_amd
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    return decode_matmul_amd
+
+
+def rows_apart(a, dtype, pad):
+    """Device [M, K] of a (exact in dtype), its rows K + pad apart with NaN between them."""
+    if dtype == torch.bfloat16:
+        return bf16_of(a, pad)
+    t = torch.full((a.shape[0], a.shape[1] + pad), NAN, device=DEV)[:, :a.shape[1]]
+    t.copy_(dev(a))
+    return t
+
+
+def empty_package(dmm, rows, K, block_rows):
+    cs, ss = dmm.f8_shape(rows, K, block_rows)
+    return torch.full(cs, 0xA5, dtype=torch.uint8, device=DEV), torch.full(ss, -7.0, device=DEV)
+
+
+def same(a, b):
+    return np.array_equal(np.asarray(a, np.float32).view(np.uint32), np.asarray(b, np.float32).view(np.uint32)) \
+        or np.array_equal(a, b, equal_nan=True)
+
+
+# ------------------------------------------------------------------ packages
+
+PACK = [(1, 1), (1, 128), (3, 127), (5, 129), (2, 256), (130, 100), (16, 4096), (129, 1000), (1, 100000), (300, 7),
+        (257, 640)]
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("rows,K", PACK)
+def test_pack_and_unpack_are_exact(dmm, rows, K, dtype, block_rows):
+    say(f"f8_pack {rows}x{K} {dtype} {block_rows}")
+    rng = np.random.default_rng(rows * 1000 + K)
+    w = (rng.standard_normal((rows, K)) * 10.0 ** rng.uniform(-6, 6, (rows, 1))).astype(np.float32)
+    w[:, ::7] = np.round(w[:, ::7])
+    if rows > 2:
+        w[1] = 0
+        w[2, :] = rng.integers(-28, 29, K) * 16 + 8                 # ties
+    if dtype == torch.bfloat16:
+        w = bf16_values(w)
+    pad = 0 if K % 256 == 0 else 5
+    W = rows_apart(w, dtype, pad)
+    codes, scales = empty_package(dmm, rows, K, block_rows)
+    st = torch.full((1,), 99, dtype=torch.int32, device=DEV)
+    dmm.f8_pack(W, codes, scales, block_rows, status=st)
+    c, s, fine = oracle.f8_pack(w, block_rows)
+    assert fine and int(host(st)[0]) == 0
+    assert np.array_equal(host(scales), s) and np.array_equal(host(codes), c)
+    for out in (torch.float32, torch.bfloat16):
+        whole, y = guarded(rows * K, out)
+        dmm.f8_unpack(codes.view(torch.float8_e4m3fn), scales, rows, K, y, block_rows, status=st)
+        assert np.array_equal(host(y).reshape(rows, K), oracle.f8_unpack(c, s, K, block_rows).astype(np.float32))
+        assert intact(whole) and int(host(st)[0]) == 0
+
+
+def test_pack_of_extreme_blocks(dmm):
+    """Zeros of both signs, subnormals, the largest values, each scale's border, every e4m3
+    value, midpoint and neighbour; then blocks that are not finite."""
+    say("f8_pack extreme blocks")
+    w = np.zeros((600, 128), np.float32)
+    w[1, 3] = -0.0
+    w[2] = 2.0 ** -149
+    w[3, 1] = -(2.0 ** -126)
+    w[4] = np.finfo(np.float32).max
+    w[5, 5] = np.nextafter(np.float32(448), np.float32(500))
+    w[6, 5] = 448
+    w[7, :2] = 2.0 ** -126 * 448, 2.0 ** -126
+    w[8, :2] = 2.0 ** -126 * 449, 2.0 ** -149
+    grid = oracle.E4M3[:127]
+    points = np.concatenate([grid, (grid[1:] + grid[:-1]) / 2])
+    points = np.concatenate([points, points * (1 + 2.0 ** -23), points * (1 - 2.0 ** -24)])
+    for i, scale in enumerate((1.0, 2.0 ** -100, 2.0 ** 100)):
+        for j, part in enumerate(np.array_split(np.minimum(points, 448), 6)):
+            w[10 + 6 * i + j, 0] = 448 * scale
+            w[10 + 6 * i + j, 1:1 + len(part)] = part * scale * (-1) ** np.arange(len(part))
+    w[40:500] = np.random.default_rng(0).standard_normal((460, 128)) * 2.0 ** np.arange(-145, 120, 265 / 460)[:460, None]
+    for block_rows in (1, 128):
+        codes, scales = empty_package(dmm, 600, 128, block_rows)
+        dmm.f8_pack(dev(w), codes, scales, block_rows)
+        c, s, _ = oracle.f8_pack(w, block_rows)
+        assert np.array_equal(host(scales), s) and np.array_equal(host(codes), c)
+    w[550, 127], w[551, 0], w[552, 3] = np.inf, -np.inf, np.nan
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    codes, scales = empty_package(dmm, 600, 128, 1)
+    dmm.f8_pack(dev(w), codes, scales, status=st)
+    c, s, fine = oracle.f8_pack(w, 1)
+    assert not fine and int(host(st)[0]) == dmm.TQ_DATA_RANGE
+    assert np.array_equal(host(scales), s, equal_nan=True) and np.array_equal(host(codes), c)
+    y = torch.zeros((600, 128), device=DEV)
+    dmm.f8_unpack(codes, scales, 600, 128, y, status=st)
+    assert int(host(st)[0]) == dmm.TQ_DATA_RANGE
+    assert np.array_equal(host(y), oracle.f8_unpack(c, s, 128, 1).astype(np.float32), equal_nan=True)
+
+
+def test_unpack_of_every_code_and_padding(dmm):
+    """All 256 codes under scales that are no powers of two (one rounding of the product,
+    one more to bf16); a code past K is reported."""
+    say("f8_unpack of every code")
+    c = np.arange(256, dtype=np.uint8).reshape(2, 1, 128)
+    s = np.array([[0.3], [7.0]], np.float32)
+    y = torch.zeros((2, 128), device=DEV)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    dmm.f8_unpack(dev(c), dev(s), 2, 128, y, status=st)
+    ref = oracle.f8_unpack(c, s, 128, 1).astype(np.float32)
+    assert np.array_equal(host(y), ref, equal_nan=True) and int(host(st)[0]) == dmm.TQ_DATA_RANGE
+    b = torch.zeros((2, 128), dtype=torch.bfloat16, device=DEV)
+    dmm.f8_unpack(dev(c), dev(s), 2, 128, b)
+    assert np.array_equal(host(b), torch.from_numpy(ref).to(torch.bfloat16).float().numpy(), equal_nan=True)
+    y = torch.zeros((2, 100), device=DEV)
+    c[:, :, 100:] = 0
+    c[:, :, 127] = 1
+    c[0, 0, :] &= 0x77
+    dmm.f8_unpack(dev(c[:1]), dev(s[:1]), 1, 100, y[:1], status=st)
+    assert int(host(st)[0]) == dmm.TQ_DATA_PADDING
+
+
+# ---------------------------------------------------------------------- norm
+
+NORM = [(1, 1), (1, 4096), (3, 7), (5, 100), (2, 128), (33, 500), (70, 1000), (9, 2048), (4, 2056), (17, 4096),
+        (3, 5000), (6, 8192), (2, 8200), (3, 20001), (1, 70000)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("mode", ["plain", "residual", "in place"])
+@pytest.mark.parametrize("M,K", NORM, ids=["x".join(map(str, n)) for n in NORM])
+def test_norm_pack(dmm, M, K, mode, dtype):
+    say(f"f8_norm_pack M={M} K={K} {mode} {dtype}")
+    rng = np.random.default_rng(M * 7 + K)
+    bf = dtype == torch.bfloat16
+    store = (lambda v: bf16_values(v.astype(np.float32))) if bf else (lambda v: v.astype(np.float32))
+    x, r = (store(rng.standard_normal((M, K)) * 10.0 ** rng.uniform(-4, 4, (M, 1))) for _ in range(2))
+    if M > 2:
+        x[1], r[1] = 0, 0                                           # a row of nothing: f = eps^-1/2
+    w_bf = K % 3 == 0
+    weight = rng.standard_normal(K).astype(np.float32)
+    weight = bf16_values(weight[None])[0] if w_bf else weight
+    with_res = mode != "plain"
+    X, R = rows_apart(x, dtype, 3), rows_apart(r, dtype, 5) if with_res else None
+    if mode == "in place":
+        H = R
+    else:
+        H = torch.full((M, K + 2), 7.0, dtype=dtype, device=DEV)[:, :K]
+    whole, y = guarded(M * K, dtype)
+    codes, scales = empty_package(dmm, M, K, 1)
+    st = torch.full((1,), 99, dtype=torch.int32, device=DEV)
+    Wt = bf16_of(weight[None])[0] if w_bf else dev(weight)
+    dmm.f8_norm_pack(X, Wt, codes, scales, 1e-5, residual=R, h_out=H, y_out=y.view(M, K), status=st)
+    # x + residual in fp32 is the sum rounded to fp32 first (bf16: 16 bits of both fit 24
+    # unless they lie far apart; the oracle adds as the kernel's type does)
+    h, ref = oracle.f8_norm((x.astype(np.float32) + r.astype(np.float32)) if with_res else x, None, weight, 1e-5, store)
+    c, s, fine = oracle.f8_pack(ref, 1)
+    assert same(host(H), h) and int(host(st)[0]) == 0 and fine
+    assert same(host(y).reshape(M, K), store(ref.astype(np.float64))) and intact(whole)
+    assert np.array_equal(host(scales), s) and np.array_equal(host(codes), c)
+    # without the optional outputs the package is the same
+    if mode != "in place":
+        codes2, scales2 = empty_package(dmm, M, K, 1)
+        dmm.f8_norm_pack(X, Wt, codes2, scales2, 1e-5, residual=R)
+        assert torch.equal(codes, codes2) and torch.equal(scales, scales2)
+
+
+def test_norm_of_extremes(dmm):
+    """Squares that fp32 cannot hold; a row that is not finite touches no other."""
+    say("f8_norm_pack extremes")
+    rng = np.random.default_rng(0)
+    x = rng.standard_normal((6, 384)).astype(np.float32)
+    x[0] *= 1e30
+    x[1] *= 1e-30
+    x[2, 5], x[3, 200] = np.inf, np.nan
+    w = np.ones(384, np.float32)
+    codes, scales = empty_package(dmm, 6, 384, 1)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    y = torch.zeros((6, 384), device=DEV)
+    dmm.f8_norm_pack(dev(x), dev(w), codes, scales, 0.0, y_out=y, status=st)
+    assert int(host(st)[0]) == dmm.TQ_DATA_RANGE
+    fine = [0, 1, 4, 5]
+    _, ref = oracle.f8_norm(x[fine], None, w, 0.0, lambda v: v.astype(np.float32))
+    c, s, _ = oracle.f8_pack(ref, 1)
+    assert same(host(y)[fine], ref) and np.array_equal(host(scales)[fine], s) and np.array_equal(host(codes)[fine], c)
+    assert np.isnan(host(y)[3]).all() and np.isnan(host(scales)[3]).all() and np.isnan(host(scales)[2, 0])
+
+
+# ------------------------------------------------------------------ products
+
+
+def random_package(rng, rows, K, block_rows, spread=0.5, exact=False):
+    """Codes of normal values (exact: small whole numbers, scales 1 and 2) with any fp32 scales;
+    what lies past K is garbage, NaN codes among it."""
+    nb, nr = -(-K // 128), -(-rows // block_rows)
+    if exact:
+        v = rng.integers(-4, 5, (rows, nb * 128)).astype(np.float64)
+        s = (2.0 ** rng.integers(0, 2, (nr, nb))).astype(np.float32)
+    else:
+        v = np.clip(rng.standard_normal((rows, nb * 128)) * 40, -448, 448)
+        s = (2.0 ** rng.normal(-6, spread, (nr, nb))).astype(np.float32)
+    c = oracle.f8_encode(v)
+    c[:, K:] = rng.integers(0, 256, (rows, nb * 128 - K))
+    c[:, K:][:, ::3] = 0x7f
+    c = c.reshape(rows, nb, 128)
+    clean = c.reshape(rows, -1).copy()
+    clean[:, K:] = 0
+    return c, s, oracle.f8_unpack(clean.reshape(c.shape), s, K, block_rows)
+
+
+def tolerance(B, ref, K, dtype):
+    nb = -(-K // 128)
+    return (K + 3 * nb + 16) * 2.0 ** -23 * B + (2.0 ** -8 * np.abs(ref) if dtype == torch.bfloat16 else 0)
+
+
+def assert_close(y, ref, B, K, dtype, what):
+    off, tol = np.abs(y.astype(np.float64) - ref), tolerance(B, ref, K, dtype)
+    assert (off <= tol).all(), f"{what}: off by {(off / np.maximum(tol, 1e-300)).max():.3g} of the tolerance"
+
+
+MATMUL = [(1, 1, 1), (1, 16, 128), (2, 33, 100), (1, 300, 1000), (5, 129, 257), (16, 256, 512), (17, 130, 384),
+          (32, 500, 1024), (33, 64, 2048), (64, 1000, 640), (100, 257, 129), (128, 128, 4096), (300, 1001, 1000),
+          (257, 513, 896), (600, 700, 256), (1, 4096, 4096), (13, 1040, 8192), (1500, 2100, 200), (2100, 1500, 384),
+          (4, 9000, 640), (1, 20000, 256)]
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", MATMUL, ids=["x".join(map(str, m)) for m in MATMUL])
+def test_matmul(dmm, M, N, K, out):
+    say(f"f8_matmul M={M} N={N} K={K} {out}")
+    rng = np.random.default_rng(M + N + K)
+    xc, xs, x = random_package(rng, M, K, 1)
+    wc, ws, w = random_package(rng, N, K, 128)
+    bias = rng.standard_normal(N).astype(np.float32) if (M + N) % 2 else None
+    whole, y = guarded(M * N, out)
+    dmm.f8_matmul(dev(xc), dev(xs), M, K, dev(wc), dev(ws), N, y, bias=None if bias is None else dev(bias))
+    ref, B = oracle.f8_matmul(x, w, bias)
+    assert_close(host(y).reshape(M, N), ref, B, K, out, "y")
+    assert intact(whole)
+    again = torch.empty_like(y)
+    dmm.f8_matmul(dev(xc), dev(xs), M, K, dev(wc), dev(ws), N, again, bias=None if bias is None else dev(bias))
+    assert torch.equal(again, y)
+
+
+@pytest.mark.parametrize("M,N,K", MATMUL, ids=["x".join(map(str, m)) for m in MATMUL])
+def test_matmul_of_whole_numbers(dmm, M, N, K):
+    """Products of whole numbers up to 16 times scales up to 4: sums below 64 K <= 2^19, so nothing rounds."""
+    say(f"f8_matmul exact M={M} N={N} K={K}")
+    rng = np.random.default_rng(M * N + K)
+    xc, xs, x = random_package(rng, M, K, 1, exact=True)
+    wc, ws, w = random_package(rng, N, K, 128, exact=True)
+    whole, y = guarded(M * N, torch.float32)
+    dmm.f8_matmul(dev(xc), dev(xs), M, K, dev(wc), dev(ws), N, y)
+    assert np.array_equal(host(y).reshape(M, N), (x @ w.T).astype(np.float32)) and intact(whole)
+
+
+@pytest.mark.parametrize("M", [1, 20, 300])
+def test_matmul_of_nothing_and_nan(dmm, M):
+    """K = 0 leaves the bias; a NaN scale or code of x takes its row, of W its column."""
+    say(f"f8_matmul nothing and NaN M={M}")
+    N, K = 200, 300
+    rng = np.random.default_rng(M)
+    bias = rng.standard_normal(N).astype(np.float32)
+    y = torch.full((M, N), 7.0, device=DEV)
+    e, f = torch.empty(0, dtype=torch.uint8, device=DEV), torch.empty(0, device=DEV)
+    dmm.f8_matmul(e, f, M, 0, e, f, N, y, bias=dev(bias))
+    assert np.array_equal(host(y), np.broadcast_to(bias, (M, N)))
+    dmm.f8_matmul(e, f, M, 0, e, f, N, y)
+    assert not host(y).any()
+    dmm.f8_matmul(e, f, 0, 0, e, f, N, y[:0])
+    xc, xs, x = random_package(rng, M, K, 1)
+    wc, ws, w = random_package(rng, N, K, 128)
+    wc[7, 1, 3] = 0xff
+    ws[1, 2] = np.nan
+    xs[M // 2, 0] = np.nan
+    dmm.f8_matmul(dev(xc), dev(xs), M, K, dev(wc), dev(ws), N, y)
+    bad = np.zeros((M, N), bool)
+    bad[:, 7], bad[:, 128:], bad[M // 2] = True, True, True
+    got = host(y)
+    assert np.array_equal(np.isnan(got), bad)
+    ref, B = oracle.f8_matmul(x, w)
+    assert_close(np.where(bad, 0, got), np.where(bad, 0, ref), np.where(bad, 0, B), K, torch.float32, "the others")
+
+
+# ------------------------------------------------------------------- experts
+
+# M, N, K, E, top_k, bias, busy: every slot of a third of the tokens goes to one expert
+EXPERTS = [(1, 16, 128, 1, 1, False, False), (1, 50, 100, 8, 2, True, False), (16, 96, 512, 64, 8, False, False),
+           (5, 33, 129, 4, 3, True, True), (40, 130, 320, 6, 2, True, True), (130, 64, 1000, 3, 2, False, True),
+           (300, 270, 384, 5, 4, True, True), (600, 256, 160, 16, 2, False, False), (64, 20, 4224, 2, 1, False, False),
+           (257, 257, 64, 2, 2, True, True), (1000, 300, 256, 4, 2, True, False)]
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K,E,top_k,bias,busy", EXPERTS, ids=["x".join(map(str, e[:5])) for e in EXPERTS])
+def test_experts(dmm, M, N, K, E, top_k, bias, busy, out):
+    say(f"f8_matmul_experts M={M} N={N} K={K} E={E} top_k={top_k} bias={bias} {out}")
+    rng = np.random.default_rng(M + N + K)
+    xc, xs, x = random_package(rng, M, K, 1)
+    made = [random_package(rng, N, K, 128) for _ in range(E)]
+    b = rng.standard_normal((E, N)).astype(np.float32) if bias else None
+    ids = rng.integers(0, E, (M, top_k)).astype(np.int32)           # the same expert twice is possible
+    if busy:
+        ids[: M // 3] = E - 1
+    ids[rng.random((M, top_k)) < 0.1] = -1
+    _, offsets, order = oracle.moe_route(ids, E)
+    whole, y = guarded(M * top_k * N, out)
+    dmm.f8_matmul_experts(dev(xc), dev(xs), M, K, dev(np.stack([m[0] for m in made])),
+                          dev(np.stack([m[1] for m in made])), N, y, E, dev(offsets), dev(order), top_k,
+                          bias=None if b is None else dev(b))
+    got = host(y).reshape(M, top_k, N)
+    assert intact(whole) and np.isnan(got[ids < 0]).all()
+    for e in range(E):
+        t, j = np.nonzero(ids == e)
+        if len(t):
+            ref, B = oracle.f8_matmul(x[t], made[e][2], None if b is None else b[e])
+            assert_close(got[t, j], ref, B, K, out, f"expert {e}")
+
+
+@pytest.mark.parametrize("M,K,N", [(6, 96, 40), (60, 200, 140), (700, 256, 300), (200, 640, 140)])
+def test_experts_skip_bad_lists(dmm, M, K, N):
+    """Offsets and slots out of range are skipped; rows listed nowhere stay as they were."""
+    say(f"f8_matmul_experts with bad lists M={M}")
+    E = 3
+    rng = np.random.default_rng(M + K)
+    xc, xs, x = random_package(rng, M, K, 1)
+    made = [random_package(rng, N, K, 128) for _ in range(E)]
+    order = rng.permutation(M).astype(np.int32)
+    bad = rng.random(M) < 0.2
+    order[bad] = rng.choice(np.array([-1, -7, M, M + 1, 2**31 - 1, -2**31], np.int64), bad.sum()).astype(np.int32)
+    offsets = np.array([-3, M // 2, M // 2 + 2, 2 * M], np.int32)
+    whole, y = guarded(M * N, torch.float32)
+    y.fill_(3.0)
+    dmm.f8_matmul_experts(dev(xc), dev(xs), M, K, dev(np.stack([m[0] for m in made])),
+                          dev(np.stack([m[1] for m in made])), N, y, E, dev(offsets), dev(order), 1)
+    got = host(y).reshape(M, N)
+    assert intact(whole)
+    listed = np.zeros(M, bool)
+    for e, (a, z) in enumerate(((0, M // 2), (M // 2, M // 2 + 2), (M // 2 + 2, M))):
+        t = order[a:z][~bad[a:z]]
+        listed[t] = True
+        ref, B = oracle.f8_matmul(x[t], made[e][2])
+        assert_close(got[t], ref, B, K, torch.float32, f"expert {e}")
+    assert (got[~listed] == 3).all()
