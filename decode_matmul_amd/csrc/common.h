@@ -358,6 +358,7 @@ struct F8MatmulArgs {
     int y_dtype;
 };
 hipError_t launch_f8_matmul(const F8MatmulArgs& a, hipStream_t s);
+hipError_t launch_f8_gemm(const F8MatmulArgs& a, hipStream_t s);       // tiled form for many tokens
 
 // Most choices of a token.
 constexpr int kGateMaxTopK = 32;

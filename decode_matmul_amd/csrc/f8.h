@@ -44,6 +44,16 @@ __device__ __forceinline__ bf16x8 f8_bf16(uint32_t lo, uint32_t hi) {
     return u.v;
 }
 
+// The first `kept` (any number) of 16 bytes; zeros behind.
+__device__ __forceinline__ u32x4 keep_bytes(u32x4 v, int kept) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int n = kept - 4 * i;
+        v[i] &= n >= 4 ? 0xffffffffu : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
+    }
+    return v;
+}
+
 // Bits of the largest magnitude of eight values (those of nonnegative floats order as integers).
 __device__ __forceinline__ uint32_t largest8(const float* v) {
     uint32_t a = 0u;

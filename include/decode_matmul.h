@@ -740,7 +740,10 @@ int f8_norm_pack(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t l
  *
  * Products of codes are exact; a block's sum, the product of its two scales and the
  * sum over blocks are fp32, in an order fixed by the shape (two calls give the same
- * bits).  The product of two scales has to be one that fp32 holds (2^-126 to 2^128);
+ * bits).  For a bf16 y of more than 16 tokens the sums come from the e4m3 matrix
+ * instructions, of twice the rate, which keep 13 bits below the largest of each eight
+ * products: they may be off by D = 7 2^-13 sum over each eight columns of the largest
+ * |x w| as well (a bf16 y is rounded by up to 2^-9 of itself).  The product of two scales has to be one that fp32 holds (2^-126 to 2^128);
  * one that overflows makes its sums infinite or NaN.  A NaN scale or code makes what
  * it takes part in NaN.  M = 0 or N = 0 is a no-op; with K = 0 the packages may be
  * NULL and y = bias (or 0).  M and N are below 2^31, K is below 2^23; sizes that need
@@ -765,7 +768,7 @@ int f8_matmul(const uint8_t* x_codes, const float* x_scales, int64_t M, int64_t 
  * top_k for M and 1 for top_k with the same lists.  Entries of the lists outside their
  * range are skipped (nothing is read or written out of bounds; rows that are then
  * listed nowhere stay as they were).  M * top_k is below 2^31.  Every other argument and
- * error is that of f8_matmul.
+ * error is that of f8_matmul; D is for a bf16 y of 8 slots and more an expert on average.
  */
 int f8_matmul_experts(const uint8_t* x_codes, const float* x_scales, int64_t M, int64_t K, const uint8_t* codes,
                       const float* scales, int64_t N, int32_t n_experts, const float* bias, const int32_t* offsets,
