@@ -14,6 +14,20 @@ __device__ __forceinline__ T moved(T v) {
     return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
 }
 
+// f of a value and the one 16 lanes on or back (32), for a symmetric f: of two copies, the
+// odd rows of one change places with the even rows of the other.
+template <int D, class T, class F>
+__device__ __forceinline__ T with_row(T v, F f) {
+    static_assert(sizeof(T) == 4 && (D == 16 || D == 32), "rows of 16 lanes");
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    if (D == 16) {
+        const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+        return f(__builtin_bit_cast(T, (uint32_t)p[0]), __builtin_bit_cast(T, (uint32_t)p[1]));
+    }
+    const auto p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return f(__builtin_bit_cast(T, (uint32_t)p[0]), __builtin_bit_cast(T, (uint32_t)p[1]));
+}
+
 // f over the values of each L lanes (a power of two), in all of them.
 template <int L, class T, class F>
 __device__ __forceinline__ T over_group(T v, F f) {
@@ -21,8 +35,8 @@ __device__ __forceinline__ T over_group(T v, F f) {
     if (L >= 4) v = f(v, moved<0x4e>(v));
     if (L >= 8) v = f(v, moved<0x141>(v));
     if (L >= 16) v = f(v, moved<0x140>(v));
-    if (L >= 32) v = f(v, __shfl_xor(v, 16));
-    if (L >= 64) v = f(v, __shfl_xor(v, 32));
+    if (L >= 32) v = with_row<16>(v, f);
+    if (L >= 64) v = with_row<32>(v, f);
     return v;
 }
 

@@ -5,6 +5,18 @@
 // or, without a bias, by z, whose order is the same.  c is compared as float64 holds it.
 // An expert whose logit or bias is -inf is not there.  NaN ranks above everything, equal
 // values by index.
+//
+// Form.  Nearly always fp32 decides the order: a token takes L lanes of a wave, eight
+// experts each, and its choices come one after another as the largest of 32-bit keys, the
+// distance from the token's best in fixed point above the index (gate_kernel).  Where two
+// choices next to each other, or the last and the first that is not chosen, lie within the
+// error of that, the wave takes the token again in float64 (choose).  bf16 logits without a
+// bias fit a key as they are.  Sizes that do not fit the lanes take float64 throughout
+// (gate_exact_kernel).
+//
+// Bound: the vector instructions of the choice, a dozen for each choice and token and sixty
+// to sort each lane's experts, beside the logits' bytes; for few tokens the chain of launch, loads
+// and choices.
 #include "lanes.h"
 
 namespace dmm {
@@ -35,6 +47,9 @@ __device__ __forceinline__ void wave_first(uint64_t& key, int& at) {
         }
     }
 }
+
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t smaller(uint32_t a, uint32_t b) { return a < b ? a : b; }
 
 __device__ __forceinline__ float logit(const GateArgs& a, int64_t at) {
     return a.l_dtype == TQ_BF16 ? bf16_bits_to_f32(((const uint16_t*)a.logits)[at]) : ((const float*)a.logits)[at];
@@ -173,11 +188,188 @@ __device__ void choose(const GateArgs& a, int64_t t, double* lds) {
     }
 }
 
-__global__ void __launch_bounds__(kThreads) gate_kernel(GateArgs a) {
+__global__ void __launch_bounds__(kThreads) gate_exact_kernel(GateArgs a) {
     __shared__ double lds[kWaves][kMoeMaxExperts];
     const int wave = readfirstlane((int)threadIdx.x >> 6);
     const int64_t t = (int64_t)blockIdx.x * kWaves + wave;
     if (t < a.M) choose(a, t, lds[wave]);
+}
+
+// Eight keys in falling order (19 exchanges, of odd and even merges).
+__device__ __forceinline__ void sort8(uint32_t* k) {
+    auto cx = [&](int i, int j) {
+        const uint32_t hi = k[i] > k[j] ? k[i] : k[j], lo = k[i] > k[j] ? k[j] : k[i];
+        k[i] = hi;
+        k[j] = lo;
+    };
+    cx(0, 1), cx(2, 3), cx(4, 5), cx(6, 7);
+    cx(0, 2), cx(1, 3), cx(4, 6), cx(5, 7);
+    cx(1, 2), cx(5, 6);
+    cx(0, 4), cx(1, 5), cx(2, 6), cx(3, 7);
+    cx(2, 4), cx(3, 5);
+    cx(1, 2), cx(3, 4), cx(5, 6);
+}
+
+// A token by L lanes.  A key is Q - (best - x) S, with x = c or z in fp32, above the index:
+// 32 - log2(8 L) bits of fixed point over W below the best.  Keys further down share the
+// least one.  (A bf16 z: its 16 bits, of the same order.)
+template <bool BF16, int L>
+__global__ void __launch_bounds__(kThreads) gate_kernel(GateArgs a) {
+    constexpr int kBits = L == 8 ? 6 : L == 16 ? 7 : L == 32 ? 8 : 9;       // of the index
+    constexpr uint32_t kMask = 8 * L - 1, kQ = 0xffffffffu >> kBits;
+    __shared__ double lds[kWaves][kMoeMaxExperts];
+    const int lane = (int)threadIdx.x & 63, l = lane % L, E = a.E;
+    const int64_t t = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / L;
+    const bool live = t < a.M && (!a.mask || a.mask[t] != 0);
+    const int e0 = l * 8, have = E - e0;
+    const bool sigmoid = a.score == DMM_SIGMOID, grouped = a.n_groups > 1;
+    const bool by_score = a.bias || (grouped && a.group_top > 1);
+    const float none = -__builtin_inff();
+    float z[8], b[8];
+    load_row8<BF16>(a.logits, live ? t * a.ldl + e0 : 0, live ? have : 0, z, none);
+    if (a.bias) load_row8<false>(a.bias, e0, have, b, none);
+    float top = z[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) top = __builtin_elementwise_maximum(top, z[i]);
+    top = group_max<L>(top);
+    // fp32 scores; inv is 1 / (sum of e^(z - top)) of a softmax
+    float x[8], inv = 1.f, best = top;
+    if (!sigmoid && (by_score || !a.renorm)) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            x[i] = __builtin_amdgcn_exp2f((z[i] - top) * 1.44269504088896340736f);
+            sum += z[i] == none ? 0.f : x[i];
+        }
+        inv = __builtin_amdgcn_rcpf(group_sum<L>(sum));
+    }
+    if (by_score) {
+        best = none;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            x[i] = sigmoid ? __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z[i] * -1.44269504088896340736f)) : x[i] * inv;
+            if (a.bias) x[i] += b[i];
+            if (z[i] == none || (a.bias && b[i] == none)) x[i] = none;
+            best = __builtin_elementwise_maximum(best, x[i]);
+        }
+        best = group_max<L>(best);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = z[i];
+    }
+    // W = 2 for scores (p lies in [0, 1]), 16 for logits
+    const bool whole = BF16 && !by_score;       // a key says all
+    const float unit = (float)(1u << (32 - kBits - 1)) * (by_score ? 1.f : 0.125f);
+    uint32_t k[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t down = (uint32_t)__builtin_fminf((best - x[i]) * unit, 4294967040.f);
+        uint32_t q = down < kQ ? kQ - down : 1u;
+        if (whole) {
+            const uint32_t u = __builtin_bit_cast(uint32_t, x[i] + 0.f);        // one zero
+            q = ((u >> 31) ? ~u : u | 0x80000000u) >> 16;
+        }
+        k[i] = x[i] == none ? 0u : q << kBits | (kMask - (uint32_t)(e0 + i));
+    }
+    sort8(k);
+    // How far keys of values in the other order can lie apart.  Rounding and truncation keep the
+    // order; scores are off by the error of p (sigmoid: 2^-21; softmax: p (d + 32) 2^-23 at a
+    // distance d from the best, at most 2^-18 inv), of the sum and of the distance.
+    const float err = (sigmoid ? 0x1p-21f : inv * 0x1p-18f) + (__builtin_fabsf(best) + 2.f) * 0x1p-23f;
+    const uint32_t margin = by_score ? 2u + (uint32_t)(2.f * err * unit) : 0u;
+    bool again = live && best != none && !(__builtin_fabsf(best) < __builtin_inff());    // NaN or +inf
+    if (grouped) {
+        // a group is S lanes; its score from the keys of its two best
+        const int size = E / a.n_groups, S = size / 8, group = l / S;
+        uint32_t m1 = k[0] >> kBits, m2 = k[1] >> kBits;
+        auto merge = [&](uint32_t o1, uint32_t o2) {
+            const uint32_t lo = m1 < o1 ? m1 : o1, hi2 = m2 > o2 ? m2 : o2;
+            m1 = m1 > o1 ? m1 : o1;
+            m2 = lo > hi2 ? lo : hi2;
+        };
+        if (S >= 2) merge(moved<0xb1>(m1), moved<0xb1>(m2));
+        if (S >= 4) merge(moved<0x4e>(m1), moved<0x4e>(m2));
+        if (S >= 8) merge(moved<0x141>(m1), moved<0x141>(m2));
+        if (S >= 16) merge(moved<0x140>(m1), moved<0x140>(m2));
+        if (S >= 32) merge((uint32_t)__shfl_xor((int)m1, 16), (uint32_t)__shfl_xor((int)m2, 16));
+        // (kQ has at most 26 bits and n_groups is at most L: 27 + 6 bits would not fit, so the
+        // group's number goes beside the score)
+        const bool there = group < a.n_groups;
+        uint32_t score = !there ? 0u : 1u + (a.group_top > 1 ? m1 + (size > 1 ? m2 : 0u) : m1);
+        // fewer experts there than group_top counts (float64's -inf), or one below W
+        again |= !whole && live && there && (m1 == 0u || (a.group_top > 1 && m2 <= 1u));
+        bool kept = false;
+        uint32_t last = 0u;
+        for (int j = 0; j <= a.top_groups && j < a.n_groups; ++j) {
+            const uint32_t s = over_group<L>(score, larger);
+            const uint32_t g = over_group<L>(score == s ? (uint32_t)group : 0xffffu, smaller);
+            if (j == a.top_groups) {
+                again |= !whole && live && last - s <= 2u * margin;
+            } else {
+                last = s;
+                if ((uint32_t)group == g) {
+                    kept = true;
+                    score = 0u;
+                }
+            }
+        }
+        if (!kept) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) k[i] = 0u;
+        }
+    }
+    // lane j keeps the j-th largest key, j <= top_k
+    uint32_t mine = 0u;
+    for (int j = 0; j <= a.top_k; ++j) {
+        const uint32_t first = over_group<L>(k[0], larger);
+        if (l == j) mine = first;
+        const bool won = k[0] == first;
+#pragma unroll
+        for (int i = 0; i < 7; ++i) k[i] = won ? k[i + 1] : k[i];
+        k[7] = won ? 0u : k[7];
+    }
+    const bool has = mine != 0u;
+    const int id = (int)(kMask - (mine & kMask));
+    float zj = has ? logit(a, t * a.ldl + id) : none;
+    if (!whole) {
+        const uint32_t next = (uint32_t)__shfl_down((int)mine, 1);  // in lane j + 1
+        const bool near = next != 0u && (mine >> kBits) - (next >> kBits) <= margin;
+        const int any = l < a.top_k && has && (near || (mine >> kBits) == 1u);
+        again |= over_group<L>(any, [](int p, int q) { return p | q; }) != 0;
+    }
+    const bool chosen = has && l < a.top_k;
+    if (!chosen) zj = none;
+    float w;
+    if (sigmoid) {
+        const float up = expf(-__builtin_fabsf(zj));            // e^-|z|
+        if (a.renorm) {
+            // p e^-m with m = min(0, the largest chosen logit): never 0 for all
+            float m = group_max<L>(zj);
+            m = m < 0.f ? m : 0.f;
+            w = (zj > 0.f ? 1.f : expf(zj - m)) / (1.f + up);
+            if (!chosen) w = 0.f;
+            w /= group_sum<L>(w);
+        } else {
+            w = (zj > 0.f ? 1.f : up) / (1.f + up);
+        }
+    } else if (a.renorm) {
+        const float m = group_max<L>(zj);
+        w = chosen ? expf(zj - m) : 0.f;
+        w /= group_sum<L>(w);
+    } else {
+        w = expf(zj - top) * inv;
+    }
+    if (t < a.M && l < a.top_k && !again) {
+        a.ids[t * a.top_k + l] = chosen ? id : -1;
+        a.weights[t * a.top_k + l] = chosen ? w * a.scale : 0.f;
+    }
+    uint64_t left = __ballot(again);
+    const int wave = readfirstlane((int)threadIdx.x >> 6);
+    while (left) {
+        const int at = __builtin_ctzll(left) / L;
+        choose(a, ((int64_t)blockIdx.x * kThreads + wave * 64) / L + at, lds[wave]);
+        left &= L == 64 ? 0ull : ~(((1ull << (L & 63)) - 1ull) << (at * L));
+    }
 }
 
 // --------------------------------------------------------------- gradient
@@ -314,6 +506,26 @@ __global__ void __launch_bounds__(kThreads) gate_grad_kernel(GateGradArgs a) {
 }
 
 template <bool BF16, int L>
+hipError_t gate(const GateArgs& a, hipStream_t s) {
+    const int size = a.E / a.n_groups, S = size / 8;
+    // lanes for one choice more than top_k; groups of whole lanes, a power of two of them
+    const bool fits = a.top_k < L && (a.n_groups == 1 || (size % 8 == 0 && (S & (S - 1)) == 0));
+    if (fits) gate_kernel<BF16, L><<<(unsigned)((a.M * L + kThreads - 1) / kThreads), kThreads, 0, s>>>(a);
+    else gate_exact_kernel<<<(unsigned)((a.M + kWaves - 1) / kWaves), kThreads, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <bool BF16>
+hipError_t gate_by_lanes(const GateArgs& a, hipStream_t s) {
+    switch (row_lanes(a.E)) {
+        case 16: return gate<BF16, 16>(a, s);
+        case 32: return gate<BF16, 32>(a, s);
+        case 64: return gate<BF16, 64>(a, s);
+        default: return gate<BF16, 8>(a, s);
+    }
+}
+
+template <bool BF16, int L>
 hipError_t grad(const GateGradArgs& a, hipStream_t s) {
     const int64_t blocks = (a.M * L + kThreads - 1) / kThreads;
     if (!grid_fits(blocks, kThreads)) return hipErrorInvalidConfiguration;
@@ -334,10 +546,8 @@ hipError_t grad_by_lanes(const GateGradArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_moe_gate(const GateArgs& a, hipStream_t s) {
-    const int64_t blocks = (a.M + kWaves - 1) / kWaves;
-    if (!grid_fits(blocks, kThreads)) return hipErrorInvalidConfiguration;
-    gate_kernel<<<(unsigned)blocks, kThreads, 0, s>>>(a);
-    return hipGetLastError();
+    if (!grid_fits((a.M + kWaves - 1) / kWaves, kThreads)) return hipErrorInvalidConfiguration;
+    return a.l_dtype == TQ_BF16 ? gate_by_lanes<true>(a, s) : gate_by_lanes<false>(a, s);
 }
 
 hipError_t launch_moe_gate_grad(const GateGradArgs& a, hipStream_t s) {
