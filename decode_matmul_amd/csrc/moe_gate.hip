@@ -26,7 +26,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kMaxGroups = 64;
-constexpr int kEach = kMoeMaxExperts / 64;      // experts a lane, at most
 
 // A float64 as an integer of the same order: 0 for an expert that is not there, NaN highest.
 __device__ __forceinline__ uint64_t order_of(double c) {
@@ -35,36 +34,36 @@ __device__ __forceinline__ uint64_t order_of(double c) {
     return (u >> 63) ? ~u : u | (1ull << 63);
 }
 
-// The largest key of the wave, of equal ones the lowest index.
-__device__ __forceinline__ void wave_first(uint64_t& key, int& at) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-        const uint64_t k = (uint64_t)__shfl_xor((unsigned long long)key, d);
-        const int i = __shfl_xor(at, d);
-        if (k > key || (k == key && i < at)) {
-            key = k;
-            at = i;
-        }
-    }
-}
-
 __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
 __device__ __forceinline__ uint32_t smaller(uint32_t a, uint32_t b) { return a < b ? a : b; }
+
+// The largest key of the wave, of equal ones the lowest index.
+__device__ __forceinline__ void wave_first(uint64_t& key, int& at) {
+    const uint32_t hi = over_group<64>((uint32_t)(key >> 32), larger);
+    const uint32_t lo = over_group<64>((uint32_t)(key >> 32) == hi ? (uint32_t)key : 0u, larger);
+    const uint64_t first = (uint64_t)hi << 32 | lo;
+    at = (int)over_group<64>(key == first ? (uint32_t)at : 0xffffffffu, smaller);
+    key = first;
+}
 
 __device__ __forceinline__ float logit(const GateArgs& a, int64_t at) {
     return a.l_dtype == TQ_BF16 ? bf16_bits_to_f32(((const uint16_t*)a.logits)[at]) : ((const float*)a.logits)[at];
 }
 
-// Token t by one wave; lds: n_experts doubles of its own.
-__device__ void choose(const GateArgs& a, int64_t t, double* lds) {
+// e^x by the hardware's exp2, off by |x| 2^-24 of itself, the rounding of its argument, and a unit.
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f); }
+
+// Token t by one wave, EACH experts a lane; lds: n_experts doubles of its own.
+template <int EACH>
+__device__ __forceinline__ void choose(const GateArgs& a, int64_t t, double* lds) {
     const int lane = (int)threadIdx.x & 63, E = a.E, size = E / a.n_groups;
     const bool live = !a.mask || a.mask[t] != 0;
     const bool by_score = a.bias || (a.n_groups > 1 && a.group_top > 1);
-    float z[kEach];
-    bool there[kEach];
+    float z[EACH];
+    bool there[EACH];
     float top = -__builtin_inff();
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
+    for (int i = 0; i < EACH; ++i) {
         const int e = lane + 64 * i;
         z[i] = live && e < E ? logit(a, t * a.ldl + e) : -__builtin_inff();
         there[i] = z[i] != -__builtin_inff() && (!a.bias || a.bias[e] != -__builtin_inff());
@@ -72,11 +71,11 @@ __device__ void choose(const GateArgs& a, int64_t t, double* lds) {
     }
     top = group_max<64>(top);
     // float64 scores
-    double p[kEach];
+    double p[EACH];
     if (by_score) {
         double sum = 0.0;
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
+        for (int i = 0; i < EACH; ++i) {
             p[i] = 0.0;
             if (z[i] == -__builtin_inff()) continue;
             p[i] = a.score == DMM_SIGMOID ? 1.0 / (1.0 + exp(-(double)z[i])) : exp((double)z[i] - (double)top);
@@ -85,19 +84,19 @@ __device__ void choose(const GateArgs& a, int64_t t, double* lds) {
         if (a.score != DMM_SIGMOID) {
             sum = wave_sum(sum);
 #pragma unroll
-            for (int i = 0; i < kEach; ++i) p[i] /= sum;
+            for (int i = 0; i < EACH; ++i) p[i] /= sum;
         }
     }
-    uint64_t key[kEach];
+    uint64_t key[EACH];
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
+    for (int i = 0; i < EACH; ++i) {
         const int e = lane + 64 * i;
         key[i] = there[i] ? order_of(a.bias ? p[i] + (double)a.bias[e] : (double)z[i]) : 0ull;
     }
     if (a.n_groups > 1) {
         // what a group's score is made of
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
+        for (int i = 0; i < EACH; ++i) {
             const int e = lane + 64 * i;
             if (e < E)
                 lds[e] = !there[i] ? -(double)__builtin_inff()
@@ -109,6 +108,7 @@ __device__ void choose(const GateArgs& a, int64_t t, double* lds) {
         if (lane < a.n_groups) {
             double first = -(double)__builtin_inff(), second = first;
             bool nan = false;
+#pragma unroll 8
             for (int i = 0; i < size; ++i) {
                 const double v = lds[lane * size + i];
                 nan |= v != v;
@@ -131,7 +131,7 @@ __device__ void choose(const GateArgs& a, int64_t t, double* lds) {
             if (lane == at) score = 0ull;
         }
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
+        for (int i = 0; i < EACH; ++i) {
             const int e = lane + 64 * i;
             if (e < E && !((kept >> (e / size)) & 1)) key[i] = 0ull;
         }
@@ -143,7 +143,7 @@ __device__ void choose(const GateArgs& a, int64_t t, double* lds) {
         uint64_t k = 0ull;
         int at = 1 << 30;
 #pragma unroll
-        for (int i = 0; i < kEach; ++i)
+        for (int i = 0; i < EACH; ++i)
             if (key[i] > k) {
                 k = key[i];
                 at = lane + 64 * i;
@@ -152,7 +152,7 @@ __device__ void choose(const GateArgs& a, int64_t t, double* lds) {
         if (k == 0ull) break;
         if (lane == j) mine = at;
 #pragma unroll
-        for (int i = 0; i < kEach; ++i)
+        for (int i = 0; i < EACH; ++i)
             if (lane + 64 * i == at) key[i] = 0ull;
     }
     // weights in fp32
@@ -177,7 +177,7 @@ __device__ void choose(const GateArgs& a, int64_t t, double* lds) {
         if (!a.renorm) {
             sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < kEach; ++i)
+            for (int i = 0; i < EACH; ++i)
                 if (z[i] != -__builtin_inff()) sum += expf(z[i] - m);
         }
         w /= group_sum<64>(sum);
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads) gate_exact_kernel(GateArgs a) {
     __shared__ double lds[kWaves][kMoeMaxExperts];
     const int wave = readfirstlane((int)threadIdx.x >> 6);
     const int64_t t = (int64_t)blockIdx.x * kWaves + wave;
-    if (t < a.M) choose(a, t, lds[wave]);
+    if (t < a.M) choose<kMoeMaxExperts / 64>(a, t, lds[wave]);
 }
 
 // Eight keys in falling order (19 exchanges, of odd and even merges).
@@ -243,19 +243,29 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(GateArgs a) {
         }
         inv = __builtin_amdgcn_rcpf(group_sum<L>(sum));
     }
-    if (by_score) {
+    if (!by_score) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = z[i];
+    } else {
+        if (sigmoid) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                x[i] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z[i] * -1.44269504088896340736f));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] *= inv;
+        }
+        if (a.bias) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = b[i] == none ? none : x[i] + b[i];
+        }
         best = none;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            x[i] = sigmoid ? __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z[i] * -1.44269504088896340736f)) : x[i] * inv;
-            if (a.bias) x[i] += b[i];
-            if (z[i] == none || (a.bias && b[i] == none)) x[i] = none;
+            x[i] = z[i] == none ? none : x[i];
             best = __builtin_elementwise_maximum(best, x[i]);
         }
         best = group_max<L>(best);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = z[i];
     }
     // W = 2 for scores (p lies in [0, 1]), 16 for logits
     const bool whole = BF16 && !by_score;       // a key says all
@@ -367,7 +377,7 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(GateArgs a) {
     const int wave = readfirstlane((int)threadIdx.x >> 6);
     while (left) {
         const int at = __builtin_ctzll(left) / L;
-        choose(a, ((int64_t)blockIdx.x * kThreads + wave * 64) / L + at, lds[wave]);
+        choose<L / 8>(a, ((int64_t)blockIdx.x * kThreads + wave * 64) / L + at, lds[wave]);
         left &= L == 64 ? 0ull : ~(((1ull << (L & 63)) - 1ull) << (at * L));
     }
 }
@@ -383,21 +393,20 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(GateArgs a) {
 // below the rounding of its mean: what the mean is off by comes back as the mean of the
 // differences and is taken off again.  A row of E logits lies with L lanes, eight
 // consecutive ones each; the slots are dealt over the same lanes.
-constexpr int kSlots = kGateMaxTopK / 8;        // slots a lane of eight, at most
-
-template <bool BF16, int L>
+template <bool BF16, int L, int SLOTS>
 __global__ void __launch_bounds__(kThreads) gate_grad_kernel(GateGradArgs a) {
+    __shared__ __attribute__((aligned(16))) float rows[kWaves][8 * 64];     // of a wave's tokens
     const int lane = (int)threadIdx.x & 63, l = lane % L;
     const int64_t t = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / L;
-    if (t >= a.M) return;                       // all L lanes alike
+    if (t >= a.M) return;                       // all L lanes alike; nothing below crosses waves
     const int E = a.E, e0 = l * 8, have = E - e0;
     const bool dense = a.score != DMM_SIGMOID && !a.renorm;
     // this lane's slots
-    int id[kSlots];
-    float zj[kSlots], dw[kSlots], v[kSlots];
+    int id[SLOTS], some = 0;
+    float zj[SLOTS], dw[SLOTS], v[SLOTS];
     float m = -__builtin_inff();
 #pragma unroll
-    for (int i = 0; i < kSlots; ++i) {
+    for (int i = 0; i < SLOTS; ++i) {
         const int j = l + i * L;
         id[i] = j < a.top_k ? a.ids[t * a.top_k + j] : -1;
         if ((uint32_t)id[i] >= (uint32_t)E) id[i] = -1;
@@ -407,17 +416,15 @@ __global__ void __launch_bounds__(kThreads) gate_grad_kernel(GateGradArgs a) {
             zj[i] = BF16 ? bf16_bits_to_f32(((const uint16_t*)a.logits)[t * a.ldl + id[i]])
                          : ((const float*)a.logits)[t * a.ldl + id[i]];
         m = __builtin_elementwise_maximum(m, zj[i]);
+        some |= id[i] >= 0;
         v[i] = 0.f;
     }
     float z[8], p[8], g[8];
     float off = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] = 0.f;
-    int some = 0;
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i) some |= id[i] >= 0;
     some = over_group<L>(some, [](int x, int y) { return x | y; });
     if (!some) {                                // a masked token, whatever its logits hold
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = 0.f;
         store_row8<BF16>(a.dlogits, t * E + e0, have, g);
         return;
     }
@@ -430,64 +437,63 @@ __global__ void __launch_bounds__(kThreads) gate_grad_kernel(GateGradArgs a) {
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            p[i] = z[i] == -__builtin_inff() ? 0.f : expf(z[i] - top);
+            p[i] = z[i] == -__builtin_inff() ? 0.f : exp_of(z[i] - top);
             sum += p[i];
         }
         sum = group_sum<L>(sum);
 #pragma unroll
         for (int i = 0; i < 8; ++i) p[i] = sum > 0.f || sum != sum ? p[i] / sum : 0.f;
 #pragma unroll
-        for (int i = 0; i < kSlots; ++i) v[i] = a.scale * dw[i];
+        for (int i = 0; i < SLOTS; ++i) v[i] = a.scale * dw[i];
     } else {
         m = group_max<L>(m);
         const bool sigmoid = a.score == DMM_SIGMOID;
         const float base = sigmoid ? (m < 0.f ? m : 0.f) : m;
-        float q[kSlots], rest[kSlots], sum = 0.f;
+        float q[SLOTS], rest[SLOTS], sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < kSlots; ++i) {
+        for (int i = 0; i < SLOTS; ++i) {
             q[i] = rest[i] = 0.f;
             if (id[i] < 0 || zj[i] == -__builtin_inff()) continue;
-            const float up = expf(-__builtin_fabsf(zj[i]));         // e^-|z|
+            const float up = exp_of(-__builtin_fabsf(zj[i]));         // e^-|z|
             rest[i] = sigmoid ? (zj[i] > 0.f ? up / (1.f + up) : 1.f / (1.f + up)) : 1.f;   // 1 - p
-            if (!sigmoid) q[i] = expf(zj[i] - base);
+            if (!sigmoid) q[i] = exp_of(zj[i] - base);
             else if (zj[i] > 0.f) q[i] = 1.f / (1.f + up);
-            else q[i] = (a.renorm ? expf(zj[i] - base) : up) / (1.f + up);
+            else q[i] = (a.renorm ? exp_of(zj[i] - base) : up) / (1.f + up);
             sum += q[i];
         }
         if (a.renorm) {
             sum = group_sum<L>(sum);
             float mean = 0.f;
 #pragma unroll
-            for (int i = 0; i < kSlots; ++i) {
+            for (int i = 0; i < SLOTS; ++i) {
                 if (id[i] >= 0) q[i] /= sum;
                 mean += q[i] * dw[i];
             }
             mean = group_sum<L>(mean);
 #pragma unroll
-            for (int i = 0; i < kSlots; ++i) {
+            for (int i = 0; i < SLOTS; ++i) {
                 dw[i] -= mean;
                 off += q[i] * dw[i];
             }
             off = group_sum<L>(off);
 #pragma unroll
-            for (int i = 0; i < kSlots; ++i) dw[i] -= off;
+            for (int i = 0; i < SLOTS; ++i) dw[i] -= off;
         }
 #pragma unroll
-        for (int i = 0; i < kSlots; ++i) v[i] = q[i] != 0.f || q[i] != q[i] ? a.scale * q[i] * dw[i] * rest[i] : 0.f;
+        for (int i = 0; i < SLOTS; ++i) v[i] = q[i] != 0.f || q[i] != q[i] ? a.scale * q[i] * dw[i] * rest[i] : 0.f;
     }
-    // slots in order to the experts they name
+    // slots in order to the experts they name: a wave's LDS accesses happen in order
+    float* const row = &rows[threadIdx.x >> 6][(lane - l) * 8];
+    *(f32x4*)(row + e0) = *(f32x4*)(row + e0 + 4) = (f32x4){0.f, 0.f, 0.f, 0.f};
+    asm volatile("" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < kSlots; ++i) {
-        if (i * L >= a.top_k) break;
-        const int n = a.top_k - i * L < L ? a.top_k - i * L : L;
-        for (int j = 0; j < n; ++j) {
-            const int from = lane - l + j;
-            const int e = __shfl(id[i], from) - e0;
-            const float x = __shfl(v[i], from);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) g[k] += e == k ? x : 0.f;
+    for (int i = 0; i < SLOTS; ++i)
+        for (int j = 0; j < L && j + i * L < a.top_k; ++j) {
+            if (l == j && id[i] >= 0) __builtin_amdgcn_ds_faddf((__attribute__((address_space(3))) float*)(row + id[i]), v[i], 0, 0, false);
+            asm volatile("" ::: "memory");
         }
-    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = row[e0 + i];
     if (dense) {
         float mean = 0.f;
 #pragma unroll
@@ -529,7 +535,10 @@ template <bool BF16, int L>
 hipError_t grad(const GateGradArgs& a, hipStream_t s) {
     const int64_t blocks = (a.M * L + kThreads - 1) / kThreads;
     if (!grid_fits(blocks, kThreads)) return hipErrorInvalidConfiguration;
-    gate_grad_kernel<BF16, L><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+    // a slot a lane, or as many as kGateMaxTopK needs
+    constexpr int most = (kGateMaxTopK + L - 1) / L;
+    if (most == 1 || a.top_k <= L) gate_grad_kernel<BF16, L, 1><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+    else gate_grad_kernel<BF16, L, most><<<(unsigned)blocks, kThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 
