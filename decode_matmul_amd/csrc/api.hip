@@ -512,7 +512,7 @@ int f8_norm_pack(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t l
     if (!aligned(x, xb) || !aligned(residual, xb) || !aligned(h_out, xb) || !aligned(y_out, xb) ||
         !aligned(weight, bytes_of(w_dtype)) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(d_status, 4))
         return TQ_ERR_ALIGN;
-    if (!dmm::grid_fits(M, 512)) return TQ_ERR_SHAPE;
+    if (!dmm::grid_fits(M, 1024)) return TQ_ERR_SHAPE;
     hipStream_t s = (hipStream_t)stream;
     if (d_status && dmm::launch_status_clear(d_status, s) != hipSuccess) return TQ_ERR_HIP;
     const dmm::F8NormArgs a = {x,   x_dtype, M,   K,     ldx, residual, ldr,    weight, w_dtype,

@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kThreads) f8_unpack_kernel(const uint8_t* code
         for (int i = 0; i < 8; ++i) rest |= i >= have && ((c[i >> 2] >> (8 * (i & 3))) & 0xffu) != 0u;
         if (rest) atomic_or_status(status, TQ_DATA_PADDING);
     }
-    if (have > 0) store_row8<BF16>(out, row * K + k, have, v);
+    if (have > 0) store_row8<BF16, true>(out, row * K + k, have, v);
 }
 
 // ------------------------------------------------------------------- norm
@@ -120,11 +120,66 @@ __global__ void __launch_bounds__(kThreads) f8_unpack_kernel(const uint8_t* code
 // fp32), rounded to fp32; y = h f weight, each product rounded to fp32; y's package.
 // The factor does not depend on how the sum is split, up to float64's own rounding, so that the package hardly ever does.
 //
-// WAVES waves a row, 4 / WAVES rows a workgroup of four.  HELD: the row's values stay in
-// registers, CHUNKS times eight a lane; longer rows are read twice.
-template <bool BF16, int WAVES, int CHUNKS, bool HELD>
+// WAVES waves a row, 4 / WAVES rows a workgroup of four.  HELD: the row's values and its weights
+// stay in registers, CHUNKS times eight a lane, all of them on their way at once; longer
+// rows are read twice.
+__device__ __forceinline__ double moved_sum(double v) {         // over the wave, in all lanes
+    auto add = [&](double o) { v += o; };
+    auto both = [&](auto f) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, v);
+        return __builtin_bit_cast(double, (uint64_t)f((uint32_t)(u >> 32)) << 32 | f((uint32_t)u));
+    };
+    add(both([](uint32_t x) { return moved<0xb1>(x); }));
+    add(both([](uint32_t x) { return moved<0x4e>(x); }));
+    add(both([](uint32_t x) { return moved<0x141>(x); }));
+    add(both([](uint32_t x) { return moved<0x140>(x); }));
+    add(both([](uint32_t x) { return (uint32_t)__builtin_amdgcn_ds_swizzle((int)x, 0x401f); }));     // lane ^ 16
+    add(both([](uint32_t x) { return (uint32_t)__shfl_xor((int)x, 32); }));
+    return v;
+}
+
+// a^-1/2 in float64: the hardware's estimate and one step of third order.
+__device__ __forceinline__ double inverse_root(double a) {
+    if (!(a > 0.0 && a < __builtin_inf())) return 1.0 / __builtin_sqrt(a);
+    const double y = __builtin_amdgcn_rsq(a);
+    const double e = __builtin_fma(-a * y, y, 1.0);
+    return __builtin_fma(y * e, __builtin_fma(e, 0.375, 0.5), y);
+}
+
+// Eight values as they lie in memory.
+template <bool BF16>
+struct Eight {
+    uint32_t d[BF16 ? 4 : 8];
+    __device__ __forceinline__ void load(const void* base, int64_t at, int have) {
+        if (have >= 8) {
+            const u32x4 v = *(const u32x4h*)((const uint8_t*)base + at * (BF16 ? 2 : 4));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[i] = v[i];
+            if (!BF16) {
+                const u32x4 w = *(const u32x4h*)((const uint8_t*)base + at * 4 + 16);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[(BF16 ? 0 : 4) + i] = w[i];
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < (BF16 ? 4 : 8); ++i) d[i] = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i >= have) continue;
+            if (BF16) d[i / 2] |= (uint32_t)((const uint16_t*)base)[at + i] << (16 * (i & 1));
+            else d[BF16 ? 0 : i] = ((const uint32_t*)base)[at + i];
+        }
+    }
+    __device__ __forceinline__ float operator[](int i) const {
+        if (!BF16) return __builtin_bit_cast(float, d[BF16 ? 0 : i]);
+        return __builtin_bit_cast(float, (i & 1) ? d[i / 2] & 0xffff0000u : d[i / 2] << 16);
+    }
+};
+
+template <bool BF16, bool WBF16, int WAVES, int CHUNKS, bool HELD>
 __global__ void __launch_bounds__(WAVES > 4 ? 64 * WAVES : kThreads) f8_norm_pack_kernel(F8NormArgs a) {
-    constexpr int kLanes = 64 * WAVES, kRows = WAVES > 4 ? 1 : 4 / WAVES;
+    constexpr int kLanes = 64 * WAVES, kRows = WAVES > 4 ? 1 : 4 / WAVES, kHeld = HELD ? CHUNKS : 1;
     __shared__ double part[kRows * WAVES];
     const int lane = (int)threadIdx.x % kLanes, in = (int)threadIdx.x / kLanes;
     const int64_t row = (int64_t)blockIdx.x * kRows + in;
@@ -134,37 +189,48 @@ __global__ void __launch_bounds__(WAVES > 4 ? 64 * WAVES : kThreads) f8_norm_pac
         const int64_t left = a.K - p * 8;
         return left < 0 || p >= pieces ? 0 : (int)(left < 8 ? left : 8);
     };
-    auto load_h = [&](int64_t p, float* h) {
+    Eight<BF16> h[kHeld], res[kHeld];
+    Eight<WBF16> weight[kHeld];
+    auto load = [&](int c, int64_t p) {
         const int have = have_of(p);
-        load_row8<BF16>(a.x, row * a.ldx + p * 8, have, h, 0.f);
-        if (a.residual) {
-            float r[8];
-            load_row8<BF16>(a.residual, row * a.ldr + p * 8, have, r, 0.f);
+        h[c].load(a.x, row * a.ldx + p * 8, have);
+        if (a.residual) res[c].load(a.residual, row * a.ldr + p * 8, have);
+    };
+    auto add = [&](int c) {
+        if (!a.residual) return;
+        if (BF16) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                h[i] += r[i];
-                if (BF16) h[i] = bf16_bits_to_f32(f32_to_bf16_rne(h[i]));
-            }
+            for (int i = 0; i < 4; ++i)
+                h[c].d[i] = bf16_pair(h[c][2 * i] + res[c][2 * i], h[c][2 * i + 1] + res[c][2 * i + 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[c].d[BF16 ? 0 : i] = __builtin_bit_cast(uint32_t, h[c][i] + res[c][i]);
         }
     };
-    float h[HELD ? CHUNKS : 1][8];
     double sum = 0.0;
-    auto square = [&](const float* v) {
+    auto square = [&](int c) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum = __builtin_fma((double)v[i], (double)v[i], sum);
+        for (int i = 0; i < 8; ++i) sum = __builtin_fma((double)h[c][i], (double)h[c][i], sum);
     };
     if (HELD) {
 #pragma unroll
-        for (int c = 0; c < CHUNKS; ++c) load_h(lane + c * kLanes, h[c]);
+        for (int c = 0; c < kHeld; ++c) load(c, lane + c * kLanes);
 #pragma unroll
-        for (int c = 0; c < CHUNKS; ++c) square(h[c]);
+        for (int c = 0; c < kHeld; ++c)
+            weight[c].load(a.weight, (int64_t)(lane + c * kLanes) * 8, have_of(lane + c * kLanes));
+#pragma unroll
+        for (int c = 0; c < kHeld; ++c) {
+            add(c);
+            square(c);
+        }
     } else {
         for (int64_t p = lane; p < pieces; p += kLanes) {
-            load_h(p, h[0]);
-            square(h[0]);
+            load(0, p);
+            add(0);
+            square(0);
         }
     }
-    sum = wave_sum(sum);
+    sum = moved_sum(sum);
     if (WAVES > 1) {
         if (lane % 64 == 0) part[in * WAVES + lane / 64] = sum;
         __syncthreads();
@@ -172,19 +238,20 @@ __global__ void __launch_bounds__(WAVES > 4 ? 64 * WAVES : kThreads) f8_norm_pac
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) sum += part[in * WAVES + w];
     }
-    const float f = (float)(1.0 / __builtin_sqrt(sum / (double)a.K + a.eps));
-    auto finish = [&](int64_t p, const float* v) {
-        const int have = have_of(p);
+    const float f = (float)inverse_root(sum / (double)a.K + a.eps);
+    auto finish = [&](int c, int64_t p) {
         if (p >= pieces) return;                // all sixteen lanes of a block alike
-        float w[8], y[8];
-        if (a.w_dtype == TQ_BF16) load_row8<true>(a.weight, p * 8, have, w, 0.f);
-        else load_row8<false>(a.weight, p * 8, have, w, 0.f);
+        const int have = have_of(p);
+        float y[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = v[i] * f * w[i];
+        for (int i = 0; i < 8; ++i) y[i] = i < have ? h[c][i] * f * weight[c][i] : 0.f;
+        if (a.h) {
+            float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = i < have ? y[i] : 0.f;   // a factor that is not finite
-        if (a.h) store_row8<BF16>(a.h, row * a.ldh + p * 8, have, v);
-        if (a.y) store_row8<BF16>(a.y, row * a.ldy + p * 8, have, y);
+            for (int i = 0; i < 8; ++i) v[i] = h[c][i];
+            store_row8<BF16, true>(a.h, row * a.ldh + p * 8, have, v);
+        }
+        if (a.y) store_row8<BF16, true>(a.y, row * a.ldy + p * 8, have, y);
         const uint32_t s = f8_scale_bits(over_group<16>(largest8(y), larger));
         *(u32x2*)(a.codes + (row * nb * 16 + p) * 8) = f8_encode8(y, s);
         if (p % 16 == 0) {
@@ -194,30 +261,40 @@ __global__ void __launch_bounds__(WAVES > 4 ? 64 * WAVES : kThreads) f8_norm_pac
     };
     if (HELD) {
 #pragma unroll
-        for (int c = 0; c < CHUNKS; ++c) finish(lane + c * kLanes, h[c]);
+        for (int c = 0; c < kHeld; ++c) finish(c, lane + c * kLanes);
     } else {
         for (int64_t p = lane; p < pieces; p += kLanes) {
-            load_h(p, h[0]);
-            finish(p, h[0]);
+            load(0, p);
+            weight[0].load(a.weight, p * 8, have_of(p));
+            add(0);
+            finish(0, p);
         }
     }
 }
 
-template <bool BF16, int WAVES, int CHUNKS, bool HELD>
+template <bool BF16, bool WBF16, int WAVES, int CHUNKS, bool HELD>
 hipError_t norm(const F8NormArgs& a, hipStream_t s) {
     constexpr int kRows = WAVES > 4 ? 1 : 4 / WAVES, kAll = WAVES > 4 ? 64 * WAVES : kThreads;
     const int64_t blocks = (a.M + kRows - 1) / kRows;
     if (!grid_fits(blocks, kAll)) return hipErrorInvalidConfiguration;
-    f8_norm_pack_kernel<BF16, WAVES, CHUNKS, HELD><<<(unsigned)blocks, kAll, 0, s>>>(a);
+    f8_norm_pack_kernel<BF16, WBF16, WAVES, CHUNKS, HELD><<<(unsigned)blocks, kAll, 0, s>>>(a);
     return hipGetLastError();
 }
 
-template <bool BF16>
+template <bool BF16, bool WBF16>
 hipError_t norm_by_size(const F8NormArgs& a, hipStream_t s) {
     const int64_t pieces = (a.K + kF8Block - 1) / kF8Block * 16;
-    if (pieces <= 256) return norm<BF16, 1, 4, true>(a, s);
-    if (pieces <= 1024) return norm<BF16, 4, 4, true>(a, s);
-    return norm<BF16, 8, 1, false>(a, s);
+    // A lane for each piece as far as a workgroup goes (us, bf16 with residual and both outputs, by
+    // pieces a lane: 8192 x 2048 four 36.4, one 29.9; 4096 x 4096 four 34.3, two 33.4, one 30.5;
+    // 2048 x 8192 four 36.6, two 33.5, one 33.0; 1 x 8192 four 4.6, one 3.6; all with
+    // stores that stay in the caches, which cost 2 us of 30 at 4096 x 4096).
+    if (pieces <= 64) return norm<BF16, WBF16, 1, 1, true>(a, s);
+    if (pieces <= 128) return norm<BF16, WBF16, 2, 1, true>(a, s);
+    if (pieces <= 256) return norm<BF16, WBF16, 4, 1, true>(a, s);
+    if (pieces <= 512) return norm<BF16, WBF16, 8, 1, true>(a, s);
+    if (pieces <= 1024) return norm<BF16, WBF16, 16, 1, true>(a, s);
+    if (pieces <= 2048) return norm<BF16, WBF16, 16, 2, true>(a, s);
+    return norm<BF16, WBF16, 16, 1, false>(a, s);
 }
 
 }  // namespace
@@ -262,7 +339,8 @@ hipError_t launch_f8_unpack(const uint8_t* codes, const float* scales, int64_t r
 
 hipError_t launch_f8_norm_pack(const F8NormArgs& a, hipStream_t s) {
     if (a.M == 0 || a.K == 0) return hipSuccess;
-    return a.x_dtype == TQ_BF16 ? norm_by_size<true>(a, s) : norm_by_size<false>(a, s);
+    if (a.x_dtype == TQ_BF16) return a.w_dtype == TQ_BF16 ? norm_by_size<true, true>(a, s) : norm_by_size<true, false>(a, s);
+    return a.w_dtype == TQ_BF16 ? norm_by_size<false, true>(a, s) : norm_by_size<false, false>(a, s);
 }
 
 }  // namespace dmm

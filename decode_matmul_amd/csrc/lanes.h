@@ -57,19 +57,22 @@ __device__ __forceinline__ double wave_sum(double v) {
 }
 
 // Eight values of a row from element `at` on (any alignment of their type), `have` of
-// them there; the others are `fill`.
-template <bool BF16>
+// them there; the others are `fill`.  STREAM: what is read once, past the caches.
+template <bool BF16, bool STREAM = false>
 __device__ __forceinline__ void load_row8(const void* base, int64_t at, int have, float* v, float fill) {
     if (have >= 8) {
         if (BF16) {
-            const u32x4 d = *(const u32x4h*)((const uint16_t*)base + at);
+            const u32x4h* const p = (const u32x4h*)((const uint16_t*)base + at);
+            const u32x4 d = STREAM ? __builtin_nontemporal_load(p) : *p;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 v[2 * i] = __builtin_bit_cast(float, d[i] << 16);
                 v[2 * i + 1] = __builtin_bit_cast(float, d[i] & 0xffff0000u);
             }
         } else {
-            const f32x4 a = *(const f32x4a*)((const float*)base + at), b = *(const f32x4a*)((const float*)base + at + 4);
+            const f32x4a* const p = (const f32x4a*)((const float*)base + at);
+            const f32x4a* const q = (const f32x4a*)((const float*)base + at + 4);
+            const f32x4 a = STREAM ? __builtin_nontemporal_load(p) : *p, b = STREAM ? __builtin_nontemporal_load(q) : *q;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 v[i] = a[i];
@@ -86,8 +89,9 @@ __device__ __forceinline__ void load_row8(const void* base, int64_t at, int have
     }
 }
 
-// The first `have` of eight values to a row, from element `at` on; bf16 rounds to nearest, ties to even.
-template <bool BF16>
+// The first `have` of eight values to a row, from element `at` on; bf16 rounds to nearest, ties to
+// even.  STREAM: what is not read soon, past the caches.
+template <bool BF16, bool STREAM = false>
 __device__ __forceinline__ void store_row8(void* base, int64_t at, int have, const float* v) {
     if (BF16) {
         uint16_t* const d = (uint16_t*)base + at;
@@ -95,7 +99,8 @@ __device__ __forceinline__ void store_row8(void* base, int64_t at, int have, con
             u32x4 w;
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
-            *(u32x4h*)d = w;
+            if (STREAM) __builtin_nontemporal_store(w, (u32x4h*)d);
+            else *(u32x4h*)d = w;
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -104,8 +109,14 @@ __device__ __forceinline__ void store_row8(void* base, int64_t at, int have, con
     } else {
         float* const d = (float*)base + at;
         if (have >= 8) {
-            *(f32x4a*)d = (f32x4){v[0], v[1], v[2], v[3]};
-            *(f32x4a*)(d + 4) = (f32x4){v[4], v[5], v[6], v[7]};
+            const f32x4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
+            if (STREAM) {
+                __builtin_nontemporal_store(lo, (f32x4a*)d);
+                __builtin_nontemporal_store(hi, (f32x4a*)(d + 4));
+            } else {
+                *(f32x4a*)d = lo;
+                *(f32x4a*)(d + 4) = hi;
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)

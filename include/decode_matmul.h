@@ -722,7 +722,7 @@ int f8_unpack(const uint8_t* codes, const float* scales, int64_t rows, int64_t K
  *            TQ_DATA_RANGE if a y is not finite.
  *
  * Matrices are aligned to their element.  M = 0 or K = 0 is a no-op.  K is below 2^23,
- * M below 2^23 (TQ_ERR_SHAPE).
+ * M below 2^22 (TQ_ERR_SHAPE).
  */
 int f8_norm_pack(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx, const void* residual,
                  int64_t ldr, const void* weight, int32_t w_dtype, double eps, void* h_out, int64_t ldh,

@@ -159,7 +159,7 @@ def test_f8_norm_pack_refusals():
     ok = [FAKE, 1, 4, 64, 64, FAKE, 64, FAKE, 1, 1e-6, FAKE, 64, FAKE, 64, FAKE, FAKE, None, None]
     refused(lib.f8_norm_pack, ok, (
         (0, None, NULL), (7, None, NULL), (14, None, NULL), (15, None, NULL), (1, 2, DTYPE), (8, 2, DTYPE),
-        (2, -1, SHAPE), (3, -1, SHAPE), (3, 1 << 23, SHAPE), (2, 1 << 23, SHAPE), (4, 63, SHAPE), (6, 63, SHAPE),
+        (2, -1, SHAPE), (3, -1, SHAPE), (3, 1 << 23, SHAPE), (2, 1 << 22, SHAPE), (4, 63, SHAPE), (6, 63, SHAPE),
         (11, 63, SHAPE), (13, 63, SHAPE), (9, -1e-9, SHAPE), (9, float("nan"), SHAPE), (0, ODD, ALIGN), (5, ODD, ALIGN),
         (7, ODD, ALIGN), (10, ODD, ALIGN), (12, ODD, ALIGN), (14, HALF, ALIGN), (15, EVEN, ALIGN), (16, ODD, ALIGN),
         (2, 0, 0), (3, 0, 0)))

@@ -152,7 +152,7 @@ def test_unpack_of_every_code_and_padding(dmm):
 # ---------------------------------------------------------------------- norm
 
 NORM = [(1, 1), (1, 4096), (3, 7), (5, 100), (2, 128), (33, 500), (70, 1000), (9, 2048), (4, 2056), (17, 4096),
-        (3, 5000), (6, 8192), (2, 8200), (3, 20001), (1, 70000)]
+        (3, 5000), (6, 8192), (2, 8200), (3, 20001), (1, 70000), (5, 640), (2, 12000)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
