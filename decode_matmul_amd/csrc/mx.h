@@ -96,10 +96,12 @@ __device__ __forceinline__ int64_t lane_offset(int64_t o) {
     return o;
 }
 
-// 16 bytes a lane from global memory to LDS: lane l's land at lds + 16 l.
+// 16 bytes a lane from global memory to LDS: lane l's land at lds + 16 l.  STREAM: what is read
+// once, past the caches.
+template <bool STREAM = false>
 __device__ __forceinline__ void load_lds16(GlobalBytes g, void* lds) {
     __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)g,
-                                     (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+                                     (__attribute__((address_space(3))) void*)lds, 16, 0, STREAM ? 2 : 0);
 }
 
 // Which of a 128-byte row's eight slots chunk 0 takes.  A 16-byte LDS read serves
