@@ -19,6 +19,7 @@
 // the other.  Rows go from global memory straight to LDS in whole lines of 128 bytes, a block
 // each, a slab ahead; pieces change places within their rows so that a fragment read
 // hits all banks (swizzle).  The products f of FU blocks come by way of registers.
+#include <stdlib.h>
 #include <type_traits>
 
 #include "experts.h"
@@ -40,9 +41,9 @@ struct Floats {
     typedef float T __attribute__((ext_vector_type(N)));
 };
 
-// BM x BN tile of WM x WN waves; KD blocks a slab.  KG groups of WM x WN waves take every
+// EXACT: y is fp32, otherwise bf16.  BM x BN tile of WM x WN waves; KD blocks a slab.  KG groups of WM x WN waves take every
 // KG-th slab each, and the first adds up the sums.
-template <bool EXACT, int BM, int BN, int WM, int WN, int KD, int KG, bool GROUPED>
+template <bool EXACT, int BM, int BN, int WM, int WN, int KD, int KG, int NS, bool GROUPED>
 __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulArgs a) {
     constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;                 // of a group
     constexpr int kXUnit = BM * kRow, kWUnit = BN * kRow;
@@ -50,19 +51,38 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
     constexpr int MT = BM / WM / 16, NT = BN / WN / 16;                     // tiles of a wave
     constexpr int kXLoads = kXBytes / 1024 / kWaves, kWLoads = kWBytes / 1024 / kWaves;
     constexpr int NB = BN > 128 ? BN / 128 : 1;                             // scales of W along n
-    constexpr int FU = KG > 1 || KD > 4 ? KD : 4, kFSlabs = FU / KD;        // blocks, slabs of a fetch of scales
+    constexpr int kFSlabs = KG > 1 ? 1 : NS, FU = kFSlabs * KD;  // slabs, blocks of a fetch of scales
+    constexpr int kLoads = kXLoads + kWLoads;
+    // Two large stages: what the first half of a slab has read is overwritten at its middle
+    constexpr bool kEarly = NS == 2 && KD == 1 && KG == 1 && BM == 256 && WM == 2 && kWaves == 8;
     static_assert(kXLoads * 1024 * kWaves == kXBytes && kWLoads * 1024 * kWaves == kWBytes, "whole loads");
     static_assert(BM * NB <= kThreads, "a thread for each row's scales");
     static_assert(BN / WN <= 128 || NB == 1, "a wave has one scale of W");
-    static_assert(FU % KD == 0 && (kFSlabs == 1 || kFSlabs >= 2), "whole slabs");
-    __shared__ __attribute__((aligned(1024))) uint8_t stages0[KG * kStage];
-    __shared__ __attribute__((aligned(1024))) uint8_t stages1[KG * kStage];
-    __shared__ float factors[KG][2][NB][FU][BM];
+    static_assert(NS == 2 || (KG == 1 && NS <= 4), "stages");
+    // A stage: x's rows by halves (below), then W's.
+    __shared__ __attribute__((aligned(1024))) uint8_t stages0[kEarly ? kXBytes / 2 : KG * kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t stages1[kEarly ? kXBytes / 2 : KG * kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t stages2[NS > 2 ? kStage : kEarly ? kXBytes / 2 : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t stages3[NS > 3 ? kStage : kEarly ? kXBytes / 2 : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t rows0[kEarly ? kWBytes : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t rows1[kEarly ? kWBytes : 16];
+    // (one index: the compiler sees through a few address computations only, and waits for all loads
+    // to LDS before a read that may be of what they write)
+    __shared__ float factors[KG * 2 * NB * FU * BM];
 
     const int kg = KG == 1 ? 0 : readfirstlane((int)threadIdx.x / kThreads);
     const int tid = (int)threadIdx.x - kg * kThreads, lane = tid & 63, wave = readfirstlane(tid >> 6);
-    uint8_t* const stage0 = stages0 + kg * kStage;
-    uint8_t* const stage1 = stages1 + kg * kStage;
+    uint8_t* const stage0 = stages0 + (KG > 1 ? kg * kStage : 0);
+    uint8_t* const stage1 = stages1 + (KG > 1 ? kg * kStage : 0);
+    struct Stage {
+        uint8_t *x0, *x1, *w;                   // of unit 0
+    };
+    const Stage stage[4] = {
+        {stage0, kEarly ? stages2 : stage0 + kXUnit / 2, kEarly ? rows0 : stage0 + kXBytes},
+        {stage1, kEarly ? stages3 : stage1 + kXUnit / 2, kEarly ? rows1 : stage1 + kXBytes},
+        {stages2, stages2 + kXUnit / 2, stages2 + kXBytes},
+        {stages3, stages3 + kXUnit / 2, stages3 + kXBytes},
+    };
     const int r = lane & 15, g = lane >> 4;
     const int wm = wave / WN, wn = wave % WN;
     const int64_t nb = (a.K + kF8Block - 1) / kF8Block;
@@ -92,7 +112,12 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
     // Loads to LDS fill 1024 bytes at a time: eight rows, lane l the piece whose slot is l % 8
     // of row l / 8.  Load j of wave w is row group w + j kWaves of the slab's, unit by unit.
     const int sub = lane >> 3;
-    auto x_group = [&](int j) { return (wave + j * kWaves) % (BM / 8); };
+    // x's rows lie by halves: first those of the first half of each wave's tiles.
+    constexpr int kHalfRows = BM / WM / 2;
+    auto x_group = [&](int j) {                 // the row group's first row of the tile, over 8
+        const int at = (wave + j * kWaves) % (BM / 8) * 8, half = at / (BM / 2), in = at % (BM / 2);
+        return (in / kHalfRows * (BM / WM) + half * kHalfRows + in % kHalfRows) / 8;
+    };
     auto x_unit = [&](int j) { return (wave + j * kWaves) / (BM / 8); };
     auto w_group = [&](int j) { return (wave + j * kWaves) % (BN / 8); };
     auto w_unit = [&](int j) { return (wave + j * kWaves) / (BN / 8); };
@@ -116,17 +141,18 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
     // Thread (row, n block) fetches FU scales of both and stages their products.
     typedef typename Floats<FU>::T Scales;
     typedef Scales ScalesAt __attribute__((aligned(4)));
-    const int frow = tid % BM, fblk = tid / BM;
+    const int frow = tid % BM, fblk = BM % 64 == 0 ? readfirstlane(tid / BM) : tid / BM;
     const bool stages_f = fblk < NB;
     const int64_t n_blocks = (a.N + 127) / 128, nblk = p.n0 / 128 + fblk;
     const float* const sx = a.x_scales + ((GROUPED ? 0 : p.m0) + (stages_f ? x_row(frow) : 0)) * nb;
     const float* const sw = a.scales + (p.expert * n_blocks + (stages_f && nblk < n_blocks ? nblk : n_blocks - 1)) * nb;
-    Scales fx, fw;
-    auto fetch_factors = [&](int64_t b) {       // of blocks b .. b + FU - 1, as far as there are any
+    Scales fx, fw;                              // fw: one for a wave, in scalar registers
+    auto fetch_factors = [&](int64_t b, bool whole) {   // of blocks b .. b + FU - 1, as far as there are any
         if (!stages_f) return;
-        if (b + FU <= nb) {
+        if (whole || b + FU <= nb) {
             fx = *(const ScalesAt*)(sx + b);
-            fw = *(const ScalesAt*)(sw + b);
+            if (BM % 64 == 0) fw = *(const __attribute__((address_space(4))) ScalesAt*)(sw + b);
+            else fw = *(const ScalesAt*)(sw + b);
         } else {
 #pragma unroll
             for (int u = 0; u < FU; ++u) {
@@ -138,7 +164,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
     auto store_factors = [&](int buf) {
         if (!stages_f) return;
 #pragma unroll
-        for (int u = 0; u < FU; ++u) factors[kg][buf][fblk][u][frow] = fx[u] * fw[u];
+        for (int u = 0; u < FU; ++u) factors[(((kg * 2 + buf) * NB + fblk) * FU + u) * BM + frow] = fx[u] * fw[u];
     };
 
     f32x4 acc[NT][MT];
@@ -147,17 +173,24 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
 #pragma unroll
         for (int j = 0; j < MT; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
 
-    auto start = [&](uint8_t* st, int64_t t) {  // slab t, a whole one
+    enum { kAll, kFirst, kSecond };             // of a slab's rows: the first half are W's and x's first half
+    auto load_x = [&](const Stage& st, int j, GlobalBytes from) {
+        const int at = (wave + j * kWaves) * 1024;
+        if (kEarly) load_lds16(from, 2 * j < kXLoads ? st.x0 + at : st.x1 + (at - kXBytes / 2));
+        else load_lds16(from, st.x0 + at);
+    };
+    auto start = [&](const Stage& st, int64_t t, int which) {   // slab t, a whole one
         const GlobalBytes xb = scalar_base(xbase + (t * KG + kg) * (KD * kRow));
         const GlobalBytes wb = scalar_base(wbase + (t * KG + kg) * (KD * kRow));
 #pragma unroll
         for (int j = 0; j < kXLoads; ++j) {
-            if (BM == 32 && x_group(j) * 8 >= m_rows) continue;     // rows no token reads
-            load_lds16(xb + lane_offset(xsrc[j]), st + (wave + j * kWaves) * 1024);
+            if (which != kAll && (2 * j >= kXLoads) != (which == kSecond)) continue;
+            if (BM == 32 && NS == 2 && x_group(j) * 8 >= m_rows) continue;      // rows no token reads (and no count of loads)
+            load_x(st, j, xb + lane_offset(xsrc[j]));
         }
+        if (which == kSecond) return;
 #pragma unroll
-        for (int j = 0; j < kWLoads; ++j)
-            load_lds16(wb + lane_offset(wsrc[j]), st + kXBytes + (wave + j * kWaves) * 1024);
+        for (int j = 0; j < kWLoads; ++j) load_lds16(wb + lane_offset(wsrc[j]), st.w + (wave + j * kWaves) * 1024);
     };
 
     // ---- fragments of a unit: the wave's rows of W, held for all of its tokens, and one
@@ -186,15 +219,18 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
             part[1] = v[1];
         }
     };
-    auto read_w = [&](const uint8_t* st, int k, int i, bool cut) {
+    auto read_w = [&](const Stage& st, int k, int i, bool cut) {
         u32x4 v[2];
-        read_raw(st + kXBytes + k * kWUnit + (wn * (BN / WN) + 16 * i) * kRow, v, cut);
+        read_raw(st.w + k * kWUnit + (wn * (BN / WN) + 16 * i) * kRow, v, cut);
         as_parts(v, wf[i]);
     };
     const int fn = NB > 1 ? wn * (BN / WN) / 128 : 0;
-    auto read_x = [&](const uint8_t* st, int buf, int k, int u, int j, bool cut) {
-        read_raw(st + k * kXUnit + (wm * (BM / WM) + 16 * j) * kRow, xf[j & 1], cut);
-        f[j & 1] = factors[kg][buf][fn][u][wm * (BM / WM) + 16 * j + r];
+    auto read_x = [&](const Stage& st, int buf, int k, int u, int j, bool cut) {
+        const int row = wm * kHalfRows + 16 * (j % (MT / 2));
+        read_raw((2 * j < MT ? st.x0 : st.x1) + k * kXUnit + row * kRow, xf[j & 1], cut);
+        // one address computation (see factors)
+        const uint32_t at = lane_offset((uint32_t)((((kg * 2 + buf) * NB + fn) * FU + u) * BM + wm * (BM / WM) + 16 * j + r));
+        f[j & 1] = factors[at];
     };
     auto multiply = [&](int j, auto next) {
         Part x[kParts];
@@ -226,20 +262,27 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
 
     // Slab t in `cur`: its first fragments are in registers.  Before the last tile every wave
     // has read `cur`, and slab t + 1 has landed in `other`: while the last tile
-    // multiplies, slab t + 2 starts into `cur` and the first fragments of slab t + 1 are read.
+    // multiplies, slab t + NS starts into `cur` and the first fragments of slab t + 1 are read.
     // The products f of slab t are in factors' half (t / kFSlabs) % 2, from block t % kFSlabs KD on.
+    // MAIN: all of these slabs, and the next kFSlabs, are there, and the slab's place among kFSlabs is PHASE; without
+    // branches the compiler can count the loads behind a fetch of scales and need not wait for them.
     const int64_t full = a.K / kF8Block / KD / KG;
     auto block_of = [&](int64_t t) { return (t * KG + kg) * KD; };
-    auto slab = [&](uint8_t* cur, uint8_t* other, int64_t t) {
-        const int buf = (int)(t / kFSlabs) & 1, u0 = (int)(t % kFSlabs) * KD;
-        const int buf1 = (int)((t + 1) / kFSlabs) & 1, u1 = (int)((t + 1) % kFSlabs) * KD;
-        if (u0 == 0) fetch_factors(block_of(t + kFSlabs));
+    auto slab = [&](const Stage& cur, const Stage& other, int64_t t, auto main, auto phase) {
+        constexpr bool MAIN = decltype(main)::value;
+        const int in = MAIN ? decltype(phase)::value : (int)(t % kFSlabs), next = in + 1 == kFSlabs ? 0 : in + 1;
+        const int buf = (int)(t / kFSlabs) & 1, u0 = in * KD, u1 = next * KD, buf1 = next == 0 ? buf ^ 1 : buf;
+        if (in == 0) fetch_factors(block_of(t + kFSlabs), MAIN);
 #pragma unroll
         for (int k = 0; k < KD; ++k) {
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
                 if (j + 1 < MT) {
                     read_x(cur, buf, k, u0 + k, j + 1, false);
+                    if (kEarly && j == MT / 2 - 1 && (MAIN || t + NS < full)) {
+                        lds_barrier();
+                        start(cur, t + NS, kFirst);
+                    }
                     multiply(j, nothing);
                 } else if (k + 1 < KD) {
                     read_x(cur, buf, k + 1, u0 + k + 1, 0, false);
@@ -247,11 +290,12 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
                 }
             }
         }
-        if ((t + 1) % kFSlabs == 0) store_factors(buf1);
-        wait_loads<0>();
+        if (next == 0) store_factors(buf1);
+        if (MAIN || t + NS - (kEarly ? 0 : 1) < full) wait_loads<(NS - 2) * kLoads + (kEarly ? kLoads - kXLoads / 2 : 0)>();
+        else wait_loads<0>();
         lds_barrier();
-        if (t + 2 < full) start(cur, t + 2);
-        if (t + 1 < full) {
+        if (MAIN || t + NS < full) start(cur, t + NS, kEarly ? kSecond : kAll);
+        if (MAIN || t + 1 < full) {
             read_x(other, buf1, 0, u1, 0, false);
             multiply(MT - 1, [&](int i) { read_w(other, 0, i, false); });
         } else {
@@ -259,20 +303,40 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
         }
     };
     static_assert(MT % 2 == 0, "the last tile's fragments and the next unit's first take turns");
+    typedef std::integral_constant<int, 0> P0;
+    typedef std::integral_constant<int, 1> P1;
+    typedef std::integral_constant<int, 2> P2;
+    typedef std::integral_constant<int, 3> P3;
+    const std::true_type always;
+    const std::false_type maybe;
 
-    fetch_factors(block_of(0));
-    if (full > 0) start(stage0, 0);
+    fetch_factors(block_of(0), false);
+    if (full > 0) start(stage[0], 0, kAll);
     store_factors(0);
     if (full > 0) {
         wait_loads<0>();
         lds_barrier();
-        if (full > 1) start(stage1, 1);
-        read_x(stage0, 0, 0, 0, 0, false);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) read_w(stage0, 0, i, false);
-        for (int64_t t = 0; t < full; t += 2) {
-            slab(stage0, stage1, t);
-            if (t + 1 < full) slab(stage1, stage0, t + 1);
+        for (int i = 1; i < NS; ++i)
+            if (i < full) start(stage[i], i, kAll);
+        read_x(stage[0], 0, 0, 0, 0, false);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) read_w(stage[0], 0, i, false);
+        int64_t t = 0;
+        if constexpr (KG == 1) {
+            static_assert(KG > 1 || kFSlabs >= NS, "what starts is there");
+            for (; t + 2 * kFSlabs <= full; t += kFSlabs) {
+                slab(stage[0], stage[1], t, always, P0());
+                slab(stage[1], stage[NS > 2 ? 2 : 0], t + 1, always, P1());
+                if constexpr (kFSlabs > 2) slab(stage[NS > 2 ? 2 : 0], stage[NS > 3 ? 3 : NS > 2 ? 0 : 1], t + 2, always, P2());
+                if constexpr (kFSlabs > 3) slab(stage[NS > 3 ? 3 : 1], stage[0], t + 3, always, P3());
+            }
+        }
+        for (; t < full; t += NS) {
+            slab(stage[0], stage[1], t, maybe, P0());
+            if (t + 1 < full) slab(stage[1], stage[NS > 2 ? 2 : 0], t + 1, maybe, P0());
+            if (NS > 2 && t + 2 < full) slab(stage[2], stage[NS > 3 ? 3 : 0], t + 2, maybe, P0());
+            if (NS > 3 && t + 3 < full) slab(stage[3], stage[0], t + 3, maybe, P0());
         }
     }
     // blocks that are left, the last one maybe cut: up to KD for each group
@@ -284,12 +348,11 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
         auto unit_of = [&](int u) { return first + u < nb ? first + u : nb - 1; };
 #pragma unroll
         for (int j = 0; j < kXLoads; ++j)
-            load_lds16((GlobalBytes)xbase + lane_offset(xsrc[j]) + (unit_of(x_unit(j)) - x_unit(j)) * kRow,
-                       stage0 + (wave + j * kWaves) * 1024);
+            load_x(stage[0], j, (GlobalBytes)xbase + lane_offset(xsrc[j]) + (unit_of(x_unit(j)) - x_unit(j)) * kRow);
 #pragma unroll
         for (int j = 0; j < kWLoads; ++j)
             load_lds16((GlobalBytes)wbase + lane_offset(wsrc[j]) + (unit_of(w_unit(j)) - w_unit(j)) * kRow,
-                       stage0 + kXBytes + (wave + j * kWaves) * 1024);
+                       stage[0].w + (wave + j * kWaves) * 1024);
         wait_loads<0>();
         lds_barrier();
         const int buf = (int)(full / kFSlabs) & 1, u0 = (int)(full % kFSlabs) * KD;
@@ -297,10 +360,10 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
         for (int k = 0; k < rest; ++k) {
             kept = a.K - (first + k) * kF8Block < kF8Block ? (int)(a.K - (first + k) * kF8Block) : kF8Block;
 #pragma unroll
-            for (int i = 0; i < NT; ++i) read_w(stage0, k, i, true);
+            for (int i = 0; i < NT; ++i) read_w(stage[0], k, i, true);
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
-                read_x(stage0, buf, k, u0 + k, j, true);
+                read_x(stage[0], buf, k, u0 + k, j, true);
                 multiply(j, nothing);
             }
         }
@@ -353,7 +416,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
         constexpr int kCols = NT * 16, kPitch = kCols * (int)sizeof(T) + 16, kEach = 16 / (int)sizeof(T);
         constexpr int kLanes = kCols / kEach, kAtOnce = 64 / kLanes < 16 ? 64 / kLanes : 16;
         constexpr int kHalf = (kWaves + 1) / 2; // waves a stage
-        static_assert(kHalf * 16 * kPitch <= kStage, "the stages hold the waves' rows");
+        static_assert(kHalf * 16 * kPitch <= (kEarly ? kXBytes / 2 : kStage), "the stages hold the waves' rows");
         uint8_t* const mine = (wave < kHalf ? stage0 : stage1) + wave % kHalf * (16 * kPitch);
         const int c = lane % kLanes, col = wn * (BN / WN) + c * kEach;
 #pragma unroll
@@ -377,11 +440,10 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
             asm volatile("" ::: "memory");
         }
     };
-    const bool f32 = a.y_dtype == TQ_F32;
+    constexpr bool f32 = EXACT;
     if (a.N % (f32 ? 4 : 8) == 0 && ((uintptr_t)a.y & 15) == 0) {
         lds_barrier();                          // every wave is done with the stages
-        if (f32) write_rows(float());
-        else write_rows((uint16_t)0);
+        write_rows(typename std::conditional<f32, float, uint16_t>::type());
         return;
     }
 #pragma unroll
@@ -403,14 +465,14 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
     }
 }
 
-template <bool EXACT, int BM, int BN, int WM, int WN, int KD, int KG, bool GROUPED>
+template <bool EXACT, int BM, int BN, int WM, int WN, int KD, int KG, int NS, bool GROUPED>
 hipError_t launch(const F8MatmulArgs& a, hipStream_t s) {
     constexpr int kThreads = 64 * WM * WN * KG;
     const int64_t nt = (a.N + BN - 1) / BN;
     int64_t blocks = (a.M + BM - 1) / BM * nt;
     if (GROUPED) blocks = grouped_blocks<BM>(a, nt);
     if (!grid_fits(blocks, kThreads)) return hipErrorInvalidConfiguration;
-    f8_gemm_kernel<EXACT, BM, BN, WM, WN, KD, KG, GROUPED><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+    f8_gemm_kernel<EXACT, BM, BN, WM, WN, KD, KG, NS, GROUPED><<<(unsigned)blocks, kThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -418,19 +480,47 @@ hipError_t launch(const F8MatmulArgs& a, hipStream_t s) {
 
 hipError_t launch_f8_gemm(const F8MatmulArgs& a, hipStream_t s) {
     const bool exact = a.y_dtype == TQ_F32;
+    static const char* v = getenv("GEMMV");
+    const int V = v ? atoi(v) : 0;
     if (a.n_experts > 0) {
+        if (!exact) {
+            if (V == 1) return launch<false, 32, 128, 1, 4, 2, 1, 2, true>(a, s);
+            if (V == 2) return launch<false, 32, 128, 1, 4, 1, 1, 4, true>(a, s);
+            if (V == 3) return launch<false, 64, 128, 1, 4, 1, 1, 3, true>(a, s);
+            if (V == 4) return launch<false, 64, 256, 1, 4, 1, 1, 3, true>(a, s);
+            if (V == 5) return launch<false, 128, 256, 2, 4, 1, 1, 2, true>(a, s);
+            if (V == 6) return launch<false, 128, 256, 2, 4, 1, 1, 3, true>(a, s);
+            if (V == 7) return launch<false, 128, 128, 2, 2, 1, 1, 2, true>(a, s);
+            if (V == 8) return launch<false, 128, 128, 2, 2, 1, 1, 4, true>(a, s);
+            if (V == 9) return launch<false, 64, 256, 1, 4, 1, 1, 2, true>(a, s);
+            if (V == 10) return launch<false, 256, 256, 2, 4, 1, 1, 2, true>(a, s);
+            if (V == 11) return launch<false, 32, 256, 1, 4, 1, 1, 4, true>(a, s);
+        }
         if (a.M * a.top_k < 40 * (int64_t)a.n_experts)
-            return exact ? launch<true, 32, 128, 1, 4, 2, 1, true>(a, s) : launch<false, 32, 128, 1, 4, 2, 1, true>(a, s);
-        return exact ? launch<true, 128, 128, 2, 2, 1, 1, true>(a, s) : launch<false, 128, 256, 2, 4, 1, 1, true>(a, s);
+            return exact ? launch<true, 32, 128, 1, 4, 2, 1, 2, true>(a, s) : launch<false, 32, 128, 1, 4, 2, 1, 2, true>(a, s);
+        return exact ? launch<true, 128, 128, 2, 2, 1, 1, 2, true>(a, s) : launch<false, 128, 256, 2, 4, 1, 1, 2, true>(a, s);
     }
     const int64_t cus = compute_unit_count();
+    if (!exact) {
+        if (V == 1) return launch<false, 32, 32, 1, 1, 2, 4, 2, false>(a, s);
+        if (V == 2) return launch<false, 64, 64, 2, 2, 2, 1, 2, false>(a, s);
+        if (V == 3) return launch<false, 64, 64, 2, 2, 2, 1, 4, false>(a, s);
+        if (V == 4) return launch<false, 64, 64, 2, 2, 1, 1, 4, false>(a, s);
+        if (V == 5) return launch<false, 128, 128, 2, 2, 1, 1, 2, false>(a, s);
+        if (V == 6) return launch<false, 128, 128, 2, 2, 1, 1, 4, false>(a, s);
+        if (V == 7) return launch<false, 128, 256, 2, 4, 1, 1, 2, false>(a, s);
+        if (V == 8) return launch<false, 128, 256, 2, 4, 1, 1, 3, false>(a, s);
+        if (V == 9) return launch<false, 256, 256, 2, 4, 1, 1, 2, false>(a, s);
+        if (V == 10) return launch<false, 64, 128, 2, 2, 1, 1, 4, false>(a, s);
+        if (V == 12) return launch<false, 64, 256, 1, 4, 1, 1, 3, false>(a, s);
+    }
     auto tiles = [&](int64_t side) { return ((a.M + side - 1) / side) * ((a.N + side - 1) / side); };
     if (tiles(32) <= 2 * cus)
-        return exact ? launch<true, 32, 32, 1, 1, 2, 4, false>(a, s) : launch<false, 32, 32, 1, 1, 2, 4, false>(a, s);
-    if (!exact && 4 * tiles(256) >= 3 * cus) return launch<false, 256, 256, 2, 4, 1, 1, false>(a, s);
+        return exact ? launch<true, 32, 32, 1, 1, 2, 4, 2, false>(a, s) : launch<false, 32, 32, 1, 1, 2, 4, 2, false>(a, s);
+    if (!exact && 4 * tiles(256) >= 3 * cus) return launch<false, 256, 256, 2, 4, 1, 1, 2, false>(a, s);
     if (4 * tiles(128) >= 3 * cus)
-        return exact ? launch<true, 128, 128, 2, 2, 1, 1, false>(a, s) : launch<false, 128, 128, 2, 2, 1, 1, false>(a, s);
-    return exact ? launch<true, 64, 64, 2, 2, 2, 1, false>(a, s) : launch<false, 64, 64, 2, 2, 2, 1, false>(a, s);
+        return exact ? launch<true, 128, 128, 2, 2, 1, 1, 2, false>(a, s) : launch<false, 128, 128, 2, 2, 1, 1, 2, false>(a, s);
+    return exact ? launch<true, 64, 64, 2, 2, 2, 1, 2, false>(a, s) : launch<false, 64, 64, 2, 2, 2, 1, 2, false>(a, s);
 }
 
 }  // namespace dmm
