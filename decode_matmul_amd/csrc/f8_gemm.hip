@@ -14,12 +14,19 @@
 //
 // Mapping.  A workgroup owns BM tokens x BN rows of W, its waves equal parts of that.  W is
 // the first operand, so a lane ends with four consecutive n of one token, and f is one value
-// for each of its tokens.  K is cut into slabs of KD blocks, which take turns in two LDS
-// arrays: distinct ones, so the compiler can tell a load in flight to one from the reads of
-// the other.  Rows go from global memory straight to LDS in whole lines of 128 bytes, a block
-// each, a slab ahead; pieces change places within their rows so that a fragment read
-// hits all banks (swizzle).  The products f of FU blocks come by way of registers.
-#include <stdlib.h>
+// for each of its tokens.  K is cut into slabs of KD blocks, which take turns in NS LDS
+// stages: distinct arrays, so the compiler can tell a load in flight to one from the reads of
+// another.  Rows go from global memory straight to LDS in whole lines of 128 bytes, a block
+// each, NS - 1 slabs ahead; pieces change places within their rows so that a fragment read
+// hits all banks (swizzle).  The products f of NS slabs come by way of registers.
+//
+// Bound, largest tile (2048 tokens, 8192 x 8192, 117 to 126 us by card): the LDS, whose reads
+// and writes of a slab take about as long as its matrix instructions.  Without the reads of x's
+// fragments 85 us remain, without the loads 102, without the multiply-adds 102.  What paid:
+// overwriting a slab's first half (W, and half of x) at its middle (with the addresses below,
+// 162 -> 126 us), adding sums four instructions late (121), the middle's barrier ahead of the
+// next read (117).  Eight waves of 64 x 128 need more registers than there are.  Smaller
+// tiles: what a compute unit can have under way against the latency of memory.
 #include <type_traits>
 
 #include "experts.h"
@@ -41,8 +48,8 @@ struct Floats {
     typedef float T __attribute__((ext_vector_type(N)));
 };
 
-// EXACT: y is fp32, otherwise bf16.  BM x BN tile of WM x WN waves; KD blocks a slab.  KG groups of WM x WN waves take every
-// KG-th slab each, and the first adds up the sums.
+// EXACT: y is fp32, otherwise bf16.  BM x BN tile of WM x WN waves; KD blocks a slab.  KG groups of WM x WN waves take a part of
+// K each, and the first adds up the sums.  NS stages.
 template <bool EXACT, int BM, int BN, int WM, int WN, int KD, int KG, int NS, bool GROUPED>
 __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulArgs a) {
     constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;                 // of a group
@@ -51,19 +58,20 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
     constexpr int MT = BM / WM / 16, NT = BN / WN / 16;                     // tiles of a wave
     constexpr int kXLoads = kXBytes / 1024 / kWaves, kWLoads = kWBytes / 1024 / kWaves;
     constexpr int NB = BN > 128 ? BN / 128 : 1;                             // scales of W along n
-    constexpr int kFSlabs = KG > 1 ? 1 : NS, FU = kFSlabs * KD;  // slabs, blocks of a fetch of scales
+    constexpr int kFSlabs = NS, FU = kFSlabs * KD;  // slabs, blocks of a fetch of scales
     constexpr int kLoads = kXLoads + kWLoads;
     // Two large stages: what the first half of a slab has read is overwritten at its middle
-    constexpr bool kEarly = NS == 2 && KD == 1 && KG == 1 && BM == 256 && WM == 2 && kWaves == 8;
+    constexpr bool kEarly = NS == 2 && KD == 1 && KG == 1 && BM == 256 && kWaves == 8;
+    static_assert(NT % 4 == 0 || NT < 4, "kLag");
     static_assert(kXLoads * 1024 * kWaves == kXBytes && kWLoads * 1024 * kWaves == kWBytes, "whole loads");
     static_assert(BM * NB <= kThreads, "a thread for each row's scales");
     static_assert(BN / WN <= 128 || NB == 1, "a wave has one scale of W");
-    static_assert(NS == 2 || (KG == 1 && NS <= 4), "stages");
+    static_assert(NS >= 2 && NS <= 4, "stages");
     // A stage: x's rows by halves (below), then W's.
     __shared__ __attribute__((aligned(1024))) uint8_t stages0[kEarly ? kXBytes / 2 : KG * kStage];
     __shared__ __attribute__((aligned(1024))) uint8_t stages1[kEarly ? kXBytes / 2 : KG * kStage];
-    __shared__ __attribute__((aligned(1024))) uint8_t stages2[NS > 2 ? kStage : kEarly ? kXBytes / 2 : 16];
-    __shared__ __attribute__((aligned(1024))) uint8_t stages3[NS > 3 ? kStage : kEarly ? kXBytes / 2 : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t stages2[NS > 2 ? KG * kStage : kEarly ? kXBytes / 2 : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t stages3[NS > 3 ? KG * kStage : kEarly ? kXBytes / 2 : 16];
     __shared__ __attribute__((aligned(1024))) uint8_t rows0[kEarly ? kWBytes : 16];
     __shared__ __attribute__((aligned(1024))) uint8_t rows1[kEarly ? kWBytes : 16];
     // (one index: the compiler sees through a few address computations only, and waits for all loads
@@ -74,14 +82,16 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
     const int tid = (int)threadIdx.x - kg * kThreads, lane = tid & 63, wave = readfirstlane(tid >> 6);
     uint8_t* const stage0 = stages0 + (KG > 1 ? kg * kStage : 0);
     uint8_t* const stage1 = stages1 + (KG > 1 ? kg * kStage : 0);
+    uint8_t* const stage2 = stages2 + (KG > 1 && NS > 2 ? kg * kStage : 0);
+    uint8_t* const stage3 = stages3 + (KG > 1 && NS > 3 ? kg * kStage : 0);
     struct Stage {
         uint8_t *x0, *x1, *w;                   // of unit 0
     };
     const Stage stage[4] = {
         {stage0, kEarly ? stages2 : stage0 + kXUnit / 2, kEarly ? rows0 : stage0 + kXBytes},
         {stage1, kEarly ? stages3 : stage1 + kXUnit / 2, kEarly ? rows1 : stage1 + kXBytes},
-        {stages2, stages2 + kXUnit / 2, stages2 + kXBytes},
-        {stages3, stages3 + kXUnit / 2, stages3 + kXBytes},
+        {stage2, stage2 + kXUnit / 2, stage2 + kXBytes},
+        {stage3, stage3 + kXUnit / 2, stage3 + kXBytes},
     };
     const int r = lane & 15, g = lane >> 4;
     const int wm = wave / WN, wn = wave % WN;
@@ -173,6 +183,9 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
 #pragma unroll
         for (int j = 0; j < MT; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
 
+    // Each group has `full` whole slabs one after the other.
+    const int64_t full = a.K / kF8Block / KD / KG;
+    auto block_of = [&](int64_t t) { return (kg * full + t) * KD; };
     enum { kAll, kFirst, kSecond };             // of a slab's rows: the first half are W's and x's first half
     auto load_x = [&](const Stage& st, int j, GlobalBytes from) {
         const int at = (wave + j * kWaves) * 1024;
@@ -180,8 +193,8 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
         else load_lds16(from, st.x0 + at);
     };
     auto start = [&](const Stage& st, int64_t t, int which) {   // slab t, a whole one
-        const GlobalBytes xb = scalar_base(xbase + (t * KG + kg) * (KD * kRow));
-        const GlobalBytes wb = scalar_base(wbase + (t * KG + kg) * (KD * kRow));
+        const GlobalBytes xb = scalar_base(xbase + block_of(t) * kRow);
+        const GlobalBytes wb = scalar_base(wbase + block_of(t) * kRow);
 #pragma unroll
         for (int j = 0; j < kXLoads; ++j) {
             if (which != kAll && (2 * j >= kXLoads) != (which == kSecond)) continue;
@@ -232,30 +245,36 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
         const uint32_t at = lane_offset((uint32_t)((((kg * 2 + buf) * NB + fn) * FU + u) * BM + wm * (BM / WM) + 16 * j + r));
         f[j & 1] = factors[at];
     };
+    // A block's sums are added kLag instructions later, when they are long done: a vector
+    // instruction that reads one right behind its matrix instruction waits.
+    constexpr int kLag = NT < 4 ? NT : 4;
+    f32x4 part[kLag];
+    float scale = 0.f;
+#pragma unroll
+    for (int i = 0; i < kLag; ++i) part[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    auto add = [&](int i, int j, float s) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(s, part[i % kLag][e], acc[i][j][e]);
+        asm volatile("" : "+v"(acc[i][j]));
+    };
     auto multiply = [&](int j, auto next) {
         Part x[kParts];
         as_parts(xf[j & 1], x);
-        const float s = f[j & 1];
-        f32x4 part[NT];
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-            part[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+            if (i < kLag) add(NT - kLag + i, j == 0 ? MT - 1 : j - 1, scale);
+            else add(i - kLag, j, f[j & 1]);
+            f32x4 sum = {0.f, 0.f, 0.f, 0.f};
             if constexpr (EXACT) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    part[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[i][q], x[q], part[i], 0, 0, 0);
+                for (int q = 0; q < 4; ++q) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[i][q], x[q], sum, 0, 0, 0);
             } else {
-                part[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(f8_operand(wf[i]), f8_operand(x), part[i],
-                                                                           0, 0, 0, 0, 0, 0);
+                sum = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(f8_operand(wf[i]), f8_operand(x), sum, 0, 0, 0, 0, 0, 0);
             }
+            part[i % kLag] = sum;
             next(i);
         }
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(s, part[i][e], acc[i][j][e]);
-            asm volatile("" : "+v"(acc[i][j]));
-        }
+        scale = f[j & 1];
         asm volatile("" ::: "memory");
     };
     auto nothing = [](int) {};
@@ -266,8 +285,6 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
     // The products f of slab t are in factors' half (t / kFSlabs) % 2, from block t % kFSlabs KD on.
     // MAIN: all of these slabs, and the next kFSlabs, are there, and the slab's place among kFSlabs is PHASE; without
     // branches the compiler can count the loads behind a fetch of scales and need not wait for them.
-    const int64_t full = a.K / kF8Block / KD / KG;
-    auto block_of = [&](int64_t t) { return (t * KG + kg) * KD; };
     auto slab = [&](const Stage& cur, const Stage& other, int64_t t, auto main, auto phase) {
         constexpr bool MAIN = decltype(main)::value;
         const int in = MAIN ? decltype(phase)::value : (int)(t % kFSlabs), next = in + 1 == kFSlabs ? 0 : in + 1;
@@ -278,11 +295,12 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
                 if (j + 1 < MT) {
-                    read_x(cur, buf, k, u0 + k, j + 1, false);
+                    // (ahead of the next read, whose return the barrier would wait for)
                     if (kEarly && j == MT / 2 - 1 && (MAIN || t + NS < full)) {
                         lds_barrier();
                         start(cur, t + NS, kFirst);
                     }
+                    read_x(cur, buf, k, u0 + k, j + 1, false);
                     multiply(j, nothing);
                 } else if (k + 1 < KD) {
                     read_x(cur, buf, k + 1, u0 + k + 1, 0, false);
@@ -323,14 +341,11 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
 #pragma unroll
         for (int i = 0; i < NT; ++i) read_w(stage[0], 0, i, false);
         int64_t t = 0;
-        if constexpr (KG == 1) {
-            static_assert(KG > 1 || kFSlabs >= NS, "what starts is there");
-            for (; t + 2 * kFSlabs <= full; t += kFSlabs) {
-                slab(stage[0], stage[1], t, always, P0());
-                slab(stage[1], stage[NS > 2 ? 2 : 0], t + 1, always, P1());
-                if constexpr (kFSlabs > 2) slab(stage[NS > 2 ? 2 : 0], stage[NS > 3 ? 3 : NS > 2 ? 0 : 1], t + 2, always, P2());
-                if constexpr (kFSlabs > 3) slab(stage[NS > 3 ? 3 : 1], stage[0], t + 3, always, P3());
-            }
+        for (; t + 2 * kFSlabs <= full; t += kFSlabs) {
+            slab(stage[0], stage[1], t, always, P0());
+            slab(stage[1], stage[NS > 2 ? 2 : 0], t + 1, always, P1());
+            if constexpr (NS > 2) slab(stage[2], stage[NS > 3 ? 3 : 0], t + 2, always, P2());
+            if constexpr (NS > 3) slab(stage[3], stage[0], t + 3, always, P3());
         }
         for (; t < full; t += NS) {
             slab(stage[0], stage[1], t, maybe, P0());
@@ -340,10 +355,12 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
         }
     }
     // blocks that are left, the last one maybe cut: up to KD for each group
-    const int64_t first = block_of(full);
+    const int64_t first = (full * KG + kg) * KD;
     if (nb > full * KG * KD) {
         const int rest = nb > first ? (int)(nb - first < KD ? nb - first : KD) : 0;
         lds_barrier();
+        fetch_factors(first, false);
+        store_factors(0);
         // units past the last block repeat it and are not multiplied
         auto unit_of = [&](int u) { return first + u < nb ? first + u : nb - 1; };
 #pragma unroll
@@ -355,7 +372,6 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
                        stage[0].w + (wave + j * kWaves) * 1024);
         wait_loads<0>();
         lds_barrier();
-        const int buf = (int)(full / kFSlabs) & 1, u0 = (int)(full % kFSlabs) * KD;
 #pragma unroll 1
         for (int k = 0; k < rest; ++k) {
             kept = a.K - (first + k) * kF8Block < kF8Block ? (int)(a.K - (first + k) * kF8Block) : kF8Block;
@@ -363,11 +379,14 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
             for (int i = 0; i < NT; ++i) read_w(stage[0], k, i, true);
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
-                read_x(stage[0], buf, k, u0 + k, j, true);
+                read_x(stage[0], 0, k, k, j, true);
                 multiply(j, nothing);
             }
         }
     }
+
+#pragma unroll
+    for (int i = NT - kLag; i < NT; ++i) add(i, MT - 1, scale);
 
     if constexpr (KG > 1) {
         static_assert((KG - 1) * BM * BN * 4 <= KG * kStage, "the sums fit the stages");
@@ -415,9 +434,10 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
         typedef decltype(type) T;
         constexpr int kCols = NT * 16, kPitch = kCols * (int)sizeof(T) + 16, kEach = 16 / (int)sizeof(T);
         constexpr int kLanes = kCols / kEach, kAtOnce = 64 / kLanes < 16 ? 64 / kLanes : 16;
-        constexpr int kHalf = (kWaves + 1) / 2; // waves a stage
-        static_assert(kHalf * 16 * kPitch <= (kEarly ? kXBytes / 2 : kStage), "the stages hold the waves' rows");
-        uint8_t* const mine = (wave < kHalf ? stage0 : stage1) + wave % kHalf * (16 * kPitch);
+        constexpr int kArrays = kEarly ? 4 : 2, kIn = (kWaves + kArrays - 1) / kArrays;         // waves in each
+        static_assert(kIn * 16 * kPitch <= (kEarly ? kXBytes / 2 : kStage), "the stages hold the waves' rows");
+        uint8_t* const in = wave / kIn == 0 ? stage0 : wave / kIn == 1 ? stage1 : wave / kIn == 2 ? stages2 : stages3;
+        uint8_t* const mine = in + wave % kIn * (16 * kPitch);
         const int c = lane % kLanes, col = wn * (BN / WN) + c * kEach;
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
@@ -478,49 +498,45 @@ hipError_t launch(const F8MatmulArgs& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_f8_gemm(const F8MatmulArgs& a, hipStream_t s) {
-    const bool exact = a.y_dtype == TQ_F32;
-    static const char* v = getenv("GEMMV");
-    const int V = v ? atoi(v) : 0;
-    if (a.n_experts > 0) {
-        if (!exact) {
-            if (V == 1) return launch<false, 32, 128, 1, 4, 2, 1, 2, true>(a, s);
-            if (V == 2) return launch<false, 32, 128, 1, 4, 1, 1, 4, true>(a, s);
-            if (V == 3) return launch<false, 64, 128, 1, 4, 1, 1, 3, true>(a, s);
-            if (V == 4) return launch<false, 64, 256, 1, 4, 1, 1, 3, true>(a, s);
-            if (V == 5) return launch<false, 128, 256, 2, 4, 1, 1, 2, true>(a, s);
-            if (V == 6) return launch<false, 128, 256, 2, 4, 1, 1, 3, true>(a, s);
-            if (V == 7) return launch<false, 128, 128, 2, 2, 1, 1, 2, true>(a, s);
-            if (V == 8) return launch<false, 128, 128, 2, 2, 1, 1, 4, true>(a, s);
-            if (V == 9) return launch<false, 64, 256, 1, 4, 1, 1, 2, true>(a, s);
-            if (V == 10) return launch<false, 256, 256, 2, 4, 1, 1, 2, true>(a, s);
-            if (V == 11) return launch<false, 32, 256, 1, 4, 1, 1, 4, true>(a, s);
-        }
-        if (a.M * a.top_k < 40 * (int64_t)a.n_experts)
-            return exact ? launch<true, 32, 128, 1, 4, 2, 1, 2, true>(a, s) : launch<false, 32, 128, 1, 4, 2, 1, 2, true>(a, s);
-        return exact ? launch<true, 128, 128, 2, 2, 1, 1, 2, true>(a, s) : launch<false, 128, 256, 2, 4, 1, 1, 2, true>(a, s);
-    }
+namespace {
+
+template <bool EXACT>
+hipError_t by_size(const F8MatmulArgs& a, hipStream_t s) {
+    if (a.n_experts > 0)
+        return a.M * a.top_k < 64 * (int64_t)a.n_experts ? launch<EXACT, 64, 128, 1, 4, 1, 1, 3, true>(a, s)
+                                                         : launch<EXACT, 128, 128, 2, 2, 1, 1, 2, true>(a, s);
     const int64_t cus = compute_unit_count();
-    if (!exact) {
-        if (V == 1) return launch<false, 32, 32, 1, 1, 2, 4, 2, false>(a, s);
-        if (V == 2) return launch<false, 64, 64, 2, 2, 2, 1, 2, false>(a, s);
-        if (V == 3) return launch<false, 64, 64, 2, 2, 2, 1, 4, false>(a, s);
-        if (V == 4) return launch<false, 64, 64, 2, 2, 1, 1, 4, false>(a, s);
-        if (V == 5) return launch<false, 128, 128, 2, 2, 1, 1, 2, false>(a, s);
-        if (V == 6) return launch<false, 128, 128, 2, 2, 1, 1, 4, false>(a, s);
-        if (V == 7) return launch<false, 128, 256, 2, 4, 1, 1, 2, false>(a, s);
-        if (V == 8) return launch<false, 128, 256, 2, 4, 1, 1, 3, false>(a, s);
-        if (V == 9) return launch<false, 256, 256, 2, 4, 1, 1, 2, false>(a, s);
-        if (V == 10) return launch<false, 64, 128, 2, 2, 1, 1, 4, false>(a, s);
-        if (V == 12) return launch<false, 64, 256, 1, 4, 1, 1, 3, false>(a, s);
-    }
     auto tiles = [&](int64_t side) { return ((a.M + side - 1) / side) * ((a.N + side - 1) / side); };
-    if (tiles(32) <= 2 * cus)
-        return exact ? launch<true, 32, 32, 1, 1, 2, 4, 2, false>(a, s) : launch<false, 32, 32, 1, 1, 2, 4, 2, false>(a, s);
-    if (!exact && 4 * tiles(256) >= 3 * cus) return launch<false, 256, 256, 2, 4, 1, 1, 2, false>(a, s);
-    if (4 * tiles(128) >= 3 * cus)
-        return exact ? launch<true, 128, 128, 2, 2, 1, 1, 2, false>(a, s) : launch<false, 128, 128, 2, 2, 1, 1, 2, false>(a, s);
-    return exact ? launch<true, 64, 64, 2, 2, 2, 1, 2, false>(a, s) : launch<false, 64, 64, 2, 2, 2, 1, 2, false>(a, s);
+    if (tiles(32) <= cus) return launch<EXACT, 32, 32, 1, 1, 1, 4, 4, false>(a, s);
+    if (tiles(32) <= 2 * cus) return launch<EXACT, 32, 64, 1, 2, 1, 4, 3, false>(a, s);
+    if constexpr (!EXACT)
+        if (4 * tiles(256) >= 3 * cus) return launch<EXACT, 256, 256, 2, 4, 1, 1, 2, false>(a, s);
+    if (4 * tiles(128) >= 3 * cus) return launch<EXACT, 128, 128, 2, 2, 1, 1, 2, false>(a, s);
+    return tiles(64) <= cus ? launch<EXACT, 64, 64, 2, 2, 2, 1, 4, false>(a, s) : launch<EXACT, 64, 64, 2, 2, 2, 1, 2, false>(a, s);
+}
+
+}  // namespace
+
+// The largest tile that still gives nearly every compute unit one (its rate is the highest, 2.3
+// PFLOP/s, but a wave of tiles costs its time whether it fills the chip or not); tiles of 128 x
+// 128 share a unit's LDS by twos.  us, bf16 y, graph replays over 600 MB of weights:
+//                          256 x 256   128 x 128   64 x 64, 2 stages / 4   32 x 64, 3   32 x 32, 4
+//   M = 2048  8192 x 8192     118         153         256 / 413
+//   M = 1024  14336 x 4096     65          80         108 / 187
+//   M =  512  8192 x 8192      97          48          58 /  92
+//   M =  256  8192 x 8192     103          60          43 /  56           91           112
+//   M =  128  8192 x 8192      99          61          34 /  31           49            59
+//   M =   64  8192 x 8192      98          59          34 /  31           27            33
+//   M =   64  4096 x 4096      52          32          18 /  17           16            11
+//   M =   32  8192 x 8192      98          58          32 /  29           27            20
+// Where few tiles leave units idle, four groups of a workgroup's waves take a part of K each, and
+// the deeper stages hide the latency that nothing else does.
+// Experts, by the slots an expert has on average (64 experts of 2048 x 4096), 64 x 128 with 3
+// stages / 128 x 128 with 2:
+//   16   123 / 128     32   142 / 153     64   157 / 157     128   204 / 190     256   321 / 255
+// (128 x 256: 202 at 128, 275 at 256; 256 x 256: 204, 262; 64 x 256 with 2: 236, 357.)
+hipError_t launch_f8_gemm(const F8MatmulArgs& a, hipStream_t s) {
+    return a.y_dtype == TQ_F32 ? by_size<true>(a, s) : by_size<false>(a, s);
 }
 
 }  // namespace dmm
