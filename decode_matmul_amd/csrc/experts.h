@@ -28,20 +28,36 @@ __device__ bool place_grouped(const Args& a, Place& p) {
         return o < 0 ? 0 : (o > slots ? slots : o);
     };
     if (tid == 0) found[2] = -1;
+    // An expert's tiles and those before it: experts e0 .. e0 + kThreads - 1, one a thread.
+    int first = 0, last = 0, n = 0, mine = 0;
+    auto scan = [&](int e0, int before) {
+        const int e = e0 + tid;
+        n = 0;
+        if (e < a.n_experts) {
+            first = bound(e);
+            last = bound(e + 1);
+            n = last > first ? (last - first + BM - 1) / BM : 0;
+        }
+        int inc = n;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(inc, d);
+            if (lane >= d) inc += o;
+        }
+        if (lane == 63) sums[wave] = inc;
+        __syncthreads();
+        int all = before;
+        mine = before + inc - n;
+        for (int w = 0; w < kThreads / 64; ++w) {
+            if (w < wave) mine += sums[w];
+            all += sums[w];
+        }
+        return all;
+    };
     int total = 0;
     for (int e0 = 0; e0 < a.n_experts; e0 += kThreads) {
-        const int e = e0 + tid;
-        int t = 0;
-        if (e < a.n_experts) {
-            const int c = bound(e + 1) - bound(e);
-            t = c > 0 ? (c + BM - 1) / BM : 0;
-        }
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) t += __shfl_xor(t, d);
-        if (lane == 0) sums[wave] = t;
-        __syncthreads();
-        for (int w = 0; w < kThreads / 64; ++w) total += sums[w];
-        __syncthreads();
+        if (e0 > 0) __syncthreads();
+        total = scan(e0, total);
     }
     total = readfirstlane(total);
     const int64_t all = (int64_t)total * ntiles;
@@ -59,41 +75,24 @@ __device__ bool place_grouped(const Args& a, Place& p) {
     p.n0 = (t - (int64_t)want * ntiles) * BN;
     int before = 0;
     for (int e0 = 0; e0 < a.n_experts; e0 += kThreads) {
-        const int e = e0 + tid;
-        int n = 0, first = 0, last = 0;
-        if (e < a.n_experts) {
-            first = bound(e);
-            last = bound(e + 1);
-            n = last > first ? (last - first + BM - 1) / BM : 0;
+        if (a.n_experts > kThreads) {           // otherwise the one scan is at hand
+            __syncthreads();
+            before = scan(e0, before);
         }
-        int inc = n;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(inc, d);
-            if (lane >= d) inc += o;
-        }
-        if (lane == 63) sums[wave] = inc;
-        __syncthreads();
-        int base = before;
-        for (int w = 0; w < kThreads / 64; ++w) {
-            if (w < wave) base += sums[w];
-            before += sums[w];
-        }
-        const int mine = base + inc - n;
         if (want >= mine && want < mine + n) {
             found[0] = first + (want - mine) * BM;
             found[1] = last;
-            found[2] = e;
+            found[2] = e0 + tid;
         }
-        __syncthreads();
     }
+    __syncthreads();
     if (readfirstlane(found[2]) < 0) {          // overlapping lists can have more tiles than an int counts
         p.m0 = p.m_end = a.M * a.top_k;
         return false;
     }
     p.m0 = readfirstlane(found[0]);
-    const int64_t last = readfirstlane(found[1]);
-    p.m_end = last < p.m0 + BM ? last : p.m0 + BM;
+    const int64_t end = readfirstlane(found[1]);
+    p.m_end = end < p.m0 + BM ? end : p.m0 + BM;
     p.expert = readfirstlane(found[2]);
     return true;
 }

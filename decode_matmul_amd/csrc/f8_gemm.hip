@@ -198,7 +198,6 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
 #pragma unroll
         for (int j = 0; j < kXLoads; ++j) {
             if (which != kAll && (2 * j >= kXLoads) != (which == kSecond)) continue;
-            if (BM == 32 && NS == 2 && x_group(j) * 8 >= m_rows) continue;      // rows no token reads (and no count of loads)
             load_x(st, j, xb + lane_offset(xsrc[j]));
         }
         if (which == kSecond) return;
@@ -328,15 +327,22 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
     const std::true_type always;
     const std::false_type maybe;
 
-    fetch_factors(block_of(0), false);
-    if (full > 0) start(stage[0], 0, kAll);
-    store_factors(0);
-    if (full > 0) {
-        wait_loads<0>();
-        lds_barrier();
+    if (full >= NS) {                           // every stage is on its way before the first is waited for
+        fetch_factors(block_of(0), true);
 #pragma unroll
-        for (int i = 1; i < NS; ++i)
+        for (int i = 0; i < NS; ++i) start(stage[i], i, kAll);
+        store_factors(0);
+        wait_loads<(NS - 1) * kLoads>();
+    } else if (full > 0) {
+        fetch_factors(block_of(0), false);
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
             if (i < full) start(stage[i], i, kAll);
+        store_factors(0);
+        wait_loads<0>();
+    }
+    if (full > 0) {
+        lds_barrier();
         read_x(stage[0], 0, 0, 0, 0, false);
 #pragma unroll
         for (int i = 0; i < NT; ++i) read_w(stage[0], 0, i, false);
