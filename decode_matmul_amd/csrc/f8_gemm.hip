@@ -111,10 +111,14 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
     // Row of tile row i, counted from the tile's first (in a list: the row of x);
     // rows that are not there repeat one that is.
     const int m_rows = (int)(p.m_end - p.m0), n_rows = (int)(a.N - p.n0 < BN ? a.N - p.n0 : BN);
+    // (A list's slots come once, to LDS, while the first rows of W are on their way.)
+    __shared__ int32_t list[GROUPED ? BM : 1];
+    int32_t entry = 0;
+    if (GROUPED && tid < BM) entry = a.order[p.m0 + (tid < m_rows ? tid : m_rows - 1)];
     auto x_row = [&](int i) -> int64_t {
         const int m = i < m_rows ? i : m_rows - 1;
         if (!GROUPED) return m;
-        const int64_t slot = a.order[p.m0 + m];
+        const int64_t slot = list[m];
         return slot >= 0 && slot < slots ? (int64_t)((uint32_t)slot / (uint32_t)a.top_k) : 0;
     };
     auto w_row = [&](int i) { return i < n_rows ? i : n_rows - 1; };
@@ -137,16 +141,34 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
     const int64_t row_bytes = nb * kRow;
     const uint8_t* const xbase = a.x_codes + (GROUPED ? 0 : p.m0) * row_bytes;
     const uint8_t* const wbase = a.codes + (p.expert * a.N + p.n0) * row_bytes;
-    XOffset xsrc[kXLoads];
     uint32_t wsrc[kWLoads];
-#pragma unroll
-    for (int j = 0; j < kXLoads; ++j)
-        xsrc[j] = lane_offset((XOffset)x_row(x_group(j) * 8 + sub) * (XOffset)row_bytes +
-                              (XOffset)(x_unit(j) * kRow + piece(x_group(j)) * 16));
 #pragma unroll
     for (int j = 0; j < kWLoads; ++j)
         wsrc[j] = lane_offset((uint32_t)w_row(w_group(j) * 8 + sub) * (uint32_t)row_bytes +
                               (uint32_t)(w_unit(j) * kRow + piece(w_group(j)) * 16));
+    // Each group has `full` whole slabs one after the other.
+    const int64_t full = a.K / kF8Block / KD / KG;
+    auto block_of = [&](int64_t t) { return (kg * full + t) * KD; };
+    auto start_w = [&](const Stage& st, int64_t t) {            // of slab t, a whole one
+        const GlobalBytes wb = scalar_base(wbase + block_of(t) * kRow);
+#pragma unroll
+        for (int j = 0; j < kWLoads; ++j) load_lds16(wb + lane_offset(wsrc[j]), st.w + (wave + j * kWaves) * 1024);
+    };
+    asm volatile("" ::: "memory");
+    if (full >= NS) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) start_w(stage[i], i);
+    }
+    asm volatile("" ::: "memory");
+    if (GROUPED) {
+        if (tid < BM) list[tid] = entry;
+        lds_barrier();
+    }
+    XOffset xsrc[kXLoads];
+#pragma unroll
+    for (int j = 0; j < kXLoads; ++j)
+        xsrc[j] = lane_offset((XOffset)x_row(x_group(j) * 8 + sub) * (XOffset)row_bytes +
+                              (XOffset)(x_unit(j) * kRow + piece(x_group(j)) * 16));
 
     // Thread (row, n block) fetches FU scales of both and stages their products.
     typedef typename Floats<FU>::T Scales;
@@ -183,26 +205,21 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
 #pragma unroll
         for (int j = 0; j < MT; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
 
-    // Each group has `full` whole slabs one after the other.
-    const int64_t full = a.K / kF8Block / KD / KG;
-    auto block_of = [&](int64_t t) { return (kg * full + t) * KD; };
     enum { kAll, kFirst, kSecond };             // of a slab's rows: the first half are W's and x's first half
     auto load_x = [&](const Stage& st, int j, GlobalBytes from) {
         const int at = (wave + j * kWaves) * 1024;
         if (kEarly) load_lds16(from, 2 * j < kXLoads ? st.x0 + at : st.x1 + (at - kXBytes / 2));
         else load_lds16(from, st.x0 + at);
     };
-    auto start = [&](const Stage& st, int64_t t, int which) {   // slab t, a whole one
+    auto start_x = [&](const Stage& st, int64_t t, int which) {
         const GlobalBytes xb = scalar_base(xbase + block_of(t) * kRow);
-        const GlobalBytes wb = scalar_base(wbase + block_of(t) * kRow);
 #pragma unroll
-        for (int j = 0; j < kXLoads; ++j) {
-            if (which != kAll && (2 * j >= kXLoads) != (which == kSecond)) continue;
-            load_x(st, j, xb + lane_offset(xsrc[j]));
-        }
-        if (which == kSecond) return;
-#pragma unroll
-        for (int j = 0; j < kWLoads; ++j) load_lds16(wb + lane_offset(wsrc[j]), st.w + (wave + j * kWaves) * 1024);
+        for (int j = 0; j < kXLoads; ++j)
+            if (which == kAll || (2 * j >= kXLoads) == (which == kSecond)) load_x(st, j, xb + lane_offset(xsrc[j]));
+    };
+    auto start = [&](const Stage& st, int64_t t, int which) {   // slab t, a whole one
+        start_x(st, t, which);
+        if (which != kSecond) start_w(st, t);
     };
 
     // ---- fragments of a unit: the wave's rows of W, held for all of its tokens, and one
@@ -330,9 +347,9 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
     if (full >= NS) {                           // every stage is on its way before the first is waited for
         fetch_factors(block_of(0), true);
 #pragma unroll
-        for (int i = 0; i < NS; ++i) start(stage[i], i, kAll);
+        for (int i = 0; i < NS; ++i) start_x(stage[i], i, kAll);
         store_factors(0);
-        wait_loads<(NS - 1) * kLoads>();
+        wait_loads<(NS - 1) * kXLoads>();
     } else if (full > 0) {
         fetch_factors(block_of(0), false);
 #pragma unroll
@@ -431,7 +448,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
     auto y_row = [&](int i) -> int64_t {
         if (i >= m_rows) return -1;
         if (!GROUPED) return p.m0 + i;
-        const int64_t slot = a.order[p.m0 + i];
+        const int64_t slot = list[i];
         return slot < slots ? slot : -1;
     };
     // Rows of y in 16-byte pieces: the wave's 16 tokens x 16 NT columns of each j change
