@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
     constexpr int kFSlabs = NS, FU = kFSlabs * KD;  // slabs, blocks of a fetch of scales
     constexpr int kLoads = kXLoads + kWLoads;
     // Two large stages: what the first half of a slab has read is overwritten at its middle
-    constexpr bool kEarly = NS == 2 && KD == 1 && KG == 1 && BM == 256 && kWaves == 8;
+    constexpr bool kEarly = NS == 2 && KD == 1 && KG == 1 && MT >= 4 && !EXACT;
     static_assert(NT % 4 == 0 || NT < 4, "kLag");
     static_assert(kXLoads * 1024 * kWaves == kXBytes && kWLoads * 1024 * kWaves == kWBytes, "whole loads");
     static_assert(BM * NB <= kThreads, "a thread for each row's scales");
