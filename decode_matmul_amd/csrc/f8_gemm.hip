@@ -301,8 +301,9 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
     // The products f of slab t are in factors' half (t / kFSlabs) % 2, from block t % kFSlabs KD on.
     // MAIN: all of these slabs, and the next kFSlabs, are there, and the slab's place among kFSlabs is PHASE; without
     // branches the compiler can count the loads behind a fetch of scales and need not wait for them.
-    auto slab = [&](const Stage& cur, const Stage& other, int64_t t, auto main, auto phase) {
-        constexpr bool MAIN = decltype(main)::value;
+    auto slab = [&](const Stage& cur, const Stage& other, int64_t t, auto busy, auto main,
+                    auto phase) __attribute__((always_inline)) {
+        constexpr bool BUSY = decltype(busy)::value, MAIN = decltype(main)::value;
         const int in = MAIN ? decltype(phase)::value : (int)(t % kFSlabs), next = in + 1 == kFSlabs ? 0 : in + 1;
         const int buf = (int)(t / kFSlabs) & 1, u0 = in * KD, u1 = next * KD, buf1 = next == 0 ? buf ^ 1 : buf;
         if (in == 0) fetch_factors(block_of(t + kFSlabs), MAIN);
@@ -316,11 +317,15 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
                         lds_barrier();
                         start(cur, t + NS, kFirst);
                     }
-                    read_x(cur, buf, k, u0 + k, j + 1, false);
-                    multiply(j, nothing);
+                    if constexpr (BUSY) {
+                        read_x(cur, buf, k, u0 + k, j + 1, false);
+                        multiply(j, nothing);
+                    }
                 } else if (k + 1 < KD) {
-                    read_x(cur, buf, k + 1, u0 + k + 1, 0, false);
-                    multiply(j, [&](int i) { read_w(cur, k + 1, i, false); });
+                    if constexpr (BUSY) {
+                        read_x(cur, buf, k + 1, u0 + k + 1, 0, false);
+                        multiply(j, [&](int i) { read_w(cur, k + 1, i, false); });
+                    }
                 }
             }
         }
@@ -329,11 +334,13 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
         else wait_loads<0>();
         lds_barrier();
         if (MAIN || t + NS < full) start(cur, t + NS, kEarly ? kSecond : kAll);
-        if (MAIN || t + 1 < full) {
-            read_x(other, buf1, 0, u1, 0, false);
-            multiply(MT - 1, [&](int i) { read_w(other, 0, i, false); });
-        } else {
-            multiply(MT - 1, nothing);
+        if constexpr (BUSY) {
+            if (MAIN || t + 1 < full) {
+                read_x(other, buf1, 0, u1, 0, false);
+                multiply(MT - 1, [&](int i) { read_w(other, 0, i, false); });
+            } else {
+                multiply(MT - 1, nothing);
+            }
         }
     };
     static_assert(MT % 2 == 0, "the last tile's fragments and the next unit's first take turns");
@@ -358,29 +365,38 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
         store_factors(0);
         wait_loads<0>();
     }
-    if (full > 0) {
+    auto slabs = [&](auto busy) __attribute__((always_inline)) {
         lds_barrier();
-        read_x(stage[0], 0, 0, 0, 0, false);
+        if constexpr (decltype(busy)::value) {
+            read_x(stage[0], 0, 0, 0, 0, false);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) read_w(stage[0], 0, i, false);
+            for (int i = 0; i < NT; ++i) read_w(stage[0], 0, i, false);
+        }
         int64_t t = 0;
+        static_assert(kFSlabs >= NS, "what starts is there");
         for (; t + 2 * kFSlabs <= full; t += kFSlabs) {
-            slab(stage[0], stage[1], t, always, P0());
-            slab(stage[1], stage[NS > 2 ? 2 : 0], t + 1, always, P1());
-            if constexpr (NS > 2) slab(stage[2], stage[NS > 3 ? 3 : 0], t + 2, always, P2());
-            if constexpr (NS > 3) slab(stage[3], stage[0], t + 3, always, P3());
+            slab(stage[0], stage[1], t, busy, always, P0());
+            slab(stage[1], stage[NS > 2 ? 2 : 0], t + 1, busy, always, P1());
+            if constexpr (NS > 2) slab(stage[2], stage[NS > 3 ? 3 : 0], t + 2, busy, always, P2());
+            if constexpr (NS > 3) slab(stage[3], stage[0], t + 3, busy, always, P3());
         }
         for (; t < full; t += NS) {
-            slab(stage[0], stage[1], t, maybe, P0());
-            if (t + 1 < full) slab(stage[1], stage[NS > 2 ? 2 : 0], t + 1, maybe, P0());
-            if (NS > 2 && t + 2 < full) slab(stage[2], stage[NS > 3 ? 3 : 0], t + 2, maybe, P0());
-            if (NS > 3 && t + 3 < full) slab(stage[3], stage[0], t + 3, maybe, P0());
+            slab(stage[0], stage[1], t, busy, maybe, P0());
+            if (t + 1 < full) slab(stage[1], stage[NS > 2 ? 2 : 0], t + 1, busy, maybe, P0());
+            if (NS > 2 && t + 2 < full) slab(stage[2], stage[NS > 3 ? 3 : 0], t + 2, busy, maybe, P0());
+            if (NS > 3 && t + 3 < full) slab(stage[3], stage[0], t + 3, busy, maybe, P0());
         }
+    };
+    // A wave whose rows are all behind a list's end brings its loads and no more.
+    const bool has_rows = !GROUPED || WM == 1 || wm * (BM / WM) < m_rows;
+    if (full > 0) {
+        if (has_rows) slabs(std::true_type());
+        else if constexpr (GROUPED && WM > 1) slabs(std::false_type());
     }
     // blocks that are left, the last one maybe cut: up to KD for each group
     const int64_t first = (full * KG + kg) * KD;
     if (nb > full * KG * KD) {
-        const int rest = nb > first ? (int)(nb - first < KD ? nb - first : KD) : 0;
+        const int rest = nb > first && has_rows ? (int)(nb - first < KD ? nb - first : KD) : 0;
         lds_barrier();
         fetch_factors(first, false);
         store_factors(0);
