@@ -328,15 +328,25 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(GateArgs a) {
             for (int i = 0; i < 8; ++i) k[i] = 0u;
         }
     }
-    // lane j keeps the j-th largest key, j <= top_k
+    // lane j keeps the j-th largest key, j <= top_k; a lane whose best it was moves up the `left`
+    // that later rounds may want
     uint32_t mine = 0u;
-    for (int j = 0; j <= a.top_k; ++j) {
+    auto round = [&](int j, int left) {
         const uint32_t first = over_group<L>(k[0], larger);
         if (l == j) mine = first;
         const bool won = k[0] == first;
 #pragma unroll
-        for (int i = 0; i < 7; ++i) k[i] = won ? k[i + 1] : k[i];
-        k[7] = won ? 0u : k[7];
+        for (int i = 0; i < 8; ++i)
+            if (i < left) k[i] = won ? (i < 7 ? k[i < 7 ? i + 1 : 7] : 0u) : k[i];
+    };
+    if (a.top_k <= 8) {
+#pragma unroll
+        for (int j = 0; j <= 8; ++j) {
+            if (j > a.top_k) break;
+            round(j, 8 - j);
+        }
+    } else {
+        for (int j = 0; j <= a.top_k; ++j) round(j, 8);
     }
     const bool has = mine != 0u;
     const int id = (int)(kMask - (mine & kMask));
