@@ -11,13 +11,23 @@ struct Place {
     int64_t m0, m_end, n0, expert;
 };
 
+// Tile t of mt tiles of rows by nt along N, in groups of GM tiles of rows that take the
+// tiles along N in turn and share the rows of W (GM = 1: the tiles along N innermost).
+template <int GM>
+__device__ inline void in_groups(int64_t t, int64_t mt, int64_t nt, int64_t& m, int64_t& n) {
+    const int64_t grp = t / (GM * nt), m8 = grp * GM, gm = mt - m8 < GM ? mt - m8 : GM;
+    const int64_t in = t - m8 * nt;
+    m = m8 + in % gm;
+    n = in / gm;
+}
+
 // Tile b of the experts' tiles: experts in turn, an expert's tiles of BM
-// positions in turn, the tiles along N innermost; each XCD gets a contiguous
+// positions and BN rows of W in groups of GM; each XCD gets a contiguous
 // share of the tiles that there are.  False when there are fewer: then m0 is the
 // workgroup's number among the m_end that have none.
-template <int BM, int BN, int kThreads, class Args>
+template <int BM, int BN, int GM, int kThreads, class Args>
 __device__ bool place_grouped(const Args& a, Place& p) {
-    __shared__ int found[3];
+    __shared__ int found[4];
     __shared__ int sums[kThreads / 64];
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int slots = (int)(a.M * a.top_k);
@@ -72,7 +82,6 @@ __device__ bool place_grouped(const Args& a, Place& p) {
         return false;
     }
     const int want = readfirstlane((int)(t / ntiles));
-    p.n0 = (t - (int64_t)want * ntiles) * BN;
     int before = 0;
     for (int e0 = 0; e0 < a.n_experts; e0 += kThreads) {
         if (a.n_experts > kThreads) {           // otherwise the one scan is at hand
@@ -80,19 +89,24 @@ __device__ bool place_grouped(const Args& a, Place& p) {
             before = scan(e0, before);
         }
         if (want >= mine && want < mine + n) {
-            found[0] = first + (want - mine) * BM;
+            int64_t m, nt;
+            in_groups<GM>(t - (int64_t)mine * ntiles, n, ntiles, m, nt);
+            found[0] = first + (int)m * BM;
             found[1] = last;
+            found[3] = (int)nt;
             found[2] = e0 + tid;
         }
     }
     __syncthreads();
-    if (readfirstlane(found[2]) < 0) {          // overlapping lists can have more tiles than an int counts
+    p.m0 = readfirstlane(found[0]);
+    const int64_t end = readfirstlane(found[1]);
+    // (overlapping lists can have more tiles than an int counts: no thread or two may have the tile)
+    if (readfirstlane(found[2]) < 0 || end <= p.m0) {
         p.m0 = p.m_end = a.M * a.top_k;
         return false;
     }
-    p.m0 = readfirstlane(found[0]);
-    const int64_t end = readfirstlane(found[1]);
     p.m_end = end < p.m0 + BM ? end : p.m0 + BM;
+    p.n0 = (int64_t)readfirstlane(found[3]) * BN;
     p.expert = readfirstlane(found[2]);
     return true;
 }
@@ -117,11 +131,11 @@ template <int BM, int BN, class Args>
 __device__ Place place_dense(const Args& a) {
     const int64_t mt = (a.M + BM - 1) / BM, nt = (a.N + BN - 1) / BN;
     const int64_t t = xcd_block(blockIdx.x, mt * nt);
-    const int64_t grp = t / (8 * nt), m8 = grp * 8, gm = mt - m8 < 8 ? mt - m8 : 8;
-    const int64_t in = t - grp * 8 * nt;
+    int64_t m, n;
+    in_groups<8>(t, mt, nt, m, n);
     Place p;
-    p.m0 = (m8 + in % gm) * BM;
-    p.n0 = in / gm * BN;
+    p.m0 = m * BM;
+    p.n0 = n * BN;
     p.m_end = p.m0 + BM < a.M ? p.m0 + BM : a.M;
     p.expert = 0;
     return p;

@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
 
     Place p;
     if (GROUPED) {
-        if (!place_grouped<BM, BN, kThreads>(a, p)) {
+        if (!place_grouped<BM, BN, 8, kThreads>(a, p)) {
             write_nan_rows(a, p.m0, p.m_end, kThreads);
             return;
         }

@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) mx_gemm_kernel(MxMatmulA
 
     Place p;
     if (GROUPED) {
-        if (!place_grouped<BM, BN, kThreads>(a, p)) {
+        if (!place_grouped<BM, BN, 1, kThreads>(a, p)) {
             write_nan_rows(a, p.m0, p.m_end, kThreads);
             return;
         }

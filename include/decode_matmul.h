@@ -743,9 +743,9 @@ int f8_norm_pack(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t l
  * bits).  For a bf16 y of more than 16 tokens the sums come from the e4m3 matrix
  * instructions, of twice the rate, which keep 13 bits below the largest of each eight
  * products: they may be off by D = 7 2^-13 sum over each eight columns of the largest
- * |x w| as well (a bf16 y is rounded by up to 2^-9 of itself).  The product of two scales has to be one that fp32 holds (2^-126 to 2^128);
- * one that overflows makes its sums infinite or NaN.  A NaN scale or code makes what
- * it takes part in NaN.  M = 0 or N = 0 is a no-op; with K = 0 the packages may be
+ * |x w| as well (a bf16 y is rounded by up to 2^-9 of itself).  The product of two
+ * scales has to be one that fp32 holds (2^-126 to 2^128); one that overflows makes its
+ * sums infinite or NaN.  A NaN scale or code makes what it takes part in NaN.  M = 0 or N = 0 is a no-op; with K = 0 the packages may be
  * NULL and y = bias (or 0).  M and N are below 2^31, K is below 2^23; sizes that need
  * more than 2^32 - 1 threads are TQ_ERR_SHAPE.
  */
@@ -805,9 +805,10 @@ int f8_matmul_experts(const uint8_t* x_codes, const float* x_scales, int64_t M, 
  *  weights     device fp32 [M, top_k]: 0 where expert_ids is -1.
  *
  * Weights are fp32, each within (d + 32) 2^-23 of itself, d the spread of the token's
- * finite logits (sigmoid: their largest magnitude); +inf and NaN logits of a softmax
- * make its weights NaN where they are chosen (without renorm: all).  Sizes that need more than 2^32 - 1
- * threads are TQ_ERR_SHAPE (M of 2^26 and more).
+ * finite logits (sigmoid: their largest magnitude), where p (renorm: p over the largest
+ * chosen one) is above 2^-126; smaller ones are within 2^-126 of scale.  +inf and NaN
+ * logits of a softmax make its weights NaN where they are chosen (without renorm: all).
+ * Sizes that need more than 2^32 - 1 threads are TQ_ERR_SHAPE (M of 2^26 and more).
  */
 int moe_gate(const void* logits, int32_t l_dtype, int64_t M, int32_t n_experts, int64_t ldl,
              const uint8_t* token_mask, const float* bias, int32_t score, int32_t n_groups, int32_t top_groups,
@@ -852,8 +853,8 @@ int moe_gate_grad(const void* logits, int32_t l_dtype, int64_t M, int32_t n_expe
  *  out         device [M, N] of out_dtype.
  *
  * Sums are fp32, add first and then the slots in order, each product fused into its
- * addition; a bf16 out is rounded once.  M * top_k is below 2^31; sizes that need more than 2^32 - 1 threads are
- * TQ_ERR_SHAPE.
+ * addition; a bf16 out is rounded once.  M * top_k is below 2^31; sizes that need more
+ * than 2^32 - 1 threads are TQ_ERR_SHAPE.
  */
 int moe_combine(const void* y, int32_t y_dtype, int64_t M, int32_t top_k, int64_t N, const int32_t* expert_ids,
                 const float* weights, int32_t n_experts, const void* add, void* out, int32_t out_dtype,
