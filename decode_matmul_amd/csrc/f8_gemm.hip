@@ -20,13 +20,15 @@
 // each, NS - 1 slabs ahead; pieces change places within their rows so that a fragment read
 // hits all banks (swizzle).  The products f of NS slabs come by way of registers.
 //
-// Bound, largest tile (2048 tokens, 8192 x 8192, 117 to 126 us by card): the LDS, whose reads
+// Bound, largest tile (2048 tokens, 8192 x 8192, 113 to 126 us by card, 2.2 to 2.4 PFLOP/s): the LDS, whose reads
 // and writes of a slab take about as long as its matrix instructions.  Without the reads of x's
 // fragments 85 us remain, without the loads 102, without the multiply-adds 102.  What paid:
 // overwriting a slab's first half (W, and half of x) at its middle (with the addresses below,
 // 162 -> 126 us), adding sums four instructions late (121), the middle's barrier ahead of the
 // next read (117).  Eight waves of 64 x 128 need more registers than there are.  Smaller
-// tiles: what a compute unit can have under way against the latency of memory.
+// tiles: what a compute unit can have under way against the latency of memory.  Experts' tiles
+// (2048 tokens top 8 of 64, 2048 x 4096: 226 us, where W's bytes take 104 at a copy's rate): 44 us are a
+// tile's beginning and end, 150 remain without loads, and 194 with every load a hit in L2.
 #include <type_traits>
 
 #include "experts.h"
@@ -48,8 +50,8 @@ struct Floats {
     typedef float T __attribute__((ext_vector_type(N)));
 };
 
-// EXACT: y is fp32, otherwise bf16.  BM x BN tile of WM x WN waves; KD blocks a slab.  KG groups of WM x WN waves take a part of
-// K each, and the first adds up the sums.  NS stages.
+// EXACT: y is fp32, otherwise bf16.  BM x BN tile of WM x WN waves; KD blocks a slab.  KG groups of
+// WM x WN waves take a part of K each, and the first adds up the sums.  NS stages.
 template <bool EXACT, int BM, int BN, int WM, int WN, int KD, int KG, int NS, bool GROUPED>
 __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulArgs a) {
     constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;                 // of a group
@@ -560,20 +562,23 @@ hipError_t by_size(const F8MatmulArgs& a, hipStream_t s) {
 // PFLOP/s, but a wave of tiles costs its time whether it fills the chip or not); tiles of 128 x
 // 128 share a unit's LDS by twos.  us, bf16 y, graph replays over 600 MB of weights:
 //                          256 x 256   128 x 128   64 x 64, 2 stages / 4   32 x 64, 3   32 x 32, 4
-//   M = 2048  8192 x 8192     118         153         256 / 413
-//   M = 1024  14336 x 4096     65          80         108 / 187
-//   M =  512  8192 x 8192      97          48          58 /  92
-//   M =  256  8192 x 8192     103          60          43 /  56           91           112
-//   M =  128  8192 x 8192      99          61          34 /  31           49            59
-//   M =   64  8192 x 8192      98          59          34 /  31           27            33
-//   M =   64  4096 x 4096      52          32          18 /  17           16            11
-//   M =   32  8192 x 8192      98          58          32 /  29           27            20
+//   M = 2048  8192 x 8192     126         151         256 / 413
+//   M = 1024  14336 x 4096     62          76         108 / 187
+//   M =  512  8192 x 8192      94          45          58 /  92
+//   M =  256  8192 x 8192      98          48          43 /  56           91           112
+//   M =  128  8192 x 8192      94          48          34 /  27           49            59
+//   M =   64  8192 x 8192      93          44          34 /  31           26            33
+//   M =   64  4096 x 4096      50          24          18 /  17           16            10
+//   M =   32  8192 x 8192      93          43          32 /  29           27            20
 // Where few tiles leave units idle, four groups of a workgroup's waves take a part of K each, and
 // the deeper stages hide the latency that nothing else does.
 // Experts, by the slots an expert has on average (64 experts of 2048 x 4096), 64 x 128 with 3
 // stages / 128 x 128 with 2:
-//   16   123 / 128     32   142 / 153     64   157 / 157     128   204 / 190     256   321 / 255
-// (128 x 256: 202 at 128, 275 at 256; 256 x 256: 204, 262; 64 x 256 with 2: 236, 357.)
+//   16   115 / 121     32   125 / 138     48   128 / 134     64   138 / 137     128   179 / 161
+//   256   274 / 226
+// (Before a list's slots came by LDS, its idle waves rested and its tiles shared W, 128 x 128 took 190
+// at 128 slots and 255 at 256; 128 x 256 then 202 and 275, 256 x 256 204 and 262, 64 x 256 with 2
+// stages 236 and 357.)
 hipError_t launch_f8_gemm(const F8MatmulArgs& a, hipStream_t s) {
     return a.y_dtype == TQ_F32 ? by_size<true>(a, s) : by_size<false>(a, s);
 }

@@ -8,7 +8,10 @@
 //
 // All of them move each byte once and compute a few operations a value: they are bound by
 // memory, or for few rows by the launch.  A lane has eight consecutive values, sixteen
-// lanes a block's 128; its largest magnitude takes four data-parallel moves.
+// lanes a block's 128; its largest magnitude takes four data-parallel moves.  us in a
+// replayed graph, bf16: pack 2048 x 8192 9.4 (5.4 TB/s), 14336 x 4096 by 128 x 128 33.8 (5.2),
+// unpack of it 26.3 (6.7); norm with residual, sum and rows 2048 x 8192 30.8 (4.9), 4096 x 4096
+// 28.4 (5.3), 1 x 4096 2.8.
 #include "f8.h"
 
 namespace dmm {

