@@ -472,6 +472,8 @@ def mx_shape(rows, K):
 
 def _rows(t, name, dtypes, rows, cols, device):
     """Check a [rows, cols] matrix whose rows may lie apart; their distance."""
+    if t is not None and t.dtype in dtypes and t.shape == (rows, cols) and t.is_contiguous() and t.device == device:
+        return cols
     if t is None:
         raise ValueError(f"{name} is required")
     if t.dtype not in dtypes:
