@@ -16,10 +16,10 @@
 //
 // Bound: the vector instructions of the choice, a dozen for each choice and token and forty
 // to sort each lane's experts, beside the logits' bytes; for few tokens the chain of launch, loads
-// and choices.  us in a replayed graph, top 8: 65536 tokens x 128 experts bf16 13.3 (its logits' bytes
-// at a copy's rate take 3.2), fp32 12.6, by sigmoid with a bias 19.7; 32768 x 256 in eight groups
-// 29.2; 16 x 256 in eight groups 4.8.  In float64 throughout: 119 for the first.  The gradient of the
-// first: 8.6, its bytes 6.5.
+// and choices.  us in a replayed graph, top 8: 65536 tokens x 128 experts bf16 11.8 (its logits' bytes
+// at a copy's rate take 3.2), fp32 12.5, by sigmoid with a bias 19.0; 32768 x 256 in eight groups
+// 29.0; 16 x 256 in eight groups 4.8.  In float64 throughout: 119 for the first.  The gradient of the
+// first: 8.5, its bytes 6.5.
 #include "lanes.h"
 
 namespace dmm {
@@ -274,15 +274,20 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(GateArgs a) {
     const bool whole = BF16 && !by_score;       // a key says all
     const float unit = (float)(1u << (32 - kBits - 1)) * (by_score ? 1.f : 0.125f);
     uint32_t k[8];
+    if (whole) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t down = (uint32_t)__builtin_fminf((best - x[i]) * unit, 4294967040.f);
-        uint32_t q = down < kQ ? kQ - down : 1u;
-        if (whole) {
+        for (int i = 0; i < 8; ++i) {
             const uint32_t u = __builtin_bit_cast(uint32_t, x[i] + 0.f);        // one zero
-            q = ((u >> 31) ? ~u : u | 0x80000000u) >> 16;
+            const uint32_t q = (u ^ ((uint32_t)((int)u >> 31) | 0x80000000u)) >> 16;
+            k[i] = x[i] == none ? 0u : q << kBits | (kMask - (uint32_t)(e0 + i));
         }
-        k[i] = x[i] == none ? 0u : q << kBits | (kMask - (uint32_t)(e0 + i));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t down = (uint32_t)__builtin_fminf((best - x[i]) * unit, 4294967040.f);
+            const uint32_t q = down < kQ ? kQ - down : 1u;
+            k[i] = x[i] == none ? 0u : q << kBits | (kMask - (uint32_t)(e0 + i));
+        }
     }
     sort8(k);
     // How far keys of values in the other order can lie apart.  Rounding and truncation keep the
@@ -353,7 +358,13 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(GateArgs a) {
     }
     const bool has = mine != 0u;
     const int id = (int)(kMask - (mine & kMask));
-    float zj = has ? logit(a, t * a.ldl + id) : none;
+    float zj = none;
+    if (whole) {                                // the key has it
+        const uint32_t q = mine >> kBits;
+        zj = __builtin_bit_cast(float, ((q & 0x8000u) ? q ^ 0x8000u : q ^ 0xffffu) << 16);
+    } else if (has) {
+        zj = logit(a, t * a.ldl + id);
+    }
     if (!whole) {
         const uint32_t next = (uint32_t)__shfl_down((int)mine, 1);  // in lane j + 1
         const bool near = next != 0u && (mine >> kBits) - (next >> kBits) <= margin;

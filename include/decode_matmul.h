@@ -745,9 +745,10 @@ int f8_norm_pack(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t l
  * products: they may be off by D = 7 2^-13 sum over each eight columns of the largest
  * |x w| as well (a bf16 y is rounded by up to 2^-9 of itself).  The product of two
  * scales has to be one that fp32 holds (2^-126 to 2^128); one that overflows makes its
- * sums infinite or NaN.  A NaN scale or code makes what it takes part in NaN.  M = 0 or N = 0 is a no-op; with K = 0 the packages may be
- * NULL and y = bias (or 0).  M and N are below 2^31, K is below 2^23; sizes that need
- * more than 2^32 - 1 threads are TQ_ERR_SHAPE.
+ * sums infinite or NaN.  A NaN scale or code makes what it takes part in NaN.  M = 0 or
+ * N = 0 is a no-op; with K = 0 the packages may be NULL and y = bias (or 0).  M and N are
+ * below 2^31, K is below 2^23; sizes that need more than 2^32 - 1 threads are
+ * TQ_ERR_SHAPE.
  */
 int f8_matmul(const uint8_t* x_codes, const float* x_scales, int64_t M, int64_t K, const uint8_t* codes,
               const float* scales, int64_t N, const float* bias, void* y, int32_t y_dtype, void* stream);
