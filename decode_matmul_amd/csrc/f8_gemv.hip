@@ -338,7 +338,7 @@ hipError_t launch_token(const F8MatmulArgs& a, hipStream_t s) {
 // Weights past the caches gain 6 to 8 % of these.
 // Experts, by the slots an expert has on average (64 of 2048 x 4096), streamed by (2, 4) 2 / tiles:
 //   3   68 / -     4   82 / 99     6   108 / 106     8   126 / 108     12   170 / 111
-// (2 on average: 54.7, 5.4 TB/s of the touched experts' packages.)
+// (2 on average: 54.7, 5.2 TB/s of the touched experts' packages.)
 hipError_t launch_f8_matmul(const F8MatmulArgs& a, hipStream_t s) {
     const int64_t tiles = (a.N + 15) / 16, cus = compute_unit_count();
     if (a.n_experts > 0)
