@@ -96,6 +96,17 @@ def test_lists(dmm, M, N, K, E, top_k, out):
     assert np.isnan(got[ids == E]).all()
 
 
+# More tiles of an expert than share W, the last group cut; more experts than a workgroup has threads.
+LONG_LISTS = [(3000, 300, 130, 2, 2), (2100, 140, 640, 1, 1), (1300, 500, 200, 3, 3), (520, 40, 130, 512, 8),
+              (4100, 40, 64, 512, 8)]
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K,E,top_k", LONG_LISTS, ids=["x".join(map(str, f)) for f in LONG_LISTS])
+def test_long_lists(dmm, M, N, K, E, top_k, out):
+    test_lists(dmm, M, N, K, E, top_k, out)
+
+
 def test_second_product_of_the_experts(dmm):
     """Every slot with its own activations: M top_k tokens, top_k 1, the same lists."""
     say("f8_matmul_experts by slots")
