@@ -213,18 +213,20 @@ __device__ __forceinline__ void sort8(uint32_t* k) {
     cx(1, 2), cx(3, 4), cx(5, 6);
 }
 
-// A token by L lanes.  A key is Q - (best - x) S, with x = c or z in fp32, above the index:
+// A token by L lanes, a group of experts by 2^shift of them (without groups: all), whose places
+// l 8 + i are in the experts' order.  A key is Q - (best - x) S, with x = c or z in fp32, above the place:
 // 32 - log2(8 L) bits of fixed point over W below the best.  Keys further down share the
 // least one.  (A bf16 z: its 16 bits, of the same order.)
 template <bool BF16, int L>
-__global__ void __launch_bounds__(kThreads) gate_kernel(GateArgs a) {
-    constexpr int kBits = L == 8 ? 6 : L == 16 ? 7 : L == 32 ? 8 : 9;       // of the index
+__global__ void __launch_bounds__(kThreads) gate_kernel(GateArgs a, int shift) {
+    constexpr int kBits = L == 8 ? 6 : L == 16 ? 7 : L == 32 ? 8 : 9;       // of the place
     constexpr uint32_t kMask = 8 * L - 1, kQ = 0xffffffffu >> kBits;
     __shared__ double lds[kWaves][kMoeMaxExperts];
-    const int lane = (int)threadIdx.x & 63, l = lane % L, E = a.E;
+    const int lane = (int)threadIdx.x & 63, l = lane % L;
     const int64_t t = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / L;
     const bool live = t < a.M && (!a.mask || a.mask[t] != 0);
-    const int e0 = l * 8, have = E - e0;
+    const int size = a.E / a.n_groups, S = 1 << shift, group = l >> shift, in = (l & (S - 1)) * 8;
+    const int e0 = group * size + in, have = group < a.n_groups ? size - in : 0;
     const bool sigmoid = a.score == DMM_SIGMOID, grouped = a.n_groups > 1;
     const bool by_score = a.bias || (grouped && a.group_top > 1);
     const float none = -__builtin_inff();
@@ -279,14 +281,14 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(GateArgs a) {
         for (int i = 0; i < 8; ++i) {
             const uint32_t u = __builtin_bit_cast(uint32_t, x[i] + 0.f);        // one zero
             const uint32_t q = (u ^ ((uint32_t)((int)u >> 31) | 0x80000000u)) >> 16;
-            k[i] = x[i] == none ? 0u : q << kBits | (kMask - (uint32_t)(e0 + i));
+            k[i] = x[i] == none ? 0u : q << kBits | (kMask - (uint32_t)(l * 8 + i));
         }
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint32_t down = (uint32_t)__builtin_fminf((best - x[i]) * unit, 4294967040.f);
             const uint32_t q = down < kQ ? kQ - down : 1u;
-            k[i] = x[i] == none ? 0u : q << kBits | (kMask - (uint32_t)(e0 + i));
+            k[i] = x[i] == none ? 0u : q << kBits | (kMask - (uint32_t)(l * 8 + i));
         }
     }
     sort8(k);
@@ -297,8 +299,7 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(GateArgs a) {
     const uint32_t margin = by_score ? 2u + (uint32_t)(2.f * err * unit) : 0u;
     bool again = live && best != none && !(__builtin_fabsf(best) < __builtin_inff());    // NaN or +inf
     if (grouped) {
-        // a group is S lanes; its score from the keys of its two best
-        const int size = E / a.n_groups, S = size / 8, group = l / S;
+        // a group's score from the keys of its two best
         uint32_t m1 = k[0] >> kBits, m2 = k[1] >> kBits;
         auto merge = [&](uint32_t o1, uint32_t o2) {
             const uint32_t lo = m1 < o1 ? m1 : o1, hi2 = m2 > o2 ? m2 : o2;
@@ -315,7 +316,7 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(GateArgs a) {
         const bool there = group < a.n_groups;
         uint32_t score = !there ? 0u : 1u + (a.group_top > 1 ? m1 + (size > 1 ? m2 : 0u) : m1);
         // fewer experts there than group_top counts (float64's -inf), or one below W
-        again |= !whole && live && there && (m1 == 0u || (a.group_top > 1 && m2 <= 1u));
+        again |= !whole && live && there && (m1 == 0u || (a.group_top > 1 && size > 1 && m2 <= 1u));
         bool kept = false;
         uint32_t last = 0u;
         for (int j = 0; j <= a.top_groups && j < a.n_groups; ++j) {
@@ -357,7 +358,8 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(GateArgs a) {
         for (int j = 0; j <= a.top_k; ++j) round(j, 8);
     }
     const bool has = mine != 0u;
-    const int id = (int)(kMask - (mine & kMask));
+    const int place = (int)(kMask - (mine & kMask)), of = place >> (3 + shift);
+    const int id = of * size + place - (of << (3 + shift));
     float zj = none;
     if (whole) {                                // the key has it
         const uint32_t q = mine >> kBits;
@@ -536,22 +538,27 @@ __global__ void __launch_bounds__(kThreads) gate_grad_kernel(GateGradArgs a) {
 }
 
 template <bool BF16, int L>
-hipError_t gate(const GateArgs& a, hipStream_t s) {
-    const int size = a.E / a.n_groups, S = size / 8;
-    // lanes for one choice more than top_k; groups of whole lanes, a power of two of them
-    const bool fits = a.top_k < L && (a.n_groups == 1 || (size % 8 == 0 && (S & (S - 1)) == 0));
-    if (fits) gate_kernel<BF16, L><<<(unsigned)((a.M * L + kThreads - 1) / kThreads), kThreads, 0, s>>>(a);
-    else gate_exact_kernel<<<(unsigned)((a.M + kWaves - 1) / kWaves), kThreads, 0, s>>>(a);
+hipError_t gate(const GateArgs& a, int shift, hipStream_t s) {
+    gate_kernel<BF16, L><<<(unsigned)((a.M * L + kThreads - 1) / kThreads), kThreads, 0, s>>>(a, shift);
     return hipGetLastError();
 }
 
 template <bool BF16>
 hipError_t gate_by_lanes(const GateArgs& a, hipStream_t s) {
-    switch (row_lanes(a.E)) {
-        case 16: return gate<BF16, 16>(a, s);
-        case 32: return gate<BF16, 32>(a, s);
-        case 64: return gate<BF16, 64>(a, s);
-        default: return gate<BF16, 8>(a, s);
+    // a power of two of lanes for each group; lanes for all of them, and for one choice more than top_k
+    int shift = 0;
+    while ((8 << shift) < a.E / a.n_groups) ++shift;
+    int L = 8;
+    while (L < (a.n_groups << shift) || L <= a.top_k) L *= 2;
+    if (a.n_groups == 1) shift = 6;             // the kernel's l has no more bits
+    switch (L) {
+        case 8: return gate<BF16, 8>(a, shift, s);
+        case 16: return gate<BF16, 16>(a, shift, s);
+        case 32: return gate<BF16, 32>(a, shift, s);
+        case 64: return gate<BF16, 64>(a, shift, s);
+        default:                                // groups that do not fit a wave
+            gate_exact_kernel<<<(unsigned)((a.M + kWaves - 1) / kWaves), kThreads, 0, s>>>(a);
+            return hipGetLastError();
     }
 }
 

@@ -88,6 +88,20 @@ def test_gate(dmm, M, E, top_k, n_groups, top_groups, group_top, biased, score, 
         assert (np.abs(w - rw) <= spread(z, score)[:, None] * np.abs(rw)).all()
 
 
+# More choices than lanes the experts fill; groups of no whole lanes, of one lane, of lanes that do not fit a wave.
+FORMS = [(65, 64, 8, 1, 1, 1), (40, 64, 31, 1, 1, 1), (10, 48, 16, 1, 1, 1), (30, 8, 8, 1, 1, 1), (64, 160, 6, 8, 3, 2),
+         (40, 64, 8, 16, 4, 2), (12, 64, 8, 32, 8, 2), (10, 24, 8, 3, 2, 1), (21, 63, 8, 7, 4, 2), (33, 500, 8, 5, 2, 2),
+         (9, 510, 20, 6, 3, 1), (17, 36, 12, 4, 2, 2)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True], ids=["plain", "biased"])
+@pytest.mark.parametrize("M,E,top_k,n_groups,top_groups,group_top", FORMS, ids=["x".join(map(str, g)) for g in FORMS])
+def test_gate_forms(dmm, M, E, top_k, n_groups, top_groups, group_top, biased, score, dtype):
+    test_gate(dmm, M, E, top_k, n_groups, top_groups, group_top, biased, score, dtype)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("n_groups,group_top", [(1, 1), (4, 2)])
 @pytest.mark.parametrize("E", [16, 64, 128, 256])
