@@ -11,15 +11,16 @@
 // distance from the token's best in fixed point above the index (gate_kernel).  Where two
 // choices next to each other, or the last and the first that is not chosen, lie within the
 // error of that, the wave takes the token again in float64 (choose).  bf16 logits without a
-// bias fit a key as they are.  Sizes that do not fit the lanes take float64 throughout
+// bias fit a key as they are.  Groups that do not fit a wave take float64 throughout
 // (gate_exact_kernel).
 //
 // Bound: the vector instructions of the choice, a dozen for each choice and token and forty
 // to sort each lane's experts, beside the logits' bytes; for few tokens the chain of launch, loads
-// and choices.  us in a replayed graph, top 8: 65536 tokens x 128 experts bf16 11.8 (its logits' bytes
-// at a copy's rate take 3.2), fp32 12.5, by sigmoid with a bias 19.0; 32768 x 256 in eight groups
-// 29.0; 16 x 256 in eight groups 4.8.  In float64 throughout: 119 for the first.  The gradient of the
-// first: 8.5, its bytes 6.5.
+// and choices.  us in a replayed graph, top 8: 65536 tokens x 128 experts bf16 11.9 (its logits' bytes
+// at a copy's rate take 3.2), fp32 12.5, by sigmoid with a bias 19.8 (16.1 without the few dozen
+// tokens that float64 decides, whose waves end last); 64 experts 10.7; 32768 x 256 in eight groups 29.5
+// (21.4); 16 x 256 in eight groups 4.8.  In float64 throughout: 119 for the first, 90 for 64 experts.
+// The gradient of the first: 8.5, its bytes 6.5.
 #include "lanes.h"
 
 namespace dmm {
@@ -216,9 +217,10 @@ __device__ __forceinline__ void sort8(uint32_t* k) {
 // A token by L lanes, a group of experts by 2^shift of them (without groups: all), whose places
 // l 8 + i are in the experts' order.  A key is Q - (best - x) S, with x = c or z in fp32, above the place:
 // 32 - log2(8 L) bits of fixed point over W below the best.  Keys further down share the
-// least one.  (A bf16 z: its 16 bits, of the same order.)
+// least one.  (A bf16 z: its 16 bits, of the same order.)  Eight waves a SIMD, at the price of a few
+// registers that choose spills: 65536 x 128 bf16 12.5 -> 11.9 us, 160 experts in eight groups 28 -> 26.
 template <bool BF16, int L>
-__global__ void __launch_bounds__(kThreads) gate_kernel(GateArgs a, int shift) {
+__global__ void __launch_bounds__(kThreads, 8) gate_kernel(GateArgs a, int shift) {
     constexpr int kBits = L == 8 ? 6 : L == 16 ? 7 : L == 32 ? 8 : 9;       // of the place
     constexpr uint32_t kMask = 8 * L - 1, kQ = 0xffffffffu >> kBits;
     __shared__ double lds[kWaves][kMoeMaxExperts];
