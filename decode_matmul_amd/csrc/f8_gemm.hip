@@ -33,6 +33,7 @@
 
 #include "experts.h"
 #include "f8.h"
+#include "waits.h"
 
 namespace dmm {
 
@@ -61,9 +62,9 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
     constexpr int kXLoads = kXBytes / 1024 / kWaves, kWLoads = kWBytes / 1024 / kWaves;
     constexpr int NB = BN > 128 ? BN / 128 : 1;                             // scales of W along n
     constexpr int kFSlabs = NS, FU = kFSlabs * KD;  // slabs, blocks of a fetch of scales
-    constexpr int kLoads = kXLoads + kWLoads;
     // Two large stages: what the first half of a slab has read is overwritten at its middle
     constexpr bool kEarly = NS == 2 && KD == 1 && KG == 1 && MT >= 4 && !EXACT;
+    constexpr StageQueue kQueue = {NS, kXLoads, kWLoads, kEarly};
     static_assert(NT % 4 == 0 || NT < 4, "kLag");
     static_assert(kXLoads * 1024 * kWaves == kXBytes && kWLoads * 1024 * kWaves == kWBytes, "whole loads");
     static_assert(BM * NB <= kThreads, "a thread for each row's scales");
@@ -332,7 +333,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
             }
         }
         if (next == 0) store_factors(buf1);
-        if (MAIN || t + NS - (kEarly ? 0 : 1) < full) wait_loads<(NS - 2) * kLoads + (kEarly ? kLoads - kXLoads / 2 : 0)>();
+        if (MAIN || t + NS - (kEarly ? 0 : 1) < full) wait_loads<kQueue.slab()>();
         else wait_loads<0>();
         lds_barrier();
         if (MAIN || t + NS < full) start(cur, t + NS, kEarly ? kSecond : kAll);
@@ -358,7 +359,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
 #pragma unroll
         for (int i = 0; i < NS; ++i) start_x(stage[i], i, kAll);
         store_factors(0);
-        wait_loads<(NS - 1) * kXLoads>();
+        wait_loads<kQueue.begin()>();
     } else if (full > 0) {
         fetch_factors(block_of(0), false);
 #pragma unroll
