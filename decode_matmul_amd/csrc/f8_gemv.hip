@@ -15,6 +15,7 @@
 // not passed: 16.3 us, 14.3 without the products, 13.6 without the activations' loads as well,
 // whether a load takes 128 bytes of eight rows or 1024 of one.)
 #include "f8.h"
+#include "waits.h"
 
 namespace dmm {
 
@@ -182,9 +183,9 @@ __global__ void __launch_bounds__(64 * W, 2) f8_gemv_kernel(F8MatmulArgs a) {
                 for (int i = 0; i < NBUF; ++i) {
                     const int c = c0 + i * W;
                     if (c >= c_end) break;
-                    // loads after this block's: of those under way that are there (the first ones all are)
-                    if (c < NBUF * W || c + (NBUF - 1) * W < nb) wait_loads<(NBUF - 1) * kLoads>();
-                    else if (NBUF > 2 && c + W < nb) wait_loads<kLoads>();
+                    const int behind = blocks_behind(c, W, NBUF, nb);
+                    if (behind == NBUF - 1) wait_loads<(NBUF - 1) * kLoads>();
+                    else if (behind == 1) wait_loads<kLoads>();
                     else wait_loads<0>();
                     multiply(bufs[i], c, kept_of(c));
                     if (c + NBUF * W < nb) load(bufs[i], c + NBUF * W);

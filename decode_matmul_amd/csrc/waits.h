@@ -20,4 +20,14 @@ struct StageQueue {
     constexpr int slab() const { return (stages - 2) * (x + w) + (early ? w + x - x / 2 : 0); }
 };
 
+// Streaming: a wave's blocks are c, c + W, ..; the first NBUF were sent for whether they are there (of nb) or
+// not, and block c + NBUF W goes once block c is multiplied.  How many blocks were sent for behind
+// block c when it is waited for.
+constexpr int blocks_behind(int c, int W, int NBUF, int nb) {
+    const int sent = nb > NBUF * W ? nb : NBUF * W;
+    int n = 0;
+    while (n < NBUF - 1 && c + (n + 1) * W < sent) ++n;
+    return n;
+}
+
 }  // namespace dmm

@@ -54,6 +54,20 @@ int play_tile(const dmm::StageQueue& q, int begin, int full, bool scales) {
     return -1;
 }
 
+// Wave `wave` of a streaming workgroup over nb blocks, `loads` a block.  The first block that is read too soon, or -1.
+int play_stream(int nbuf, int W, int loads, int wave, int nb, bool old) {
+    Queue q;
+    for (int i = 0; i < nbuf; ++i) q.send(wave + i * W, 'w', loads);
+    for (int c = wave; c < nb; c += W) {
+        int behind = dmm::blocks_behind(c, W, nbuf, nb);
+        if (old) behind = c < nbuf * W || c + (nbuf - 1) * W < nb ? nbuf - 1 : nbuf > 2 && c + W < nb ? 1 : 0;
+        q.wait(behind * loads);
+        if (!q.here(c)) return c;
+        if (c + nbuf * W < nb) q.send(c + nbuf * W, 'w', loads);
+    }
+    return -1;
+}
+
 }  // namespace
 
 int main() {
@@ -70,6 +84,14 @@ int main() {
                     bad = play_tile(q, begin < 0 ? q.begin() : begin, full, scales != 0);
             if (bad < 0) std::puts("ok");
             else std::printf("slab %d of %d\n", bad, full - 1);
+        } else if (!std::strcmp(kind, "stream")) {
+            int nbuf, W, loads, old;            // old: all first blocks count as sent for behind each of them
+            if (std::scanf("%d %d %d %d", &nbuf, &W, &loads, &old) != 4) return 1;
+            int bad = -1, nb = 0;
+            for (nb = 0; bad < 0 && nb < 8 * nbuf * W; ++nb)
+                for (int wave = 0; bad < 0 && wave < W; ++wave) bad = play_stream(nbuf, W, loads, wave, nb, old != 0);
+            if (bad < 0) std::puts("ok");
+            else std::printf("block %d of %d\n", bad, nb - 1);
         } else {
             return 1;
         }

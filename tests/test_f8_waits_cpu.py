@@ -54,5 +54,26 @@ def test_tiles_that_begin_with_more_under_way(play):
     assert all(g == "ok" or g.startswith("slab 1 ") for g in got)
 
 
+def streams():
+    """(buffers, waves, loads of a block) of every form of f8_gemv.hip."""
+    found = re.findall(r"launch<(\d+), (\d+), (\d+), (\d+), (?:true|false)>\(a, s\)", source("f8_gemv.hip"))
+    return sorted({(nbuf, W, 2 * NT + TB // 8) for TB, NT, W, nbuf in (map(int, f) for f in found)})
+
+
+def test_streams(play):
+    forms = streams()
+    assert {f[0] for f in forms} == {2, 3} and {f[1] for f in forms} == {4, 8}
+    assert play([f"stream {n} {w} {loads} 0" for n, w, loads in forms]) == ["ok"] * len(forms)
+
+
+def test_streams_whose_next_block_is_not_there(play):
+    """The blocks behind the first ones count only where there are any."""
+    forms = streams()
+    got = play([f"stream {n} {w} {loads} 1" for n, w, loads in forms])
+    assert got == [f"block {w} of {w + 1}" for n, w, loads in forms]
+
+
 def test_the_kernels_wait_by_these_counts():
+    assert set(re.findall(r"wait_loads<([^;]*)>\(\)", source("f8_gemv.hip"))) == {"0", "kLoads", "(NBUF - 1) * kLoads"}
+    assert "blocks_behind(c, W, NBUF, nb)" in source("f8_gemv.hip")
     assert set(re.findall(r"wait_loads<([^;]*)>\(\)", source("f8_gemm.hip"))) == {"0", "kQueue.begin()", "kQueue.slab()"}
