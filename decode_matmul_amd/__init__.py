@@ -22,6 +22,7 @@ LIB_PATH = os.path.join(_HERE, "libdecode_matmul.so")
 TQ_OK = 0
 TQ_F32 = 0
 TQ_BF16 = 1
+DMM_SHORT_SUMS = 0x100
 TQ_DATA_RANGE = 1
 TQ_DATA_CODE = 2
 TQ_DATA_PADDING = 4
@@ -717,21 +718,33 @@ def f8_norm_pack(x, weight, codes, scales, eps, residual=None, h_out=None, y_out
     return status
 
 
-def f8_matmul(x_codes, x_scales, M, K, codes, scales, N, y, bias=None):
+def _f8_ydtype(y, short_sums):
+    """The result type of an e4m3 product."""
+    if not short_sums:
+        return _ydtype(y)
+    if y.dtype not in _BF16:
+        raise TypeError(f"short_sums needs a bfloat16 y, not {y.dtype}")
+    return TQ_BF16 | DMM_SHORT_SUMS
+
+
+def f8_matmul(x_codes, x_scales, M, K, codes, scales, N, y, bias=None, short_sums=False):
     """y = x_hat W_hat^T (+ bias) for e4m3 packages of the [M, K] activations
-    (block_rows 1) and the [N, K] weights (block_rows 128)."""
+    (block_rows 1) and the [N, K] weights (block_rows 128).  Sums are fp32; with
+    short_sums (a bfloat16 y) those of many tokens keep 13 bits below the largest of
+    each eight products, at up to twice the rate."""
     dev = x_codes.device
     nb = -(-K // 128)
     _call("f8_matmul", _lib.f8_matmul, dev, _checked(x_codes, "x_codes", _F8, M * nb * 128, dev),
           _checked(x_scales, "x_scales", _F32, M * nb, dev), M, K,
           _checked(codes, "codes", _F8, N * nb * 128, dev),
           _checked(scales, "scales", _F32, -(-N // 128) * nb, dev), N, _maybe(bias, "bias", _F32, N, dev),
-          _checked(y, "y", (y.dtype,), M * N, dev), _ydtype(y))
+          _checked(y, "y", (y.dtype,), M * N, dev), _f8_ydtype(y, short_sums))
 
 
-def f8_matmul_experts(x_codes, x_scales, M, K, codes, scales, N, y, n_experts, offsets, order, top_k, bias=None):
+def f8_matmul_experts(x_codes, x_scales, M, K, codes, scales, N, y, n_experts, offsets, order, top_k, bias=None,
+                      short_sums=False):
     """Grouped f8_matmul: y[t, j] = x_hat[t] W_hat_e^T (+ bias[e]) for the expert
-    e of slot (t, j), with offsets and order from moe_route."""
+    e of slot (t, j), with offsets and order from moe_route; short_sums as there."""
     dev = x_codes.device
     nb = -(-K // 128)
     _call("f8_matmul_experts", _lib.f8_matmul_experts, dev,
@@ -740,7 +753,7 @@ def f8_matmul_experts(x_codes, x_scales, M, K, codes, scales, N, y, n_experts, o
           _checked(scales, "scales", _F32, n_experts * -(-N // 128) * nb, dev), N, n_experts,
           _maybe(bias, "bias", _F32, n_experts * N, dev),
           _checked(offsets, "offsets", _I32, n_experts + 1, dev), _checked(order, "order", _I32, M * top_k, dev),
-          top_k, _checked(y, "y", (y.dtype,), M * top_k * N, dev), _ydtype(y))
+          top_k, _checked(y, "y", (y.dtype,), M * top_k * N, dev), _f8_ydtype(y, short_sums))
 
 
 _SCORES = {"softmax": 0, "sigmoid": 1}

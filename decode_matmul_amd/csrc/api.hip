@@ -520,6 +520,10 @@ int f8_norm_pack(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t l
     return grid_status(dmm::launch_f8_norm_pack(a, s));
 }
 
+// An e4m3 product takes DMM_SHORT_SUMS with TQ_BF16 only; any other type with it is none.
+static bool short_sums(int32_t y_dtype) { return y_dtype == (TQ_BF16 | DMM_SHORT_SUMS); }
+static int32_t plain(int32_t y_dtype) { return short_sums(y_dtype) ? TQ_BF16 : y_dtype; }
+
 static int f8_matmul_common(const dmm::F8MatmulArgs& a, void* stream) {
     if (a.M < 0 || a.K < 0 || a.N < 0 || a.M >= kMaxDim || a.K >= dmm::kF8MaxK || a.N >= kMaxDim) return TQ_ERR_SHAPE;
     if (!is_dtype(a.y_dtype)) return TQ_ERR_DTYPE;
@@ -533,8 +537,8 @@ static int f8_matmul_common(const dmm::F8MatmulArgs& a, void* stream) {
 
 int f8_matmul(const uint8_t* x_codes, const float* x_scales, int64_t M, int64_t K, const uint8_t* codes,
               const float* scales, int64_t N, const float* bias, void* y, int32_t y_dtype, void* stream) {
-    const dmm::F8MatmulArgs a = {x_codes, x_scales, M, K,       N,       codes, scales,
-                                 bias,    0,        nullptr, nullptr, 1,     y,      y_dtype};
+    const dmm::F8MatmulArgs a = {x_codes, x_scales, M,       K, N, codes,           scales,            bias,
+                                 0,       nullptr,  nullptr, 1, y, plain(y_dtype), short_sums(y_dtype)};
     return f8_matmul_common(a, stream);
 }
 
@@ -545,8 +549,8 @@ int f8_matmul_experts(const uint8_t* x_codes, const float* x_scales, int64_t M, 
     if (M >= 0 && M < kMaxDim && M * top_k >= kMaxDim) return TQ_ERR_SHAPE;
     if (M > 0 && N > 0 && (!offsets || !order)) return TQ_ERR_NULL;
     if (!aligned(offsets, 4) || !aligned(order, 4)) return TQ_ERR_ALIGN;
-    const dmm::F8MatmulArgs a = {x_codes, x_scales,  M,       K,     N,     codes, scales,
-                                 bias,    n_experts, offsets, order, top_k, y,     y_dtype};
+    const dmm::F8MatmulArgs a = {x_codes,   x_scales, M,     K,     N, codes,           scales,            bias,
+                                 n_experts, offsets,  order, top_k, y, plain(y_dtype), short_sums(y_dtype)};
     return f8_matmul_common(a, stream);
 }
 

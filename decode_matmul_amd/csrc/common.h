@@ -356,6 +356,7 @@ struct F8MatmulArgs {
     int top_k;                // 1 when dense
     void* y;                  // [M, N] or [M, top_k, N]
     int y_dtype;
+    bool short_sums;          // a bf16 y of many tokens from the e4m3 instructions
 };
 hipError_t launch_f8_matmul(const F8MatmulArgs& a, hipStream_t s);
 hipError_t launch_f8_gemm(const F8MatmulArgs& a, hipStream_t s);       // tiled form for many tokens

@@ -89,6 +89,9 @@ enum tq_data_flag {
 /* Element types of outputs. */
 enum tq_dtype { TQ_F32 = 0, TQ_BF16 = 1 };
 
+/* Joined to TQ_BF16 as the y_dtype of f8_matmul and f8_matmul_experts (see there). */
+enum dmm_sums { DMM_SHORT_SUMS = 0x100 };
+
 /* Scores of moe_gate. */
 enum dmm_score { DMM_SOFTMAX = 0, DMM_SIGMOID = 1 };
 
@@ -737,13 +740,14 @@ int f8_norm_pack(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t l
  *  codes, scales      device package of the [N, K] weights, block_rows = 128.
  *  bias    device fp32 [N] or NULL.
  *  y       device [M, N] of y_dtype (fp32, or bf16 nearest-even of the fp32 result).
+ *  y_dtype  TQ_F32, TQ_BF16, or TQ_BF16 | DMM_SHORT_SUMS.
  *
  * Products of codes are exact; a block's sum, the product of its two scales and the
  * sum over blocks are fp32, in an order fixed by the shape (two calls give the same
- * bits).  For a bf16 y of more than 16 tokens the sums come from the e4m3 matrix
- * instructions, of twice the rate, which keep 13 bits below the largest of each eight
- * products: they may be off by D = 7 2^-13 sum over each eight columns of the largest
- * |x w| as well (a bf16 y is rounded by up to 2^-9 of itself).  The product of two
+ * bits).  With DMM_SHORT_SUMS the block sums of more than 16 tokens come from the e4m3
+ * matrix instructions, of twice the rate, which keep 13 bits below the largest of each
+ * eight products: they may be off by D = 7 2^-13 sum over each eight columns of the
+ * largest |x w| as well (a bf16 y is rounded by up to 2^-9 of itself).  The product of two
  * scales has to be one that fp32 holds (2^-126 to 2^128); one that overflows makes its
  * sums infinite or NaN.  A NaN scale or code makes what it takes part in NaN.  M = 0 or
  * N = 0 is a no-op; with K = 0 the packages may be NULL and y = bias (or 0).  M and N are
@@ -769,7 +773,8 @@ int f8_matmul(const uint8_t* x_codes, const float* x_scales, int64_t M, int64_t 
  * top_k for M and 1 for top_k with the same lists.  Entries of the lists outside their
  * range are skipped (nothing is read or written out of bounds; rows that are then
  * listed nowhere stay as they were).  M * top_k is below 2^31.  Every other argument and
- * error is that of f8_matmul; D is for a bf16 y of 8 slots and more an expert on average.
+ * error is that of f8_matmul; with DMM_SHORT_SUMS, D is for 8 slots and more an expert on
+ * average.
  */
 int f8_matmul_experts(const uint8_t* x_codes, const float* x_scales, int64_t M, int64_t K, const uint8_t* codes,
                       const float* scales, int64_t N, int32_t n_experts, const float* bias, const int32_t* offsets,
