@@ -372,8 +372,9 @@ __global__ void __launch_bounds__(kThreads, 8) gate_kernel(GateArgs a, int shift
     if (!whole) {
         const uint32_t next = (uint32_t)__shfl_down((int)mine, 1);  // in lane j + 1
         const bool near = next != 0u && (mine >> kBits) - (next >> kBits) <= margin;
-        const int any = l < a.top_k && has && (near || (mine >> kBits) == 1u);
-        again |= over_group<L>(any, [](int p, int q) { return p | q; }) != 0;
+        // (again: with groups a lane knows of its own only; the token's lanes agree, so that it is written once)
+        const int any = again || (l < a.top_k && has && (near || (mine >> kBits) == 1u));
+        again = over_group<L>(any, [](int p, int q) { return p | q; }) != 0;
     }
     const bool chosen = has && l < a.top_k;
     if (!chosen) zj = none;
