@@ -298,7 +298,8 @@ __global__ void __launch_bounds__(kThreads, 8) gate_kernel(GateArgs a, int shift
     // order; scores are off by the error of p (sigmoid: 2^-21; softmax: p (d + 32) 2^-23 at a
     // distance d from the best, at most 2^-18 inv), of the sum and of the distance.
     const float err = (sigmoid ? 0x1p-21f : inv * 0x1p-18f) + (__builtin_fabsf(best) + 2.f) * 0x1p-23f;
-    const uint32_t margin = by_score ? 2u + (uint32_t)(2.f * err * unit) : 0u;
+    // (Beyond 2^30, for a bias of 2^28 and more, no two keys are further apart: at most 2^27.)
+    const uint32_t margin = by_score ? 2u + (uint32_t)__builtin_fminf(2.f * err * unit, 0x1p30f) : 0u;
     bool again = live && best != none && !(__builtin_fabsf(best) < __builtin_inff());    // NaN or +inf
     if (grouped) {
         // a group's score from the keys of its two best
