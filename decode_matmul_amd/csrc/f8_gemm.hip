@@ -17,18 +17,24 @@
 // for each of its tokens.  K is cut into slabs of KD blocks, which take turns in NS LDS
 // stages: distinct arrays, so the compiler can tell a load in flight to one from the reads of
 // another.  Rows go from global memory straight to LDS in whole lines of 128 bytes, a block
-// each, NS - 1 slabs ahead; pieces change places within their rows so that a fragment read
-// hits all banks (swizzle).  The products f of NS slabs come by way of registers.
+// each, up to NS - 1 slabs ahead; pieces change places within their rows so that a fragment read
+// hits all banks (swizzle).  The products f of NS slabs come by way of registers.  What may be under way
+// where a slab is waited for stands in waits.h.  (The compiler does not tell the stages of 32 x 64
+// apart: it waits there for everything before it reads W's second fragment, so that the slabs ahead
+// land within the slab that sent for them.)
 //
-// Bound, largest tile (2048 tokens, 8192 x 8192, 113 to 126 us by card, 2.2 to 2.4 PFLOP/s): the LDS, whose reads
+// Bound.  Sums in fp32, 2048 tokens, 8192 x 8192: 217 to 230 us, 1.2 to 1.27 PFLOP/s, the bf16
+// instructions' rate (the vendor's bf16 product of 8192 cubed runs at 1.36 to 1.44: 191 to 202 us).
+// Short sums, largest tile, the same product (107 to 126 us by card, 2.2 to 2.6 PFLOP/s): the LDS, whose reads
 // and writes of a slab take about as long as its matrix instructions.  Without the reads of x's
 // fragments 85 us remain, without the loads 102, without the multiply-adds 102.  What paid:
 // overwriting a slab's first half (W, and half of x) at its middle (with the addresses below,
 // 162 -> 126 us), adding sums four instructions late (121), the middle's barrier ahead of the
 // next read (117).  Eight waves of 64 x 128 need more registers than there are.  Smaller
 // tiles: what a compute unit can have under way against the latency of memory.  Experts' tiles
-// (2048 tokens top 8 of 64, 2048 x 4096: 226 us, where W's bytes take 104 at a copy's rate): 44 us are a
-// tile's beginning and end, 150 remain without loads, and 194 with every load a hit in L2.
+// (2048 tokens top 8 of 64, 2048 x 4096: 319 to 330 us, short sums 224 to 226, where W's bytes take 104 at a
+// copy's rate): of the 226, 44 are a tile's beginning and end, 150 remain without loads, and 194 with
+// every load a hit in L2.
 #include <type_traits>
 
 #include "experts.h"
@@ -114,7 +120,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) f8_gemm_kernel(F8MatmulA
     // Row of tile row i, counted from the tile's first (in a list: the row of x);
     // rows that are not there repeat one that is.
     const int m_rows = (int)(p.m_end - p.m0), n_rows = (int)(a.N - p.n0 < BN ? a.N - p.n0 : BN);
-    // (A list's slots come once, to LDS, while the first rows of W are on their way.)
+    // (A list's slots come once, to LDS, behind the first rows of W, which the compiler waits for with them.)
     __shared__ int32_t list[GROUPED ? BM : 1];
     int32_t entry = 0;
     if (GROUPED && tid < BM) entry = a.order[p.m0 + (tid < m_rows ? tid : m_rows - 1)];
@@ -567,7 +573,7 @@ hipError_t by_size(const F8MatmulArgs& a, hipStream_t s) {
 
 // The largest tile that still gives nearly every compute unit one (its rate is the highest, 2.3
 // PFLOP/s, but a wave of tiles costs its time whether it fills the chip or not); tiles of 128 x
-// 128 share a unit's LDS by twos.  us, bf16 y, graph replays over 600 MB of weights:
+// 128 share a unit's LDS by twos.  us, bf16 y, graph replays over 600 MB of weights, short sums:
 //                          256 x 256   128 x 128   64 x 64, 2 stages / 4   32 x 64, 3   32 x 32, 4
 //   M = 2048  8192 x 8192     126         151         256 / 413
 //   M = 1024  14336 x 4096     62          76         108 / 187
@@ -577,12 +583,25 @@ hipError_t by_size(const F8MatmulArgs& a, hipStream_t s) {
 //   M =   64  8192 x 8192      93          44          34 /  31           26            33
 //   M =   64  4096 x 4096      50          24          18 /  17           16            10
 //   M =   32  8192 x 8192      93          43          32 /  29           27            20
-// Where few tiles leave units idle, four groups of a workgroup's waves take a part of K each, and
-// the deeper stages hide the latency that nothing else does.
+// Sums in fp32 (256 x 256 would need more registers than there are):
+//                          128 x 128   64 x 64, 2 stages / 4   32 x 64, 3   32 x 32, 4
+//   M = 2048  8192 x 8192     224         329 / 464
+//   M = 1024  14336 x 4096    112         146 / 224
+//   M =  512  8192 x 8192      65          86 / 115
+//   M =  256  8192 x 8192      66          48 /  61           93           105
+//   M =  128  8192 x 8192      66          34 /  33           49            56
+//   M =   64  8192 x 8192      65          34 /  32           27            32
+//   M =   64  4096 x 4096      35          19 /  19           15            11
+//   M =   32  8192 x 8192      64          33 /  32           28            20
+// Where few tiles leave units idle, four groups of a workgroup's waves take a part of K each; the
+// four stages of 32 x 32 and of the 64 x 64 tiles that fill the chip once hide latency.
 // Experts, by the slots an expert has on average (64 experts of 2048 x 4096), 64 x 128 with 3
-// stages / 128 x 128 with 2:
+// stages / 128 x 128 with 2, short sums:
 //   16   115 / 121     32   125 / 138     48   128 / 134     64   138 / 137     128   179 / 161
 //   256   274 / 226
+// and sums in fp32:
+//   8   112 / 123      16   116 / 127     32   128 / 150     48   141 / 151     64   158 / 152
+//   128   230 / 209    256   368 / 321
 // (Before a list's slots came by LDS, its idle waves rested and its tiles shared W, 128 x 128 took 190
 // at 128 slots and 255 at 256; 128 x 256 then 202 and 275, 256 x 256 204 and 262, 64 x 256 with 2
 // stages 236 and 357.)

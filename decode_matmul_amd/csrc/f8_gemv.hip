@@ -8,7 +8,9 @@
 // g and 4 + g of a block.
 //
 // Bound: the package's bytes.  A workgroup owns 16 NT rows and its W waves take the blocks in
-// turn, each with NBUF blocks' loads in flight; the waves' sums meet in LDS, in wave order.
+// turn, each with up to NBUF blocks' loads in flight (for passes of 8 tokens the compiler waits for all of
+// them once a round, before it reads the first buffer's fragments of W); the waves' sums meet in
+// LDS, in wave order.
 // Codes go straight to LDS, whole lines of 8 rows a load; pieces change places within their
 // rows so that the 16 rows of a fragment read hit all banks.  The products f of up to
 // kSegBlocks blocks are staged once by the workgroup.  (14336 x 4096, 8 tokens, (1, 8) 2, caches

@@ -19,8 +19,13 @@
 // and choices.  us in a replayed graph, top 8: 65536 tokens x 128 experts bf16 11.9 (its logits' bytes
 // at a copy's rate take 3.2), fp32 12.5, by sigmoid with a bias 19.8 (16.1 without the few dozen
 // tokens that float64 decides, whose waves end last); 64 experts 10.7; 32768 x 256 in eight groups 29.5
-// (21.4); 16 x 256 in eight groups 4.8.  In float64 throughout: 119 for the first, 90 for 64 experts.
-// The gradient of the first: 8.5, its bytes 6.5.
+// (21.4); 16 x 256 in eight groups 4.8.  In float64 throughout: 119 for the first, 90 for 64 experts,
+// 172 for 65536 x 480 in forty groups (73 to 76 in 32, which fit a wave).  The gradient of the first: 8.5,
+// its bytes 6.5; by whole rows 12.3, of fp32 logits 13.3 and 13.8.
+//
+// What float64 decides costs a wave's time each.  fp32 logits without a bias go there where two of the first
+// top_k + 1 are equal or a chosen one lies 16 and more below the best; 65536 x 128 in us: normal logits
+// 13.5, times 8 20, times 16 52, rounded to bf16's values 41, all equal 70 (bf16 logits 11 in all of these).
 #include "lanes.h"
 
 namespace dmm {

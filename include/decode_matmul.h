@@ -815,6 +815,13 @@ int f8_matmul_experts(const uint8_t* x_codes, const float* x_scales, int64_t M, 
  * chosen one) is above 2^-126; smaller ones are within 2^-126 of scale.  +inf and NaN
  * logits of a softmax make its weights NaN where they are chosen (without renorm: all).
  * Sizes that need more than 2^32 - 1 threads are TQ_ERR_SHAPE (M of 2^26 and more).
+ *
+ * Most tokens are decided in fp32.  Those whose order it cannot prove are taken again in
+ * float64, at several times the cost: with a bias or groups by two, tokens whose choices
+ * (or groups) lie closer than fp32's error; with fp32 logits and no bias those with equal
+ * logits among the first top_k + 1, or with a chosen logit 16 and more below the largest.
+ * A batch of fp32 logits that are all equal takes five times as long as one of spread
+ * logits, one of bf16 logits the same time.
  */
 int moe_gate(const void* logits, int32_t l_dtype, int64_t M, int32_t n_experts, int64_t ldl,
              const uint8_t* token_mask, const float* bias, int32_t score, int32_t n_groups, int32_t top_groups,
