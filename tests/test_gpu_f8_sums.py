@@ -160,3 +160,46 @@ def test_short_sums_keep_nan_and_nothing(dmm):
     bad = np.zeros((M, N), bool)
     bad[:, 7], bad[:, 128:], bad[5] = True, True, True
     assert np.array_equal(np.isnan(host(y)), bad)
+
+
+@pytest.mark.parametrize("short_sums", [False, True], ids=["fp32 sums", "short sums"])
+def test_captured_and_on_two_streams(dmm, short_sums):
+    """Products of both kinds captured once and replayed on other inputs, while another stream multiplies
+    too: the bits of an eager pass."""
+    say(f"f8 products captured, short_sums={short_sums}")
+    rng = np.random.default_rng(3)
+    M, N, K, E, top_k = 300, 520, 900, 4, 2
+    cs, ss = dmm.f8_shape(M, K)
+    xc, xs = torch.empty(cs, dtype=torch.uint8, device=DEV), torch.empty(ss, device=DEV)
+    made = [random_package(rng, N, K, 128) for _ in range(E)]
+    wc, ws = dev(np.stack([m[0] for m in made])), dev(np.stack([m[1] for m in made]))
+    _, offsets, order = (dev(v) for v in oracle.moe_route(rng.integers(0, E, (M, top_k)).astype(np.int32), E))
+
+    def products(y, rows):
+        dmm.f8_matmul(xc, xs, M, K, wc[0], ws[0], N, y, short_sums=short_sums)
+        dmm.f8_matmul_experts(xc, xs, M, K, wc, ws, N, rows, E, offsets, order, top_k, short_sums=short_sums)
+
+    def results():
+        return torch.zeros((M, N), dtype=BF16, device=DEV), torch.zeros((M, top_k, N), dtype=BF16, device=DEV)
+
+    captured, eager, beside = results(), results(), results()
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    dmm.f8_pack(torch.randn((M, K), device=DEV), xc, xs)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(one):
+        products(*captured)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=one):
+        products(*captured)
+    for i in range(4):
+        dmm.f8_pack(torch.randn((M, K), device=DEV), xc, xs)
+        products(*eager)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(one):
+            graph.replay()
+        with torch.cuda.stream(two):
+            products(*beside)
+        torch.cuda.synchronize()
+        for got in (captured, beside):
+            assert all(torch.equal(a, b) for a, b in zip(got, eager)), i
